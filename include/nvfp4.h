@@ -63,7 +63,8 @@ typedef enum nvfp4_status {
     NVFP4_ERR_UNSUPPORTED_DEVICE = 5, /* current device is not sm_103        */
     NVFP4_ERR_CUDA = 6,               /* a CUDA runtime call or launch failed */
     NVFP4_ERR_NONFINITE = 7,          /* device: non-finite weight or scale  */
-    NVFP4_ERR_TIMEOUT = 8             /* device: a bounded wait gave up      */
+    NVFP4_ERR_TIMEOUT = 8,            /* device: a bounded wait gave up      */
+    NVFP4_ERR_INDEX = 9               /* device: an index beyond its range   */
 } nvfp4_status;
 
 typedef enum nvfp4_dtype {
@@ -341,6 +342,140 @@ nvfp4_status nvfp4_encode_debug(const float *x, int64_t n, int which, uint8_t *o
  * number of pairs where that quotient differs from IEEE division. */
 nvfp4_status nvfp4_quotient_check(uint32_t sig_lo, uint32_t sig_hi,
                                   unsigned long long *mismatches, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Four-bit activations and distillation: the operators of a quantisation-
+ * aware distillation step (Nemotron NVFP4/QAD page, section 03: a student in
+ * 4 bits trained against a teacher) and of a layer whose activations are in 4
+ * bits as well (W4A4).
+ *
+ * A 4-bit operand is a rows x cols matrix with its blocks along cols (the
+ * axis that a product contracts): E2M1 codes, rows x cols/2 bytes, even
+ * element in the low nibble, and one scale byte per block:
+ *   NVFP4_FORMAT_MXFP4: blocks of 32, E8M0 scales (byte e stands for
+ *     2^(e-127), 255 for NaN);
+ *   NVFP4_FORMAT_NVFP4: blocks of 16, E4M3 scales, one FP32 tensor scale.
+ * cols is a multiple of 32 in the entry points below.
+ * Scales are TILED, the layout the tensor cores copy: tiles of 128 rows x 4
+ * blocks, 512 bytes each, the tiles of 128 rows one after the other along
+ * cols; block j of row r is byte 16 (r % 32) + 4 (r % 128 / 32) + j % 4 of
+ * tile (r / 128, j / 4).  Bytes of rows and blocks that do not exist are 0.
+ */
+typedef enum nvfp4_fp4_format {
+    NVFP4_FORMAT_MXFP4 = 0,
+    NVFP4_FORMAT_NVFP4 = 1
+} nvfp4_fp4_format;
+
+/* Bytes of the tiled scales of a rows x cols operand (0 for invalid sizes;
+ * cols a multiple of the block: 32, or 16 for NVFP4). */
+size_t nvfp4_tiled_scale_bytes(int64_t rows, int64_t cols, nvfp4_fp4_format format);
+
+/* Row-major scale bytes (rows x cols/block, as nvfp4_quantize writes them for
+ * NVFP4 and as checkpoints hold them) -> tiled. */
+nvfp4_status nvfp4_tile_scales(const uint8_t *scales, int64_t rows, int64_t cols, nvfp4_fp4_format format,
+                               uint8_t *tiled, void *stream);
+
+/* MXFP4 quantisation of x (rows x cols, bf16 or FP32, ld elements between
+ * rows), in one read of x:
+ *   codes, scales: blocks along cols (an operand rows x cols);
+ *   codes_t, scales_t: blocks along rows, transposed: an operand cols x
+ *     rows32, rows32 = rows rounded up to 32, the missing rows taken as 0
+ *     (what a product that contracts over the rows needs: a layer's weight
+ *     gradient, and its input gradient for the weight);
+ *   values_bf16, values_t_bf16: rows x cols, x as its codes and scales stand
+ *     for it (exact in bf16), with the blocks along cols and along rows.
+ * Each output may be NULL; codes and scales of a direction go together; at
+ * least one output.  Per block: scale byte max(F - 2, 0), F the FP32 exponent
+ * field of the largest magnitude, i.e. exponent floor(log2 amax) - 2 (the
+ * microscaling formats' rule: magnitudes above 6 scales saturate); code
+ * E2M1_RNE(x / scale) with the sign of x.  A block with an infinity or a NaN
+ * has byte 255 and codes 0: its values are NaN.
+ * rows >= 1, cols a positive multiple of 32, both <= 2^30, ld >= cols; x and
+ * every row of it on 16-byte boundaries (ld a multiple of 8, FP32: 4). */
+nvfp4_status nvfp4_mx_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                               uint8_t *codes, uint8_t *scales, void *values_bf16,
+                               uint8_t *codes_t, uint8_t *scales_t, void *values_t_bf16, void *stream);
+
+/* The values of an MXFP4 operand (tiled scales) as FP32 or bf16, exact:
+ * out is rows x cols. */
+nvfp4_status nvfp4_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
+                                 void *out, nvfp4_dtype out_dtype, void *stream);
+
+/* Y = s_a s_w A W^T from two 4-bit operands of one format (A: M x K, W: N x
+ * K, tiled scales), FP32 accumulation on the block-scaled tensor cores; Y: M x
+ * N, FP32 or bf16 (RNE of the FP32 result).  a_tensor_scale, w_tensor_scale:
+ * one device float each, or NULL for 1.  1 <= M, N <= 2^30, 32 <= K <= 2^30,
+ * K % 32 == 0.  Results do not depend on scheduling.  workspace:
+ * nvfp4_w4a4_workspace_bytes(M, N, K) bytes (0 for sizes it does not take). */
+size_t nvfp4_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nvfp4_status nvfp4_w4a4_gemm(nvfp4_fp4_format format, const uint8_t *a_codes, const uint8_t *a_scales,
+                             const float *a_tensor_scale, const uint8_t *w_codes, const uint8_t *w_scales,
+                             const float *w_tensor_scale, int64_t M, int64_t N, int64_t K, void *y,
+                             nvfp4_dtype y_dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* A layer with 4-bit weights and activations: Y = Q(X) W^T, X: M x K bf16 or
+ * FP32 (ldx elements between rows, as in nvfp4_mx_quantize), Q the MXFP4
+ * quantiser along K, W an MXFP4 operand N x K.  The same Y as
+ * nvfp4_mx_quantize followed by nvfp4_w4a4_gemm, any M >= 1 (one token
+ * upwards).  workspace: nvfp4_mx_linear_workspace_bytes(M, N, K) bytes. */
+size_t nvfp4_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nvfp4_status nvfp4_mx_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, int64_t M, int64_t N, int64_t K,
+                             const uint8_t *w_codes, const uint8_t *w_scales, void *y, nvfp4_dtype y_dtype,
+                             void *workspace, size_t ws_bytes, void *stream);
+
+/* The layer's backward pass with straight-through quantisers, both products
+ * on 4-bit operands quantised along the axis they contract:
+ *     dX = Q(dY) Q_c(W)          (M x K, over N),
+ *     dW = Q_c(dY)^T Q_c(X)      (N x K, over M),
+ * dY: M x N bf16 or FP32 (lddy elements between rows); Q_c(X) and Q_c(W) are
+ * the codes_t, scales_t that nvfp4_mx_quantize wrote for X (K x M32) and W (K
+ * x N).  dx, dw: FP32 or bf16, overwritten; either may be NULL (then its
+ * operand may be NULL too).  M >= 1, N and K multiples of 32.
+ * workspace: nvfp4_mx_linear_backward_workspace_bytes(M, N, K) bytes. */
+size_t nvfp4_mx_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nvfp4_status nvfp4_mx_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int64_t lddy, int64_t M, int64_t N,
+                                      int64_t K, const uint8_t *x_codes_t, const uint8_t *x_scales_t,
+                                      const uint8_t *w_codes_t, const uint8_t *w_scales_t, void *dx,
+                                      nvfp4_dtype dx_dtype, void *dw, nvfp4_dtype dw_dtype, void *workspace,
+                                      size_t ws_bytes, void *stream);
+
+/* Distillation from a teacher's top logits, loss and gradient (Nemotron
+ * NVFP4/QAD page, section 03: KL divergence between the teacher's and the
+ * 4-bit student's output distributions).  Per row t of the student's logits z
+ * (T x V, bf16 or FP32, ldz elements between rows) with q = softmax(z / tau)
+ * and the teacher's k entries (index[t][j], teacher[t][j]):
+ *   rest_class == 0: teacher values are logits, p = softmax_j(teacher / tau);
+ *     loss[t] = w tau^2 sum_j p_j (log p_j - log q_j);
+ *   rest_class != 0: teacher values are log-probabilities at temperature tau,
+ *     p_j = exp(teacher_j); the mass the teacher did not list is one more
+ *     class, p_r = max(0, 1 - sum_j p_j), q_r = the sum of q over the entries
+ *     not listed (no such class when every entry of the vocabulary is listed):
+ *     loss[t] = w tau^2 [sum_j p_j (log p_j - log q_j) + p_r (log p_r - log q_r)].
+ * w = row_weight[t] (NULL: 1).  dz (T x V, z's type, lddz elements between
+ * rows) = grad_loss[t] times the derivative of loss[t]; grad_loss: T floats,
+ * or one for all rows (grad_loss_count 1), or NULL for 1.  dz may be z itself
+ * (with lddz == ldz) and must not overlap it otherwise.  loss or dz may be
+ * NULL; dz alone is the backward pass.
+ *   - A negative index marks an unused slot, whose value is not looked at.
+ *     Used indices of a row are distinct, as a top-k's are.  An index >= V is
+ *     taken as unused and recorded as NVFP4_ERR_INDEX when there is a
+ *     workspace (zero-filled, >= 256 bytes; NULL: not recorded).
+ *   - A teacher value of -inf has p = 0.  A row of weight 0, without a used
+ *     slot, or (rest_class == 0) whose used values are all -inf gives loss 0
+ *     and gradient 0, whatever its logits hold.
+ *   - A student logit of -inf has q = 0: the loss is +inf where the teacher
+ *     gives it mass, the gradient stays finite.  A NaN or +inf among the
+ *     logits, or a row of nothing but -inf, makes the row's loss and gradient
+ *     NaN.
+ * T >= 1; 1 <= V, a row of at most 1638272 bytes; 1 <= k <= 1024; index_bytes
+ * 4 or 8; temperature finite and positive.  z, dz 16-byte aligned as every
+ * pointer; ldz, lddz >= V arbitrary. */
+nvfp4_status nvfp4_distill_topk(const void *z, nvfp4_dtype z_dtype, int64_t T, int64_t V, int64_t ldz,
+                                const void *index, int index_bytes, const void *teacher,
+                                nvfp4_dtype teacher_dtype, int64_t k, float temperature, int rest_class,
+                                const float *row_weight, const float *grad_loss, int64_t grad_loss_count,
+                                float *loss, void *dz, int64_t lddz, void *workspace, size_t ws_bytes,
+                                void *stream);
 
 #ifdef __cplusplus
 }

@@ -19,8 +19,9 @@ _lib = None
 _lock = threading.Lock()
 
 OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_UNSUPPORTED_DEVICE, ERR_CUDA, \
-    ERR_NONFINITE, ERR_TIMEOUT = range(9)
+    ERR_NONFINITE, ERR_TIMEOUT, ERR_INDEX = range(10)
 OUT_BF16, OUT_FP32 = 0, 1
+FORMAT_MXFP4, FORMAT_NVFP4 = 0, 1
 
 EXPORTS = [
     "nvfp4_workspace_bytes", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_w4a16_lora_gemm",
@@ -28,7 +29,9 @@ EXPORTS = [
     "nvfp4_quotient_check", "nvfp4_w4a16_lora_gemm_static", "nvfp4_wait_selftest", "nvfp4_gemm_kernel",
     "nvfp4_scale_qlora_gemm", "nvfp4_w4a16_lora_gemm_dgrad", "nvfp4_dgrad_workspace_bytes",
     "nvfp4_lora_grads", "nvfp4_lora_grads_workspace_bytes", "nvfp4_gemm_list_workspace_bytes",
-    "nvfp4_w4a16_lora_gemm_list",
+    "nvfp4_w4a16_lora_gemm_list", "nvfp4_tiled_scale_bytes", "nvfp4_tile_scales", "nvfp4_mx_quantize",
+    "nvfp4_mx_dequantize", "nvfp4_w4a4_workspace_bytes", "nvfp4_w4a4_gemm", "nvfp4_mx_linear_workspace_bytes",
+    "nvfp4_mx_linear", "nvfp4_mx_linear_backward_workspace_bytes", "nvfp4_mx_linear_backward", "nvfp4_distill_topk",
 ]
 
 
@@ -89,6 +92,21 @@ def load(build_if_missing: bool = True):
             "nvfp4_lora_grads_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i64]),
             "nvfp4_gemm_list_workspace_bytes": (ctypes.c_size_t, [P, ctypes.c_int, i64, i64]),
             "nvfp4_w4a16_lora_gemm_list": (st, [P, ctypes.c_int, i64, i64, ctypes.c_int, P, ctypes.c_size_t, P]),
+            "nvfp4_tiled_scale_bytes": (ctypes.c_size_t, [i64, i64, ctypes.c_int]),
+            "nvfp4_tile_scales": (st, [P, i64, i64, ctypes.c_int, P, P]),
+            "nvfp4_mx_quantize": (st, [P, ctypes.c_int, i64, i64, i64, P, P, P, P, P, P, P]),
+            "nvfp4_mx_dequantize": (st, [P, P, i64, i64, P, ctypes.c_int, P]),
+            "nvfp4_w4a4_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64]),
+            "nvfp4_w4a4_gemm": (st, [ctypes.c_int, P, P, P, P, P, P, i64, i64, i64, P, ctypes.c_int, P,
+                                     ctypes.c_size_t, P]),
+            "nvfp4_mx_linear_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64]),
+            "nvfp4_mx_linear": (st, [P, ctypes.c_int, i64, i64, i64, i64, P, P, P, ctypes.c_int, P, ctypes.c_size_t,
+                                     P]),
+            "nvfp4_mx_linear_backward_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64]),
+            "nvfp4_mx_linear_backward": (st, [P, ctypes.c_int, i64, i64, i64, i64, P, P, P, P, P, ctypes.c_int, P,
+                                              ctypes.c_int, P, ctypes.c_size_t, P]),
+            "nvfp4_distill_topk": (st, [P, ctypes.c_int, i64, i64, i64, P, ctypes.c_int, P, ctypes.c_int, i64,
+                                        ctypes.c_float, ctypes.c_int, P, P, i64, P, P, i64, P, ctypes.c_size_t, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -440,3 +458,234 @@ def gemm(x, q: QuantizedWeight, lora_a=None, lora_b=None, lora_scale=0.0, noise=
     nvfp4_w4a16_lora_gemm(x, q.codes, q.scales, q.tensor_scale, lora_a, lora_b, lora_scale, noise,
                           y, ws)
     return y
+
+
+# ------------------------------------------------------------------ 4-bit activations
+def _out_code(dtype, name):
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return OUT_FP32 if dtype == torch.float32 else OUT_BF16
+
+
+def _matrix(t, name):
+    """Checks a 2-D CUDA matrix whose rows are contiguous; returns its row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def nvfp4_tiled_scale_bytes(rows: int, cols: int, fmt: int) -> int:
+    return int(load().nvfp4_tiled_scale_bytes(rows, cols, int(fmt)))
+
+
+class _Fp4Operand:
+    """A 4-bit operand: codes (rows, cols/2) uint8 with the blocks along cols, and tiled scales (1-D uint8)."""
+
+    format, block = None, None
+
+    def __init__(self, codes, scales, tensor_scale=None):
+        rows, cols = codes.shape[0], codes.shape[1] * 2
+        _need(codes, torch.uint8, (rows, cols // 2), "codes")
+        _need(scales, torch.uint8, (nvfp4_tiled_scale_bytes(rows, cols, self.format),), "scales")
+        if tensor_scale is not None:
+            _need(tensor_scale, torch.float32, (1,), "tensor_scale")
+        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.codes.shape[1] * 2
+
+    @classmethod
+    def from_row_major(cls, codes, scales, *tensor_scale):
+        """From row-major scales (rows, cols/block), as a checkpoint or nvfp4_quantize has them."""
+        rows, cols = codes.shape[0], codes.shape[1] * 2
+        _need(scales, torch.uint8, (rows, cols // cls.block), "scales")
+        tiled = torch.empty(nvfp4_tiled_scale_bytes(rows, cols, cls.format), dtype=torch.uint8, device=codes.device)
+        _check(load().nvfp4_tile_scales(_ptr(scales), rows, cols, cls.format, _ptr(tiled), _stream()),
+               "nvfp4_tile_scales")
+        return cls(codes, tiled, *tensor_scale)
+
+
+class MxOperand(_Fp4Operand):
+    """MXFP4: blocks of 32, E8M0 scales."""
+
+    format, block = FORMAT_MXFP4, 32
+
+    def __init__(self, codes, scales):
+        super().__init__(codes, scales)
+
+    def dequantize(self, dtype=torch.float32):
+        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        _check(load().nvfp4_mx_dequantize(_ptr(self.codes), _ptr(self.scales), *self.shape, _ptr(out),
+                                          _out_code(dtype, "dtype"), _stream()), "nvfp4_mx_dequantize")
+        return out
+
+
+class Nvfp4Operand(_Fp4Operand):
+    """NVFP4: blocks of 16, E4M3 scales, a tensor scale."""
+
+    format, block = FORMAT_NVFP4, 16
+
+    @classmethod
+    def from_weight(cls, q: QuantizedWeight):
+        """The library's NVFP4 weight (or an activation quantised the same way) as an operand; shares its codes."""
+        return cls.from_row_major(q.codes, q.scales, q.tensor_scale)
+
+
+class MxQuantized:
+    """What mx_quantize returns: .row and .col are MxOperands (blocks along the columns, along the rows and
+    transposed), .values and .values_t bf16 matrices of x's shape; each None when it was not asked for."""
+
+    def __init__(self, row, col, values, values_t):
+        self.row, self.col, self.values, self.values_t = row, col, values, values_t
+
+
+def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values=False) -> MxQuantized:
+    """MXFP4 quantisation of x (rows, cols), bf16 or float32, along its columns (rowwise) and/or its rows (colwise).
+    codes: return operands for products; values: return x as the codes stand for it (bf16), e.g. for a
+    straight-through forward."""
+    ld = _matrix(x, "x")
+    dt = _out_code(x.dtype, "x")
+    rows, cols = x.shape
+    dev = x.device
+    u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device=dev)  # noqa: E731
+    bf = lambda want: torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if want else None  # noqa: E731
+    q = qs = qt = qts = None
+    rows32 = (rows + 31) // 32 * 32
+    if codes and rowwise:
+        q, qs = u8(rows, cols // 2), u8(nvfp4_tiled_scale_bytes(rows, cols, FORMAT_MXFP4))
+    if codes and colwise:
+        qt, qts = u8(cols, rows32 // 2), u8(nvfp4_tiled_scale_bytes(cols, rows32, FORMAT_MXFP4))
+    v, vt = bf(values and rowwise), bf(values and colwise)
+    _check(load().nvfp4_mx_quantize(_ptr(x), dt, rows, cols, ld, _ptr(q), _ptr(qs), _ptr(v), _ptr(qt), _ptr(qts),
+                                    _ptr(vt), _stream()), "nvfp4_mx_quantize")
+    return MxQuantized(None if q is None else MxOperand(q, qs), None if qt is None else MxOperand(qt, qts), v, vt)
+
+
+def nvfp4_w4a4_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().nvfp4_w4a4_workspace_bytes(M, N, K))
+
+
+def nvfp4_mx_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().nvfp4_mx_linear_workspace_bytes(M, N, K))
+
+
+def nvfp4_mx_linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().nvfp4_mx_linear_backward_workspace_bytes(M, N, K))
+
+
+def w4a4_gemm(a, w, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
+    """Y (M, N) = A W^T of two operands of one format (MxOperand or Nvfp4Operand)."""
+    if a.format != w.format:
+        raise ValueError("a and w must have the same format")
+    (M, K), (N, Kw) = a.shape, w.shape
+    if K != Kw:
+        raise ValueError(f"a and w must have the same number of columns, got {K} and {Kw}")
+    ydt = _out_code(out_dtype, "out_dtype")
+    y = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
+    ws = workspace if workspace is not None else new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), y.device)
+    _check(load().nvfp4_w4a4_gemm(a.format, _ptr(a.codes), _ptr(a.scales), _ptr(a.tensor_scale), _ptr(w.codes),
+                                  _ptr(w.scales), _ptr(w.tensor_scale), M, N, K, _ptr(y), ydt, _ptr(ws), ws.numel(),
+                                  _stream()), "nvfp4_w4a4_gemm")
+    return y
+
+
+def mx_linear(x: torch.Tensor, w: MxOperand, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
+    """Y (M, N) = Q(X) W^T: x (M, K) bf16 or float32, quantised to MXFP4 on the way."""
+    ld = _matrix(x, "x")
+    dt, ydt = _out_code(x.dtype, "x"), _out_code(out_dtype, "out_dtype")
+    (M, K), (N, Kw) = x.shape, w.shape
+    if not isinstance(w, MxOperand) or K != Kw:
+        raise ValueError("w must be an MxOperand with x's number of columns")
+    y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    ws = workspace if workspace is not None else new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
+    _check(load().nvfp4_mx_linear(_ptr(x), dt, ld, M, N, K, _ptr(w.codes), _ptr(w.scales), _ptr(y), ydt, _ptr(ws),
+                                  ws.numel(), _stream()), "nvfp4_mx_linear")
+    return y
+
+
+def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, dw_dtype=torch.float32,
+                       workspace=None):
+    """(dX (M, K), dW (N, K)) of Y = X W^T with straight-through MXFP4 quantisers.  dy (M, N) bf16 or float32;
+    x_col, w_col: mx_quantize(..., colwise=True).col of X and W; None leaves that operand's gradient partner
+    out (w_col None: no dX; x_col None: no dW)."""
+    ld = _matrix(dy, "dy")
+    dt = _out_code(dy.dtype, "dy")
+    xdt, wdt = _out_code(dx_dtype, "dx_dtype"), _out_code(dw_dtype, "dw_dtype")
+    M, N = dy.shape
+    if x_col is None and w_col is None:
+        raise ValueError("one of x_col and w_col is needed")
+    K = (x_col if x_col is not None else w_col).shape[0]
+    if x_col is not None and (not isinstance(x_col, MxOperand) or x_col.shape != (K, (M + 31) // 32 * 32)):
+        raise ValueError(f"x_col must be an MxOperand of shape {(K, (M + 31) // 32 * 32)}")
+    if w_col is not None and (not isinstance(w_col, MxOperand) or w_col.shape != (K, N)):
+        raise ValueError(f"w_col must be an MxOperand of shape {(K, N)}")
+    dx = torch.empty((M, K), dtype=dx_dtype, device=dy.device) if w_col is not None else None
+    dw = torch.empty((N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
+    ws = workspace if workspace is not None else \
+        new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
+    part = lambda o: (None, None) if o is None else (_ptr(o.codes), _ptr(o.scales))  # noqa: E731
+    _check(load().nvfp4_mx_linear_backward(_ptr(dy), dt, ld, M, N, K, *part(x_col), *part(w_col), _ptr(dx), xdt,
+                                           _ptr(dw), wdt, _ptr(ws), ws.numel(), _stream()),
+           "nvfp4_mx_linear_backward")
+    return dx, dw
+
+
+# ------------------------------------------------------------------ distillation
+def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, loss, dz, workspace):
+    """The C entry point on tensors; loss or dz may be None (see include/nvfp4.h)."""
+    ldz = _matrix(z, "z")
+    zdt, tdt = _out_code(z.dtype, "z"), _out_code(teacher.dtype, "teacher")
+    T, V = z.shape
+    if index.dtype not in (torch.int32, torch.int64) or index.dim() != 2:
+        raise ValueError("index must be a 2-dimensional int32 or int64 tensor")
+    k = index.shape[1]
+    _need(index, index.dtype, (T, k), "index")
+    _need(teacher, teacher.dtype, (T, k), "teacher")
+    if row_weight is not None:
+        _need(row_weight, torch.float32, (T,), "row_weight")
+    if grad_loss is not None:
+        _need(grad_loss, torch.float32, (T,) if grad_loss.numel() != 1 else grad_loss.shape, "grad_loss")
+    if loss is not None:
+        _need(loss, torch.float32, (T,), "loss")
+    lddz = V
+    if dz is not None:
+        lddz = _matrix(dz, "dz")
+        if dz.dtype != z.dtype or dz.shape != z.shape:
+            raise ValueError("dz must have z's type and shape")
+    st = load().nvfp4_distill_topk(_ptr(z), zdt, T, V, ldz, _ptr(index), index.element_size(), _ptr(teacher), tdt, k,
+                                   float(temperature), int(bool(tail)), _ptr(row_weight), _ptr(grad_loss),
+                                   0 if grad_loss is None else grad_loss.numel(), _ptr(loss), _ptr(dz), lddz,
+                                   _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream())
+    _check(st, "nvfp4_distill_topk")
+
+
+def distill_topk_loss(z, index, teacher, temperature=1.0, tail=False, row_weight=None, workspace=None):
+    """Loss per row (T,) float32 of student logits z (T, V) against the teacher's top entries (T, k): index (int32 or
+    int64, negative: unused slot) and teacher (logits, or log-probabilities with tail=True, where the teacher's
+    remaining mass is one more class)."""
+    loss = torch.empty(z.shape[0], dtype=torch.float32, device=z.device)
+    nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, None, loss, None, workspace)
+    return loss
+
+
+def distill_topk_loss_grad(z, index, teacher, temperature=1.0, tail=False, row_weight=None, grad_loss=None,
+                           out=None, workspace=None):
+    """(loss (T,), dz (T, V)) in one pass over z; dz = grad_loss (T values, one, or None for 1) times d loss / d z.
+    out: where dz goes (z itself for an update in place)."""
+    loss = torch.empty(z.shape[0], dtype=torch.float32, device=z.device)
+    dz = out if out is not None else torch.empty(z.shape, dtype=z.dtype, device=z.device)
+    nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, loss, dz, workspace)
+    return loss, dz
+
+
+def distill_topk_grad(z, index, teacher, grad_loss=None, temperature=1.0, tail=False, row_weight=None, out=None,
+                      workspace=None):
+    """dz alone, for a backward pass whose incoming gradient was not known with the loss."""
+    dz = out if out is not None else torch.empty(z.shape, dtype=z.dtype, device=z.device)
+    nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, None, dz, workspace)
+    return dz

@@ -459,6 +459,7 @@ const char *nvfp4_status_string(nvfp4_status s)
     case NVFP4_ERR_CUDA: return "CUDA runtime error";
     case NVFP4_ERR_NONFINITE: return "non-finite weight, tensor scale or scale parameter";
     case NVFP4_ERR_TIMEOUT: return "a bounded device-side wait gave up";
+    case NVFP4_ERR_INDEX: return "an index beyond its range";
     }
     return "unknown status";
 }

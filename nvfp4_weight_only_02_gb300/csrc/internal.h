@@ -106,6 +106,60 @@ cudaError_t encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const
                                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                                  CUtensorMapSwizzle swizzle);
 
+// MXFP4 quantisation of a rows x cols matrix (csrc/mx_quant.cu); each output
+// may be null, codes and scales of a direction go together.
+struct MxQuantArgs {
+    const void *x;
+    bool x_fp32;
+    int64_t rows, cols, ld;
+    uint8_t *codes, *scales;      // blocks along the rows
+    uint16_t *values;             // bf16, rows x cols
+    uint8_t *codes_t, *scales_t;  // blocks along the columns, transposed
+    uint16_t *values_t;           // bf16, rows x cols
+};
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s);
+cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
+                                 bool fp32, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_tile_scales(const uint8_t *in, int64_t rows, int64_t nb, uint8_t *out, cudaStream_t s,
+                               const DeviceInfo &dev);
+
+// Block-scaled product of two 4-bit operands (csrc/gemm_w4a4.cu).
+struct W4A4Args {
+    bool nvfp4;                    // blocks of 16 with E4M3 scales (else 32, E8M0)
+    const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
+    const float *a_ts, *w_ts;      // tensor scales or null (1)
+    int64_t M, N, K;
+    void *y;
+    bool y_fp32;
+    uint32_t *ctl;
+    bool after_quantise;           // launched right behind the quantiser of A on the same stream
+};
+cudaError_t launch_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
+
+// Distillation loss and gradient (csrc/distill.cu).
+constexpr int kDistillMaxK = 1024;             // teacher entries per row
+constexpr int64_t kDistillMaxSlice = 200 * 1024;  // bytes of a row one CTA (of up to 8) holds
+struct DistillArgs {
+    const void *z;
+    bool z_fp32;
+    int64_t T, V, ldz;
+    const void *idx;
+    bool idx64;
+    const void *val;
+    bool val_fp32;
+    int k;
+    float tau, inv_tau;
+    bool tail;
+    const float *weight;      // T or null
+    const float *grad_loss;   // T, 1 or null
+    bool grad_rows;           // grad_loss has T values
+    float *loss;              // T or null
+    void *dz;                 // T x V (leading dimension lddz) or null
+    int64_t lddz;
+    uint32_t *ctl;            // status words or null
+};
+cudaError_t launch_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev);
+
 bool aligned16(const void *p);
 
 // All host-side checks of nvfp4_w4a16_lora_gemm's arguments (pointers, enum

@@ -260,5 +260,55 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int abf)
            ((uint32_t)(M >> 4) << 24);
 }
 
+// ---------------------------------------------------------------- block-scaled MMA
+// Four copies of 32 lanes x 16 bytes (512 contiguous bytes of shared memory,
+// one scale tile) into TMEM columns taddr .. taddr + 3, one copy per warp's
+// lanes.  Ordered with the MMAs of the same thread.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Descriptor of such a tile: no swizzle, 8-row groups of 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(128u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    return d;
+}
+
+// D[tmem] (+)= (A * scale_A)[smem] * (B * scale_B)[smem]^T over 64 elements of
+// K: 4-bit operands, scales of blocks of 32 (E8M0) or 16 (E4M3) in TMEM.
+template <bool kBlock16>
+__device__ __forceinline__ void mma_fp4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
+{
+    if (kBlock16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+            : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: E2M1 x E2M1, both K-major,
+// shape M x N x 64, E8M0 (ue8m0 = 1) or E4M3 scales.  sf: which byte of a
+// 32-bit scale column the first block of this instruction has (0 or 2).
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, int ue8m0, int sf)
+{
+    return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)ue8m0 << 23) |
+           ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf << 29);
+}
+
 }  // namespace sm100
 }  // namespace nvfp4
