@@ -461,21 +461,46 @@ def gemm(x, q: QuantizedWeight, lora_a=None, lora_b=None, lora_scale=0.0, noise=
 
 
 # ------------------------------------------------------------------ 4-bit activations
+# One decode call is a few microseconds on the device, so these wrappers keep
+# the host side short: sizes are computed here, pointers go over as integers.
+_DTYPE_CODE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
+_U8, _F32 = torch.uint8, torch.float32
+
+
 def _out_code(dtype, name):
-    if dtype not in (torch.float32, torch.bfloat16):
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    return OUT_FP32 if dtype == torch.float32 else OUT_BF16
+    return code
+
+
+def _raw_stream():
+    # torch.cuda.current_stream() without building the Stream object
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _call(name, *args):
+    st = getattr(_lib or load(), name)(*args)
+    if st != OK:
+        raise NVFP4Error(st, name)
 
 
 def _matrix(t, name):
-    """Checks a 2-D CUDA matrix whose rows are contiguous; returns its row stride in elements."""
+    """Checks a 2-D CUDA matrix whose rows are contiguous; returns (rows, cols, row stride in elements, type code)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    code = _out_code(t.dtype, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return rows, cols, ld if rows > 1 else cols, code
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def nvfp4_tiled_scale_bytes(rows: int, cols: int, fmt: int) -> int:
@@ -488,25 +513,36 @@ class _Fp4Operand:
     format, block = None, None
 
     def __init__(self, codes, scales, tensor_scale=None):
-        rows, cols = codes.shape[0], codes.shape[1] * 2
-        _need(codes, torch.uint8, (rows, cols // 2), "codes")
-        _need(scales, torch.uint8, (nvfp4_tiled_scale_bytes(rows, cols, self.format),), "scales")
+        if not (codes.is_cuda and scales.is_cuda):
+            raise ValueError("codes and scales must be CUDA tensors")
+        if codes.dtype != _U8 or scales.dtype != _U8:
+            raise ValueError("codes and scales must be torch.uint8")
+        if codes.dim() != 2 or not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes must be a contiguous matrix and scales contiguous")
+        rows, half = codes.shape
+        cols = 2 * half
+        # tiles of 128 rows x 4 blocks, 512 bytes each
+        tiles = (rows + 127) // 128 * ((cols // self.block + 3) // 4)
+        if cols % self.block or rows == 0 or cols == 0 or tuple(scales.shape) != (512 * tiles,):
+            raise ValueError(f"scales must hold {512 * tiles} bytes in one dimension, and codes whole blocks of "
+                             f"{self.block}")
         if tensor_scale is not None:
-            _need(tensor_scale, torch.float32, (1,), "tensor_scale")
+            _need(tensor_scale, _F32, (1,), "tensor_scale")
         self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+        self.rows, self.cols = rows, cols
 
     @property
     def shape(self):
-        return self.codes.shape[0], self.codes.shape[1] * 2
+        return self.rows, self.cols
 
     @classmethod
     def from_row_major(cls, codes, scales, *tensor_scale):
         """From row-major scales (rows, cols/block), as a checkpoint or nvfp4_quantize has them."""
         rows, cols = codes.shape[0], codes.shape[1] * 2
-        _need(scales, torch.uint8, (rows, cols // cls.block), "scales")
-        tiled = torch.empty(nvfp4_tiled_scale_bytes(rows, cols, cls.format), dtype=torch.uint8, device=codes.device)
-        _check(load().nvfp4_tile_scales(_ptr(scales), rows, cols, cls.format, _ptr(tiled), _stream()),
-               "nvfp4_tile_scales")
+        _need(codes, _U8, (rows, cols // 2), "codes")
+        _need(scales, _U8, (rows, cols // cls.block), "scales")
+        tiled = torch.empty(nvfp4_tiled_scale_bytes(rows, cols, cls.format), dtype=_U8, device=codes.device)
+        _call("nvfp4_tile_scales", _addr(scales), rows, cols, cls.format, _addr(tiled), _raw_stream())
         return cls(codes, tiled, *tensor_scale)
 
 
@@ -520,8 +556,8 @@ class MxOperand(_Fp4Operand):
 
     def dequantize(self, dtype=torch.float32):
         out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
-        _check(load().nvfp4_mx_dequantize(_ptr(self.codes), _ptr(self.scales), *self.shape, _ptr(out),
-                                          _out_code(dtype, "dtype"), _stream()), "nvfp4_mx_dequantize")
+        _call("nvfp4_mx_dequantize", _addr(self.codes), _addr(self.scales), self.rows, self.cols, _addr(out),
+              _out_code(dtype, "dtype"), _raw_stream())
         return out
 
 
@@ -540,6 +576,8 @@ class MxQuantized:
     """What mx_quantize returns: .row and .col are MxOperands (blocks along the columns, along the rows and
     transposed), .values and .values_t bf16 matrices of x's shape; each None when it was not asked for."""
 
+    __slots__ = ("row", "col", "values", "values_t")
+
     def __init__(self, row, col, values, values_t):
         self.row, self.col, self.values, self.values_t = row, col, values, values_t
 
@@ -548,21 +586,23 @@ def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values
     """MXFP4 quantisation of x (rows, cols), bf16 or float32, along its columns (rowwise) and/or its rows (colwise).
     codes: return operands for products; values: return x as the codes stand for it (bf16), e.g. for a
     straight-through forward."""
-    ld = _matrix(x, "x")
-    dt = _out_code(x.dtype, "x")
-    rows, cols = x.shape
+    rows, cols, ld, dt = _matrix(x, "x")
     dev = x.device
-    u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device=dev)  # noqa: E731
-    bf = lambda want: torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if want else None  # noqa: E731
-    q = qs = qt = qts = None
-    rows32 = (rows + 31) // 32 * 32
-    if codes and rowwise:
-        q, qs = u8(rows, cols // 2), u8(nvfp4_tiled_scale_bytes(rows, cols, FORMAT_MXFP4))
-    if codes and colwise:
-        qt, qts = u8(cols, rows32 // 2), u8(nvfp4_tiled_scale_bytes(cols, rows32, FORMAT_MXFP4))
-    v, vt = bf(values and rowwise), bf(values and colwise)
-    _check(load().nvfp4_mx_quantize(_ptr(x), dt, rows, cols, ld, _ptr(q), _ptr(qs), _ptr(v), _ptr(qt), _ptr(qts),
-                                    _ptr(vt), _stream()), "nvfp4_mx_quantize")
+    q = qs = qt = qts = v = vt = None
+    if rowwise:
+        if codes:
+            q = torch.empty((rows, cols // 2), dtype=_U8, device=dev)
+            qs = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=_U8, device=dev)
+        if values:
+            v = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    if colwise:
+        if codes:
+            qt = torch.empty((cols, (rows + 31) // 32 * 16), dtype=_U8, device=dev)
+            qts = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=_U8, device=dev)
+        if values:
+            vt = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    _call("nvfp4_mx_quantize", x.data_ptr(), dt, rows, cols, ld, _addr(q), _addr(qs), _addr(v), _addr(qt), _addr(qts),
+          _addr(vt), _raw_stream())
     return MxQuantized(None if q is None else MxOperand(q, qs), None if qt is None else MxOperand(qt, qts), v, vt)
 
 
@@ -582,86 +622,83 @@ def w4a4_gemm(a, w, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
     """Y (M, N) = A W^T of two operands of one format (MxOperand or Nvfp4Operand)."""
     if a.format != w.format:
         raise ValueError("a and w must have the same format")
-    (M, K), (N, Kw) = a.shape, w.shape
-    if K != Kw:
-        raise ValueError(f"a and w must have the same number of columns, got {K} and {Kw}")
+    M, N, K = a.rows, w.rows, a.cols
+    if K != w.cols:
+        raise ValueError(f"a and w must have the same number of columns, got {K} and {w.cols}")
     ydt = _out_code(out_dtype, "out_dtype")
     y = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
     ws = workspace if workspace is not None else new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), y.device)
-    _check(load().nvfp4_w4a4_gemm(a.format, _ptr(a.codes), _ptr(a.scales), _ptr(a.tensor_scale), _ptr(w.codes),
-                                  _ptr(w.scales), _ptr(w.tensor_scale), M, N, K, _ptr(y), ydt, _ptr(ws), ws.numel(),
-                                  _stream()), "nvfp4_w4a4_gemm")
+    _call("nvfp4_w4a4_gemm", a.format, a.codes.data_ptr(), a.scales.data_ptr(), _addr(a.tensor_scale),
+          w.codes.data_ptr(), w.scales.data_ptr(), _addr(w.tensor_scale), M, N, K, y.data_ptr(), ydt, ws.data_ptr(),
+          ws.numel(), _raw_stream())
     return y
 
 
 def mx_linear(x: torch.Tensor, w: MxOperand, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
     """Y (M, N) = Q(X) W^T: x (M, K) bf16 or float32, quantised to MXFP4 on the way."""
-    ld = _matrix(x, "x")
-    dt, ydt = _out_code(x.dtype, "x"), _out_code(out_dtype, "out_dtype")
-    (M, K), (N, Kw) = x.shape, w.shape
-    if not isinstance(w, MxOperand) or K != Kw:
+    M, K, ld, dt = _matrix(x, "x")
+    ydt = _out_code(out_dtype, "out_dtype")
+    if not isinstance(w, MxOperand) or K != w.cols:
         raise ValueError("w must be an MxOperand with x's number of columns")
+    N = w.rows
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     ws = workspace if workspace is not None else new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
-    _check(load().nvfp4_mx_linear(_ptr(x), dt, ld, M, N, K, _ptr(w.codes), _ptr(w.scales), _ptr(y), ydt, _ptr(ws),
-                                  ws.numel(), _stream()), "nvfp4_mx_linear")
+    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(), y.data_ptr(), ydt,
+          ws.data_ptr(), ws.numel(), _raw_stream())
     return y
 
 
 def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, dw_dtype=torch.float32,
                        workspace=None):
     """(dX (M, K), dW (N, K)) of Y = X W^T with straight-through MXFP4 quantisers.  dy (M, N) bf16 or float32;
-    x_col, w_col: mx_quantize(..., colwise=True).col of X and W; None leaves that operand's gradient partner
-    out (w_col None: no dX; x_col None: no dW)."""
-    ld = _matrix(dy, "dy")
-    dt = _out_code(dy.dtype, "dy")
+    x_col, w_col: mx_quantize(..., colwise=True).col of X and W.  w_col None: no dX; x_col None: no dW."""
+    M, N, ld, dt = _matrix(dy, "dy")
     xdt, wdt = _out_code(dx_dtype, "dx_dtype"), _out_code(dw_dtype, "dw_dtype")
-    M, N = dy.shape
     if x_col is None and w_col is None:
         raise ValueError("one of x_col and w_col is needed")
-    K = (x_col if x_col is not None else w_col).shape[0]
-    if x_col is not None and (not isinstance(x_col, MxOperand) or x_col.shape != (K, (M + 31) // 32 * 32)):
-        raise ValueError(f"x_col must be an MxOperand of shape {(K, (M + 31) // 32 * 32)}")
+    K = (x_col if x_col is not None else w_col).rows
+    M32 = (M + 31) // 32 * 32
+    if x_col is not None and (not isinstance(x_col, MxOperand) or x_col.shape != (K, M32)):
+        raise ValueError(f"x_col must be an MxOperand of shape {(K, M32)}")
     if w_col is not None and (not isinstance(w_col, MxOperand) or w_col.shape != (K, N)):
         raise ValueError(f"w_col must be an MxOperand of shape {(K, N)}")
     dx = torch.empty((M, K), dtype=dx_dtype, device=dy.device) if w_col is not None else None
     dw = torch.empty((N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
     ws = workspace if workspace is not None else \
         new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
-    part = lambda o: (None, None) if o is None else (_ptr(o.codes), _ptr(o.scales))  # noqa: E731
-    _check(load().nvfp4_mx_linear_backward(_ptr(dy), dt, ld, M, N, K, *part(x_col), *part(w_col), _ptr(dx), xdt,
-                                           _ptr(dw), wdt, _ptr(ws), ws.numel(), _stream()),
-           "nvfp4_mx_linear_backward")
+    part = lambda o: (None, None) if o is None else (o.codes.data_ptr(), o.scales.data_ptr())  # noqa: E731
+    _call("nvfp4_mx_linear_backward", dy.data_ptr(), dt, ld, M, N, K, *part(x_col), *part(w_col), _addr(dx), xdt,
+          _addr(dw), wdt, ws.data_ptr(), ws.numel(), _raw_stream())
     return dx, dw
 
 
 # ------------------------------------------------------------------ distillation
 def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, loss, dz, workspace):
     """The C entry point on tensors; loss or dz may be None (see include/nvfp4.h)."""
-    ldz = _matrix(z, "z")
-    zdt, tdt = _out_code(z.dtype, "z"), _out_code(teacher.dtype, "teacher")
-    T, V = z.shape
+    T, V, ldz, zdt = _matrix(z, "z")
+    tdt = _out_code(teacher.dtype, "teacher")
     if index.dtype not in (torch.int32, torch.int64) or index.dim() != 2:
         raise ValueError("index must be a 2-dimensional int32 or int64 tensor")
     k = index.shape[1]
     _need(index, index.dtype, (T, k), "index")
     _need(teacher, teacher.dtype, (T, k), "teacher")
     if row_weight is not None:
-        _need(row_weight, torch.float32, (T,), "row_weight")
+        _need(row_weight, _F32, (T,), "row_weight")
+    ng = 0
     if grad_loss is not None:
-        _need(grad_loss, torch.float32, (T,) if grad_loss.numel() != 1 else grad_loss.shape, "grad_loss")
+        ng = grad_loss.numel()
+        _need(grad_loss, _F32, (T,) if ng != 1 else grad_loss.shape, "grad_loss")
     if loss is not None:
-        _need(loss, torch.float32, (T,), "loss")
+        _need(loss, _F32, (T,), "loss")
     lddz = V
     if dz is not None:
-        lddz = _matrix(dz, "dz")
-        if dz.dtype != z.dtype or dz.shape != z.shape:
+        rows, cols, lddz, ddt = _matrix(dz, "dz")
+        if ddt != zdt or rows != T or cols != V:
             raise ValueError("dz must have z's type and shape")
-    st = load().nvfp4_distill_topk(_ptr(z), zdt, T, V, ldz, _ptr(index), index.element_size(), _ptr(teacher), tdt, k,
-                                   float(temperature), int(bool(tail)), _ptr(row_weight), _ptr(grad_loss),
-                                   0 if grad_loss is None else grad_loss.numel(), _ptr(loss), _ptr(dz), lddz,
-                                   _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream())
-    _check(st, "nvfp4_distill_topk")
+    nws = 0 if workspace is None else workspace.numel()
+    _call("nvfp4_distill_topk", z.data_ptr(), zdt, T, V, ldz, index.data_ptr(), index.element_size(),
+          teacher.data_ptr(), tdt, k, temperature, 1 if tail else 0, _addr(row_weight), _addr(grad_loss), ng,
+          _addr(loss), _addr(dz), lddz, _addr(workspace), nws, _raw_stream())
 
 
 def distill_topk_loss(z, index, teacher, temperature=1.0, tail=False, row_weight=None, workspace=None):
