@@ -1035,6 +1035,23 @@ cudaError_t encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const
     return cr == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_scale_map(CUtensorMap *map, const uint8_t *scales, uint64_t ktiles, uint64_t row_tiles,
+                             uint32_t box_k, uint32_t box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    cudaError_t e = get_encoder(&encode);
+    if (e != cudaSuccess)
+        return e;
+    const cuuint64_t gdim[3] = {128, (cuuint64_t)ktiles, (cuuint64_t)row_tiles};
+    const cuuint64_t gstride[2] = {512, (cuuint64_t)ktiles * 512};
+    const cuuint32_t box[3] = {128, box_k, box_rows};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    CUresult cr = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(scales), gdim, gstride, box,
+                         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return cr == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 struct PrefillPlan {
     int ES;
     size_t off_xh, off_pexp, off_flags, off_wh, off_ta, off_tb, off_bt, total;

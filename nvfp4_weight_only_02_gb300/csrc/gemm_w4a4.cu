@@ -289,7 +289,9 @@ cudaError_t run_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
         return run_stream<kNv, 32>(a, s, dev);
     if (a.M <= 64)
         return run_stream<kNv, 64>(a, s, dev);
-    return run_stream<kNv, 128>(a, s, dev);
+    if (a.M <= 128)
+        return run_stream<kNv, 128>(a, s, dev);
+    return launch_w4a4_tile(a, s, dev);
 }
 
 }  // namespace

@@ -1,0 +1,465 @@
+// gemm_w4a4_tile.cu -- the W4A4 product for many tokens: CTA pairs, one
+// 256 x BN output tile per pair at a time.
+//
+// At 4 bits the tensor cores consume operands faster than a single CTA can be
+// fed: a stage of 256 elements of K keeps them busy for about 512 cycles on
+// a 128 x 256 tile, and such a tile would need 48 KB per stage.  The two CTAs
+// of a pair therefore run one MMA (cta_group::2): each holds its 128 rows of A
+// and half of the rows of B (32 KB per stage), and the instruction reads B from
+// both.  The accumulator (128 lanes x BN columns in each CTA) is drained to
+// registers at once when the K loop ends, so that the next tile's MMAs start
+// while this one's rows are converted and stored.
+//
+// Scales: each CTA loads the scale tiles of its own A rows and of all B rows;
+// the leader's copies to TMEM (cta_group::2) work on both CTAs' memory.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace nvfp4 {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kTlEpiWarps = 8;
+constexpr int kTlThreads = 32 * (kTlEpiWarps + 2);  // + copies, MMA
+constexpr int kTlGroup = 8;                          // raster: pairs of row tiles per group
+constexpr int kTlStoreBytes = 4096;                  // a warp's staging for TMA stores: 32 rows x 128 bytes
+
+struct TileParams {
+    const float *a_ts, *w_ts;
+    int M, N;
+    int ksteps;  // stages over K
+    int mpairs, ntiles;
+    void *y;
+    int y_fp32, tma_store;
+    uint32_t *ctl;
+};
+
+template <bool kNv, int BN>
+struct TlShape {
+    static constexpr int kTiles = kNv ? 4 : 2;                 // scale tiles per stage and 128 rows
+    static constexpr int kBRowTiles = BN / 128;
+    static constexpr int kABytes = 128 * 128, kBBytes = BN / 2 * 128;
+    static constexpr int kSaBytes = kTiles * 512, kSbBytes = kBRowTiles * kTiles * 512;
+    static constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
+    static constexpr int kFixed = 1024 + kTlEpiWarps * kTlStoreBytes + 512;
+    static constexpr int kFit = (232448 - kFixed) / kStageBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr size_t kSmem = kFixed + (size_t)kStages * kStageBytes;
+    static constexpr int kSfA = kTiles * 4, kSfB = kTiles * kBRowTiles * 4, kSf = kSfA + kSfB;
+    static constexpr int kTmemCols = 512;
+    static_assert(BN + 2 * kSf <= kTmemCols, "TMEM");
+};
+
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+
+// Loads whose bytes are counted on the pair leader's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_addr(dst)),
+        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5}], [%2];" ::"r"(smem_addr(dst)),
+        "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"((uint64_t)map),
+                 "r"(smem_addr(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <bool kBlock16>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
+{
+    if (kBlock16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+            : "memory");
+}
+
+// One arrival on the barrier at bar's offset in both CTAs when the MMAs (and
+// scale copies) issued so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// 32 lanes x 32 columns without waiting for the data.
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Raster: groups of kTlGroup row-tile pairs, the pair index fastest.
+__device__ __forceinline__ void tile_at(int t, int mpairs, int ntiles, int &mp, int &nt)
+{
+    const int per = kTlGroup * ntiles, g = t / per, i = t % per;
+    const int gm = min(kTlGroup, mpairs - g * kTlGroup);
+    mp = g * kTlGroup + i % gm;
+    nt = i / gm;
+}
+
+template <bool kNv, int BN>
+__global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
+    w4a4_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                     const __grid_constant__ CUtensorMap tm_y, const TileParams p)
+{
+    using S = TlShape<kNv, BN>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sA = smem, *sB = sA + kStages * S::kABytes, *sOut = sB + kStages * S::kBBytes;
+    uint8_t *sSa = sOut + kTlEpiWarps * kTlStoreBytes, *sSb = sSa + kStages * S::kSaBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sSb + kStages * S::kSbBytes);
+    uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 1;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 1);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = (int)cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * kTlEpiWarps);
+        *s_abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kTlEpiWarps + 1)
+        tmem_alloc_pair(s_tmem, S::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers and TMEM before anything of the pair touches them
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+
+    const int cid = (int)cluster_id_x(), ncl = (int)cluster_count_x();
+    const int ntot = p.mpairs * p.ntiles;
+    auto fail = [&]() {
+        record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+        *s_abort = 1;
+    };
+
+    if (warp == kTlEpiWarps) {
+        // ---------------- copies: this CTA's half of each operand
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int t = cid; t < ntot && !*s_abort; t += ncl) {
+                int mp, nt;
+                tile_at(t, p.mpairs, p.ntiles, mp, nt);
+                const int mt = 2 * mp + crank;
+                for (int ks = 0; ks < p.ksteps; ks++, it++) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1)) {
+                        fail();
+                        break;
+                    }
+                    const uint32_t bar = cluster_addr(&full[st], 0);
+                    if (crank == 0)
+                        mbar_arrive_expect_tx(&full[st], 2 * S::kStageBytes);
+                    tma_load_2d_pair(sA + st * S::kABytes, &tm_a, bar, ks * 128, mt * 128);
+                    tma_load_2d_pair(sB + st * S::kBBytes, &tm_b, bar, ks * 128, nt * BN + crank * (BN / 2));
+                    tma_load_3d_pair(sSa + st * S::kSaBytes, &tm_sa, bar, 0, ks * S::kTiles, mt);
+                    tma_load_3d_pair(sSb + st * S::kSbBytes, &tm_sb, bar, 0, ks * S::kTiles, nt * S::kBRowTiles);
+                }
+            }
+            // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
+            for (int k = 0; k < kStages && !*s_abort; k++) {
+                const uint32_t i2 = it + k;
+                if (i2 >= (uint32_t)kStages && !mbar_wait(&empty[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
+                    fail();
+            }
+        }
+    } else if (warp == kTlEpiWarps + 1) {
+        // ---------------- MMA, by the pair's leader
+        if (lane == 0 && crank == 0) {
+            constexpr uint32_t id0 = idesc_fp4(256, BN, kNv ? 0 : 1, 0), id2 = idesc_fp4(256, BN, kNv ? 0 : 1, 2);
+            uint32_t it = 0, lt = 0;
+            for (int t = cid; t < ntot && !*s_abort; t += ncl, lt++) {
+                if (!mbar_wait(acc_empty, (lt & 1) ^ 1)) {
+                    fail();
+                    break;
+                }
+                tc_fence_after();
+                bool ok = true;
+                for (int ks = 0; ks < p.ksteps; ks++, it++) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(&full[st], (it / kStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc_sw128(smem_addr(sA + st * S::kABytes));
+                    const uint64_t bd = smem_desc_sw128(smem_addr(sB + st * S::kBBytes));
+                    const uint64_t sad = smem_desc_scales(smem_addr(sSa + st * S::kSaBytes));
+                    const uint64_t sbd = smem_desc_scales(smem_addr(sSb + st * S::kSbBytes));
+                    const uint32_t sfa = tmem + BN + (it & 1) * S::kSf, sfb = sfa + S::kSfA;
+#pragma unroll
+                    for (int k = 0; k < S::kTiles; k++) {
+                        tmem_cp_scales_pair(sfa + 4 * k, sad + k * 32);
+#pragma unroll
+                        for (int r = 0; r < S::kBRowTiles; r++)
+                            tmem_cp_scales_pair(sfb + 4 * (k * S::kBRowTiles + r), sbd + (r * S::kTiles + k) * 32);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int k = kNv ? j : j / 2;
+                        const uint32_t sa = sfa + 4 * k, sb = sfb + 4 * k * S::kBRowTiles;
+                        mma_fp4_pair<kNv>(tmem, ad + 2 * j, bd + 2 * j, !kNv && (j & 1) ? id2 : id0, sa, sb,
+                                          (ks | j) != 0);
+                    }
+                    mma_commit_pair(&empty[st]);
+                }
+                if (!ok) {
+                    fail();
+                    break;
+                }
+                mma_commit_pair(acc_full);
+            }
+        }
+    } else {
+        // ---------------- epilogue: warp w has lanes 32 (w % 4) .. + 31 and half of the columns
+        constexpr int kCols = BN / 2;
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+        const uint32_t bar = cluster_addr(acc_empty, 0);
+        uint8_t *out = sOut + warp * kTlStoreBytes;
+        const float s_a = p.a_ts ? *p.a_ts : 1.0f, s_w = p.w_ts ? *p.w_ts : 1.0f;
+        uint32_t lt = 0;
+        for (int t = cid; t < ntot && !*s_abort; t += ncl, lt++) {
+            int mp, nt;
+            tile_at(t, p.mpairs, p.ntiles, mp, nt);
+            if (!mbar_wait(acc_full, lt & 1)) {
+                fail();
+                break;
+            }
+            tc_fence_after();
+            uint32_t v[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32)
+                tmem_ld32_nowait(lane_base + c, v + c);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(bar);
+            if (p.a_ts || p.w_ts) {
+                // one after the other: the product of two small tensor scales may underflow
+#pragma unroll
+                for (int c = 0; c < kCols; c++)
+                    v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), s_a), s_w));
+            }
+            const int m0 = (2 * mp + crank) * 128 + quad * 32, n0 = nt * BN + half * kCols;
+            if (m0 >= p.M || n0 >= p.N)
+                continue;
+            if (p.tma_store && p.y_fp32) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    if (lane == 0)
+                        bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; q++)
+                        *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                            make_uint4(v[c + 4 * q], v[c + 4 * q + 1], v[c + 4 * q + 2], v[c + 4 * q + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && n0 + c < p.N) {
+                        tma_store_2d(&tm_y, out, n0 + c, m0);
+                        bulk_commit();
+                    }
+                }
+            } else if (p.tma_store) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 64) {
+                    if (lane == 0)
+                        bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; q++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[c + 8 * q + 2 * e]),
+                                                                           __uint_as_float(v[c + 8 * q + 2 * e + 1]));
+                            w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && n0 + c < p.N) {
+                        tma_store_2d(&tm_y, out, n0 + c, m0);
+                        bulk_commit();
+                    }
+                }
+            } else {
+                // rows of Y that do not start on 16-byte boundaries
+                const int m = m0 + lane;
+                if (m < p.M) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c++) {
+                        if (n0 + c < p.N) {
+                            const size_t at = (size_t)m * p.N + n0 + c;
+                            if (p.y_fp32)
+                                reinterpret_cast<uint32_t *>(p.y)[at] = v[c];
+                            else
+                                reinterpret_cast<__nv_bfloat16 *>(p.y)[at] =
+                                    __float2bfloat16_rn(__uint_as_float(v[c]));
+                        }
+                    }
+                }
+            }
+        }
+        if (lane == 0)
+            bulk_wait_read();
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still signal or read it
+    if (warp == kTlEpiWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, S::kTmemCols);
+    }
+}
+
+template <bool kNv, int BN>
+cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    using S = TlShape<kNv, BN>;
+    const uint64_t row = (uint64_t)a.K / 2;
+    const uint64_t kt = ((uint64_t)a.K + (kNv ? 63 : 127)) / (kNv ? 64 : 128);
+    CUtensorMap ta, tb, tsa, tsb, ty;
+    cudaError_t e = encode_tensor_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a_codes, row, (uint64_t)a.M, row, 128,
+                                         128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = encode_tensor_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, row, (uint64_t)a.N, row, 128, BN / 2,
+                                 CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = encode_scale_map(&tsa, a.a_scales, kt, (uint64_t)(a.M + 127) / 128, S::kTiles, 1);
+    if (e == cudaSuccess)
+        e = encode_scale_map(&tsb, a.w_scales, kt, (uint64_t)(a.N + 127) / 128, S::kTiles, S::kBRowTiles);
+    const int esize = a.y_fp32 ? 4 : 2;
+    const bool tma_store = a.N * esize % 16 == 0;
+    if (e == cudaSuccess)
+        e = tma_store ? encode_tensor_map_2d(&ty, a.y_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                             a.y, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.N * esize, 128 / esize, 32,
+                                             CU_TENSOR_MAP_SWIZZLE_128B)
+                      : (ty = ta, cudaSuccess);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(w4a4_tile_kernel<kNv, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)S::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    TileParams p;
+    p.a_ts = a.a_ts;
+    p.w_ts = a.w_ts;
+    p.M = (int)a.M;
+    p.N = (int)a.N;
+    p.ksteps = (int)((a.K + 255) / 256);
+    p.mpairs = (int)((a.M + 255) / 256);
+    p.ntiles = (int)((a.N + BN - 1) / BN);
+    p.y = a.y;
+    p.y_fp32 = a.y_fp32 ? 1 : 0;
+    p.tma_store = tma_store ? 1 : 0;
+    p.ctl = a.ctl;
+    const int64_t tiles = (int64_t)p.mpairs * p.ntiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, dev.num_sms / 2));
+    cfg.blockDim = dim3(kTlThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.after_quantise ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, w4a4_tile_kernel<kNv, BN>, ta, tb, tsa, tsb, ty, p);
+}
+
+}  // namespace
+
+cudaError_t launch_w4a4_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    return a.nvfp4 ? run_tile<true, 256>(a, s, dev) : run_tile<false, 256>(a, s, dev);
+}
+
+}  // namespace nvfp4

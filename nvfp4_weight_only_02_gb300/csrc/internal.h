@@ -135,6 +135,12 @@ struct W4A4Args {
     bool after_quantise;           // launched right behind the quantiser of A on the same stream
 };
 cudaError_t launch_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
+// Its variant for many tokens (csrc/gemm_w4a4_tile.cu).
+cudaError_t launch_w4a4_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
+// Tiled scales (row_tiles x ktiles tiles of 512 bytes) as a tensor map whose
+// box is box_rows x box_k tiles, in that order in shared memory.
+cudaError_t encode_scale_map(CUtensorMap *map, const uint8_t *scales, uint64_t ktiles, uint64_t row_tiles,
+                             uint32_t box_k, uint32_t box_rows);
 
 // Distillation loss and gradient (csrc/distill.cu).
 constexpr int kDistillMaxK = 1024;             // teacher entries per row
