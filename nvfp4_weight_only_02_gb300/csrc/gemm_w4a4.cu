@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kWsThreads)
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_full + 1);
     float *red = reinterpret_cast<float *>(smem);  // [NT][128], once the ring is drained
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(&full[s], 1);
@@ -105,73 +105,89 @@ __global__ void __launch_bounds__(kWsThreads)
     const int nk = ks1 - ks0;
 
     if (warp == 4) {
-        if (lane == 0) {
-            const uint8_t *wsc = p.w_scales + (size_t)nt * p.ktiles * 512;
-            const uint8_t *xsc = p.a_scales + (size_t)(mt * NT / 128) * p.ktiles * 512;
-            auto scale_bytes = [&](int ks) { return (uint32_t)min(S::kTiles, p.ktiles - ks * S::kTiles) * 512u; };
-            auto load_w = [&](int i, int st) {
-                const int ks = ks0 + i;
-                const uint32_t sb = scale_bytes(ks);
-                mbar_arrive_expect_tx(&full[st], (kWsRows + NT) * 128 + 2 * sb);
-                tma_load_2d(sW + st * kWsRows * 128, &tmap_w, &full[st], ks * 128, nt * kWsRows);
-                bulk_g2s(sWs + st * S::kScaleBytes, wsc + (size_t)ks * S::kScaleBytes, sb, &full[st]);
-            };
-            auto load_x = [&](int i, int st) {
-                const int ks = ks0 + i;
-                tma_load_2d(sX + st * NT * 128, &tmap_a, &full[st], ks * 128, mt * NT);
-                bulk_g2s(sXs + st * S::kScaleBytes, xsc + (size_t)ks * S::kScaleBytes, scale_bytes(ks), &full[st]);
-            };
-            // weights do not depend on the kernel before this one: they start first
-            const int head = min(nk, kStages);
-            for (int i = 0; i < head; i++)
+        const uint8_t *wsc = p.w_scales + (size_t)nt * p.ktiles * 512;
+        const uint8_t *xsc = p.a_scales + (size_t)(mt * NT / 128) * p.ktiles * 512;
+        auto scale_bytes = [&](int ks) { return (uint32_t)min(S::kTiles, p.ktiles - ks * S::kTiles) * 512u; };
+        auto load_w = [&](int i, int st) {
+            const int ks = ks0 + i;
+            const uint32_t sb = scale_bytes(ks);
+            mbar_arrive_expect_tx(&full[st], (kWsRows + NT) * 128 + 2 * sb);
+            tma_load_2d(sW + st * kWsRows * 128, &tmap_w, &full[st], ks * 128, nt * kWsRows);
+            bulk_g2s(sWs + st * S::kScaleBytes, wsc + (size_t)ks * S::kScaleBytes, sb, &full[st]);
+        };
+        auto load_x = [&](int i, int st) {
+            const int ks = ks0 + i;
+            tma_load_2d(sX + st * NT * 128, &tmap_a, &full[st], ks * 128, mt * NT);
+            bulk_g2s(sXs + st * S::kScaleBytes, xsc + (size_t)ks * S::kScaleBytes, scale_bytes(ks), &full[st]);
+        };
+        // weights do not depend on the kernel before this one: they start first
+        const int head = min(nk, kStages);
+        for (int i = 0; i < head; i++) {
+            if (elect_one())
                 load_w(i, i);
-            pdl_wait();
-            for (int i = 0; i < head; i++)
+            __syncwarp();
+        }
+        pdl_wait();
+        for (int i = 0; i < head; i++) {
+            if (elect_one())
                 load_x(i, i);
-            for (int i = head; i < nk; i++) {
-                const int st = i % kStages;
-                if (!mbar_wait(&empty[st], (i / kStages + 1) & 1)) {
-                    record_status(p.ctl, NVFP4_ERR_TIMEOUT);
-                    break;
-                }
+            __syncwarp();
+        }
+        for (int i = head; i < nk; i++) {
+            const int st = i % kStages;
+            if (!mbar_wait_warp(&empty[st], (i / kStages + 1) & 1)) {
+                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                break;
+            }
+            if (elect_one()) {
                 load_w(i, st);
                 load_x(i, st);
             }
+            __syncwarp();
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            constexpr uint32_t id0 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 0);
-            constexpr uint32_t id2 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 2);
-            bool ok = true;
-            for (int i = 0; i < nk; i++) {
-                const int st = i % kStages;
-                if (!mbar_wait(&full[st], (i / kStages) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+        constexpr uint32_t id0 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 0);
+        constexpr uint32_t id2 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 2);
+        for (int i = 0; i < nk; i++) {
+            const int st = i % kStages;
+            // the MMAs that read this half of the scale columns (two stages ago) are done, and this stage's
+            // operands have landed
+            if ((i >= 2 && !mbar_wait_warp(&empty[(i - 2) % kStages], ((i - 2) / kStages) & 1)) ||
+                !mbar_wait_warp(&full[st], (i / kStages) & 1)) {
+                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
                 const uint64_t wd = smem_desc_sw128(smem_addr(sW + st * kWsRows * 128));
                 const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * NT * 128));
+                const uint64_t wsd = smem_desc_scales(smem_addr(sWs + st * S::kScaleBytes));
+                const uint64_t xsd = smem_desc_scales(smem_addr(sXs + st * S::kScaleBytes));
                 const uint32_t sfw = tmem + S::kAccCols + (i & 1) * S::kSfCols, sfx = sfw + S::kTiles * 4;
                 const int tiles = min(S::kTiles, p.ktiles - (ks0 + i) * S::kTiles);
-                for (int t = 0; t < tiles; t++) {
-                    tmem_cp_scales(sfw + 4 * t, smem_desc_scales(smem_addr(sWs + st * S::kScaleBytes + t * 512)));
-                    tmem_cp_scales(sfx + 4 * t, smem_desc_scales(smem_addr(sXs + st * S::kScaleBytes + t * 512)));
-                    if (kNv) {
-                        mma_fp4_ss<true>(tmem, wd + 2 * t, xd + 2 * t, id0, sfw + 4 * t, sfx + 4 * t, (i | t) != 0);
-                    } else {
-                        mma_fp4_ss<false>(tmem, wd + 4 * t, xd + 4 * t, id0, sfw + 4 * t, sfx + 4 * t, (i | t) != 0);
-                        mma_fp4_ss<false>(tmem, wd + 4 * t + 2, xd + 4 * t + 2, id2, sfw + 4 * t, sfx + 4 * t, 1);
+#pragma unroll
+                for (int t = 0; t < S::kTiles; t++) {
+                    if (t < tiles) {
+                        tmem_cp_scales(sfw + 4 * t, wsd + 32 * t);
+                        tmem_cp_scales(sfx + 4 * t, xsd + 32 * t);
                     }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int t = kNv ? j : j / 2;
+                    if (t < tiles)
+                        mma_fp4_ss<kNv>(tmem, wd + 2 * j, xd + 2 * j, !kNv && (j & 1) ? id2 : id0, sfw + 4 * t,
+                                        sfx + 4 * t, (i | j) != 0);
                 }
                 mma_commit(&empty[st]);
             }
-            if (!ok)
-                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
-            mma_commit(acc_full);
+            __syncwarp();
         }
+        if (elect_one())
+            mma_commit(acc_full);
+        __syncwarp();
     } else {
-        if (!mbar_wait(acc_full, 0)) {
+        if (!mbar_wait_warp(acc_full, 0)) {
             if (threadIdx.x == 0)
                 record_status(p.ctl, NVFP4_ERR_TIMEOUT);
         }
@@ -197,7 +213,8 @@ __global__ void __launch_bounds__(kWsThreads)
         constexpr int kChunk = NT < 32 ? NT : 32;
         for (int c = 0; c < NT; c += 32) {
             uint32_t v[32];
-            tmem_ld32(lane_base + c, v);
+            tmem_ld32_start(lane_base + c, v);
+            tmem_ld32_finish(v);
 #pragma unroll
             for (int i = 0; i < kChunk; i++) {
                 if (p.split == 1)

@@ -27,7 +27,7 @@ namespace {
 constexpr int kTlEpiWarps = 8;
 constexpr int kTlThreads = 32 * (kTlEpiWarps + 2);  // + copies, MMA
 constexpr int kTlGroup = 8;                          // raster: pairs of row tiles per group
-constexpr int kTlStoreBytes = 4096;                  // a warp's staging for TMA stores: 32 rows x 128 bytes
+constexpr int kTlStoreBytes = 4096;                  // a warp's staging for TMA stores: 32 x 32 FP32, or bf16 twice
 
 struct TileParams {
     const float *a_ts, *w_ts;
@@ -52,7 +52,11 @@ struct TlShape {
     static constexpr size_t kSmem = kFixed + (size_t)kStages * kStageBytes;
     static constexpr int kSfA = kTiles * 4, kSfB = kTiles * kBRowTiles * 4, kSf = kSfA + kSfB;
     static constexpr int kTmemCols = 512;
-    static_assert(BN + 2 * kSf <= kTmemCols, "TMEM");
+    // columns: accumulator 0 at 0, accumulator 1 at BN - kShared, then two stages' scales
+    static constexpr int kFree = 2 * BN + 2 * kSf - kTmemCols;
+    static constexpr int kShared = kFree > 0 ? (kFree + 31) / 32 * 32 : 0;
+    static constexpr int kAcc1 = BN - kShared, kSfCol = 2 * BN - kShared;
+    static_assert(kSfCol + 2 * kSf <= kTmemCols && kShared >= 64, "TMEM; each half of the epilogue has a shared chunk");
 };
 
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
@@ -89,7 +93,11 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
 }
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
@@ -144,22 +152,6 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
         : "memory");
 }
 
-// 32 lanes x 32 columns without waiting for the data.
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
 // Raster: groups of kTlGroup row-tile pairs, the pair index fastest.
 __device__ __forceinline__ void tile_at(int t, int mpairs, int ntiles, int &mp, int &nt)
 {
@@ -213,21 +205,22 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
         record_status(p.ctl, NVFP4_ERR_TIMEOUT);
         *s_abort = 1;
     };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *s_abort); };
 
     if (warp == kTlEpiWarps) {
         // ---------------- copies: this CTA's half of each operand
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int t = cid; t < ntot && !*s_abort; t += ncl) {
-                int mp, nt;
-                tile_at(t, p.mpairs, p.ntiles, mp, nt);
-                const int mt = 2 * mp + crank;
-                for (int ks = 0; ks < p.ksteps; ks++, it++) {
-                    const int st = it % kStages;
-                    if (!mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1)) {
-                        fail();
-                        break;
-                    }
+        uint32_t it = 0;
+        for (int t = cid; t < ntot && !aborted(); t += ncl) {
+            int mp, nt;
+            tile_at(t, p.mpairs, p.ntiles, mp, nt);
+            const int mt = 2 * mp + crank;
+            for (int ks = 0; ks < p.ksteps; ks++, it++) {
+                const int st = it % kStages;
+                if (!mbar_wait_warp(&empty[st], ((it / kStages) & 1) ^ 1)) {
+                    fail();
+                    break;
+                }
+                if (elect_one()) {
                     const uint32_t bar = cluster_addr(&full[st], 0);
                     if (crank == 0)
                         mbar_arrive_expect_tx(&full[st], 2 * S::kStageBytes);
@@ -236,150 +229,162 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                     tma_load_3d_pair(sSa + st * S::kSaBytes, &tm_sa, bar, 0, ks * S::kTiles, mt);
                     tma_load_3d_pair(sSb + st * S::kSbBytes, &tm_sb, bar, 0, ks * S::kTiles, nt * S::kBRowTiles);
                 }
+                __syncwarp();
             }
-            // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
-            for (int k = 0; k < kStages && !*s_abort; k++) {
-                const uint32_t i2 = it + k;
-                if (i2 >= (uint32_t)kStages && !mbar_wait(&empty[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
-                    fail();
-            }
+        }
+        // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
+        for (int k = 0; k < kStages && !aborted(); k++) {
+            const uint32_t i2 = it + k;
+            if (i2 >= (uint32_t)kStages && !mbar_wait_warp(&empty[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
+                fail();
         }
     } else if (warp == kTlEpiWarps + 1) {
         // ---------------- MMA, by the pair's leader
-        if (lane == 0 && crank == 0) {
+        if (crank == 0) {
             constexpr uint32_t id0 = idesc_fp4(256, BN, kNv ? 0 : 1, 0), id2 = idesc_fp4(256, BN, kNv ? 0 : 1, 2);
             uint32_t it = 0, lt = 0;
-            for (int t = cid; t < ntot && !*s_abort; t += ncl, lt++) {
-                if (!mbar_wait(acc_empty, (lt & 1) ^ 1)) {
+            for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
+                // the shared columns of the accumulator before this one have been read
+                if (lt > 0 && !mbar_wait_warp(acc_empty, (lt - 1) & 1)) {
                     fail();
                     break;
                 }
                 tc_fence_after();
+                const uint32_t acc = tmem + (lt & 1 ? S::kAcc1 : 0);
                 bool ok = true;
                 for (int ks = 0; ks < p.ksteps; ks++, it++) {
                     const int st = it % kStages;
-                    if (!mbar_wait(&full[st], (it / kStages) & 1)) {
+                    // the MMAs that read this half of the scale columns (two stages ago) are done, and this
+                    // stage's operands have landed
+                    if ((it >= 2 && !mbar_wait_warp(&empty[(it - 2) % kStages], ((it - 2) / kStages) & 1)) ||
+                        !mbar_wait_warp(&full[st], (it / kStages) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = smem_desc_sw128(smem_addr(sA + st * S::kABytes));
-                    const uint64_t bd = smem_desc_sw128(smem_addr(sB + st * S::kBBytes));
-                    const uint64_t sad = smem_desc_scales(smem_addr(sSa + st * S::kSaBytes));
-                    const uint64_t sbd = smem_desc_scales(smem_addr(sSb + st * S::kSbBytes));
-                    const uint32_t sfa = tmem + BN + (it & 1) * S::kSf, sfb = sfa + S::kSfA;
+                    if (elect_one()) {
+                        const uint64_t ad = smem_desc_sw128(smem_addr(sA + st * S::kABytes));
+                        const uint64_t bd = smem_desc_sw128(smem_addr(sB + st * S::kBBytes));
+                        const uint64_t sad = smem_desc_scales(smem_addr(sSa + st * S::kSaBytes));
+                        const uint64_t sbd = smem_desc_scales(smem_addr(sSb + st * S::kSbBytes));
+                        const uint32_t sfa = tmem + S::kSfCol + (it & 1) * S::kSf, sfb = sfa + S::kSfA;
 #pragma unroll
-                    for (int k = 0; k < S::kTiles; k++) {
-                        tmem_cp_scales_pair(sfa + 4 * k, sad + k * 32);
+                        for (int k = 0; k < S::kTiles; k++) {
+                            tmem_cp_scales_pair(sfa + 4 * k, sad + k * 32);
 #pragma unroll
-                        for (int r = 0; r < S::kBRowTiles; r++)
-                            tmem_cp_scales_pair(sfb + 4 * (k * S::kBRowTiles + r), sbd + (r * S::kTiles + k) * 32);
+                            for (int r = 0; r < S::kBRowTiles; r++)
+                                tmem_cp_scales_pair(sfb + 4 * (k * S::kBRowTiles + r),
+                                                    sbd + (r * S::kTiles + k) * 32);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const int k = kNv ? j : j / 2;
+                            const uint32_t sa = sfa + 4 * k, sb = sfb + 4 * k * S::kBRowTiles;
+                            mma_fp4_pair<kNv>(acc, ad + 2 * j, bd + 2 * j, !kNv && (j & 1) ? id2 : id0, sa, sb,
+                                              (ks | j) != 0);
+                        }
+                        mma_commit_pair(&empty[st]);
+                        if (ks + 1 == p.ksteps)
+                            mma_commit_pair(acc_full);
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int k = kNv ? j : j / 2;
-                        const uint32_t sa = sfa + 4 * k, sb = sfb + 4 * k * S::kBRowTiles;
-                        mma_fp4_pair<kNv>(tmem, ad + 2 * j, bd + 2 * j, !kNv && (j & 1) ? id2 : id0, sa, sb,
-                                          (ks | j) != 0);
-                    }
-                    mma_commit_pair(&empty[st]);
+                    __syncwarp();
                 }
                 if (!ok) {
                     fail();
                     break;
                 }
-                mma_commit_pair(acc_full);
             }
         }
     } else {
-        // ---------------- epilogue: warp w has lanes 32 (w % 4) .. + 31 and half of the columns
-        constexpr int kCols = BN / 2;
+        // ---------------- epilogue: warp w has lanes 32 (w % 4) .. + 31 and every other 32 columns, the columns
+        // that both accumulators use first
+        constexpr int kChunks = BN / 32, kSharedChunks = S::kShared / 32;
         const int quad = warp & 3, half = warp >> 2;
-        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
         const uint32_t bar = cluster_addr(acc_empty, 0);
         uint8_t *out = sOut + warp * kTlStoreBytes;
         const float s_a = p.a_ts ? *p.a_ts : 1.0f, s_w = p.w_ts ? *p.w_ts : 1.0f;
+        const bool scaled = p.a_ts || p.w_ts;
         uint32_t lt = 0;
-        for (int t = cid; t < ntot && !*s_abort; t += ncl, lt++) {
+        for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
             int mp, nt;
             tile_at(t, p.mpairs, p.ntiles, mp, nt);
-            if (!mbar_wait(acc_full, lt & 1)) {
+            if (!mbar_wait_warp(acc_full, lt & 1)) {
                 fail();
                 break;
             }
             tc_fence_after();
-            uint32_t v[kCols];
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (lt & 1 ? S::kAcc1 : 0);
+            const int m0 = (2 * mp + crank) * 128 + quad * 32;
+            // accumulator 0 ends with the shared columns, accumulator 1 begins with them
+            const int first = lt & 1 ? 0 : kChunks - kSharedChunks;
+            uint32_t buf[2][32];
+            tmem_ld32_start(acc + (first + half) % kChunks * 32, buf[0]);
 #pragma unroll
-            for (int c = 0; c < kCols; c += 32)
-                tmem_ld32_nowait(lane_base + c, v + c);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(bar);
-            if (p.a_ts || p.w_ts) {
-                // one after the other: the product of two small tensor scales may underflow
-#pragma unroll
-                for (int c = 0; c < kCols; c++)
-                    v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), s_a), s_w));
-            }
-            const int m0 = (2 * mp + crank) * 128 + quad * 32, n0 = nt * BN + half * kCols;
-            if (m0 >= p.M || n0 >= p.N)
-                continue;
-            if (p.tma_store && p.y_fp32) {
-#pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
+            for (int i = 0; i < kChunks / 2; i++) {
+                uint32_t(&v)[32] = buf[i & 1];
+                tmem_ld32_finish(v);
+                if (i + 1 < kChunks / 2)
+                    tmem_ld32_start(acc + (first + half + 2 * (i + 1)) % kChunks * 32, buf[(i + 1) & 1]);
+                if (half + 2 * i < kSharedChunks && half + 2 * i + 2 >= kSharedChunks) {
+                    // this warp's part of the shared columns is in registers
+                    tc_fence_before();
+                    __syncwarp();
                     if (lane == 0)
-                        bulk_wait_read();
-                    __syncwarp();
-#pragma unroll
-                    for (int q = 0; q < 8; q++)
-                        *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                            make_uint4(v[c + 4 * q], v[c + 4 * q + 1], v[c + 4 * q + 2], v[c + 4 * q + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && n0 + c < p.N) {
-                        tma_store_2d(&tm_y, out, n0 + c, m0);
-                        bulk_commit();
-                    }
+                        mbar_arrive_cluster(bar);
                 }
-            } else if (p.tma_store) {
+                const int n0 = nt * BN + (first + half + 2 * i) % kChunks * 32;
+                if (m0 >= p.M || n0 >= p.N)
+                    continue;
+                if (scaled) {
+                    // one after the other: the product of two small tensor scales may underflow
 #pragma unroll
-                for (int c = 0; c < kCols; c += 64) {
-                    if (lane == 0)
-                        bulk_wait_read();
-                    __syncwarp();
+                    for (int c = 0; c < 32; c++)
+                        v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), s_a), s_w));
+                }
+                if (p.tma_store) {
+                    uint8_t *at = out;
+                    if (p.y_fp32) {
+                        if (lane == 0)
+                            bulk_wait_read<0>();
+                        __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 8; q++) {
-                        uint32_t w[4];
+                        for (int q = 0; q < 8; q++)
+                            *reinterpret_cast<uint4 *>(at + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                                make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    } else {
+                        at += (i & 1) * (kTlStoreBytes / 2);
+                        if (lane == 0)
+                            bulk_wait_read<1>();
+                        __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[c + 8 * q + 2 * e]),
-                                                                           __uint_as_float(v[c + 8 * q + 2 * e + 1]));
-                            w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        for (int q = 0; q < 4; q++) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(
+                                    __uint_as_float(v[8 * q + 2 * e]), __uint_as_float(v[8 * q + 2 * e + 1]));
+                                w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            *reinterpret_cast<uint4 *>(at + lane * 64 + ((q ^ (lane >> 1 & 3)) * 16)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        *reinterpret_cast<uint4 *>(out + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && n0 + c < p.N) {
-                        tma_store_2d(&tm_y, out, n0 + c, m0);
+                    if (lane == 0) {
+                        tma_store_2d(&tm_y, at, n0, m0);
                         bulk_commit();
                     }
-                }
-            } else {
-                // rows of Y that do not start on 16-byte boundaries
-                const int m = m0 + lane;
-                if (m < p.M) {
+                } else if (m0 + lane < p.M) {
+                    // rows of Y that do not start on 16-byte boundaries
+                    const size_t at = (size_t)(m0 + lane) * p.N + n0;
 #pragma unroll
-                    for (int c = 0; c < kCols; c++) {
+                    for (int c = 0; c < 32; c++) {
                         if (n0 + c < p.N) {
-                            const size_t at = (size_t)m * p.N + n0 + c;
                             if (p.y_fp32)
-                                reinterpret_cast<uint32_t *>(p.y)[at] = v[c];
+                                reinterpret_cast<uint32_t *>(p.y)[at + c] = v[c];
                             else
-                                reinterpret_cast<__nv_bfloat16 *>(p.y)[at] =
+                                reinterpret_cast<__nv_bfloat16 *>(p.y)[at + c] =
                                     __float2bfloat16_rn(__uint_as_float(v[c]));
                         }
                     }
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
         if (lane == 0)
-            bulk_wait_read();
+            bulk_wait_read<0>();
     }
 
     __syncwarp();
@@ -421,8 +426,8 @@ cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
     if (e == cudaSuccess)
         e = tma_store ? encode_tensor_map_2d(&ty, a.y_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                             a.y, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.N * esize, 128 / esize, 32,
-                                             CU_TENSOR_MAP_SWIZZLE_128B)
+                                             a.y, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.N * esize, 32, 32,
+                                             a.y_fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)
                       : (ty = ta, cudaSuccess);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(w4a4_tile_kernel<kNv, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
