@@ -99,9 +99,13 @@ __device__ __forceinline__ void bulk_wait_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// Arrival on a barrier of the pair.  What it hands over is TMEM that has been
+// read (tcgen05.wait::ld), so a release of this thread's memory operations at
+// cluster scope is not needed; it would wait for the stores in flight (1500
+// cycles between two tiles).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols)
