@@ -21,6 +21,9 @@
 // after their logits have been fetched), never as 1 - sum: with a confident
 // student the difference would have no correct digit.  All statistics are
 // FP32; sums have a fixed order, so results do not depend on scheduling.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -32,8 +35,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kDsThreads = 256, kDsWarps = kDsThreads / 32;
-constexpr int kDsEntries = kDistillMaxK / kDsThreads;  // teacher entries a thread holds
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // 2^x; results below 2^-126 are flushed to 0, which a sum of values in (0, 1]
 // whose largest is 1 cannot notice.
@@ -44,32 +46,66 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// log2 of a sum (error below 2^-22; of 0: -inf).
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 
-// Running maximum m of logits and sum s of 2^((z - m) k2), k2 = log2(e) / tau.
-// The difference is taken before the scaling: a row whose logits are all the
-// type's lowest value is uniform, not a row of infinities.
+// A maximum m of logits and the sum s of 2^((z - m) k2), k2 = log2(e) / tau.
+// The difference is taken before the scaling where z is so large that z k2
+// may leave FP32's range: a row whose logits are all the type's lowest value is
+// uniform, not a row of infinities.
 struct MaxSum {
     float m, s;
 };
 
 __device__ __forceinline__ float finite_or_zero(float m) { return m == neg_inf() ? 0.0f : m; }
 
+// s of a MaxSum with its maximum moved to m (which is not below v.m)
+__device__ __forceinline__ float sum_at(MaxSum v, float m, float k2) { return v.s * ex2((v.m - finite_or_zero(m)) * k2); }
+
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k2)
 {
-    const float m = fmaxf(a.m, b.m), base = finite_or_zero(m);
-    return {m, a.s * ex2((a.m - base) * k2) + b.s * ex2((b.m - base) * k2)};
+    const float m = fmaxf(a.m, b.m);
+    return {m, sum_at(a, m, k2) + sum_at(b, m, k2)};
 }
 
-__device__ __forceinline__ MaxSum warp_merge(MaxSum v, float k2)
+__device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        MaxSum u;
-        u.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-        u.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-        v = merge(v, u, k2);
-    }
+    for (int o = 16; o >= 1; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
@@ -81,18 +117,17 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Every thread gets the block's merged value (the warps' in order).
-__device__ __forceinline__ MaxSum block_merge(MaxSum v, float k2, MaxSum *s_w, int warp, int lane)
+// One value per warp -> all of them to every thread, combined in warp order.
+__device__ __forceinline__ float over_warps_max(const float4 *s_w)
 {
-    v = warp_merge(v, k2);
-    if (lane == 0)
-        s_w[warp] = v;
-    __syncthreads();
-    MaxSum r = s_w[0];
-#pragma unroll
-    for (int i = 1; i < kDsWarps; i++)
-        r = merge(r, s_w[i], k2);
-    return r;
+    const float4 a = s_w[0], b = s_w[1];
+    return fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+}
+
+__device__ __forceinline__ float over_warps_sum(const float4 *s_w)
+{
+    const float4 a = s_w[0], b = s_w[1];
+    return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
 }
 
 __device__ __forceinline__ void st_cluster_f4(uint32_t local, uint32_t rank, float4 v)
@@ -158,18 +193,173 @@ struct Vec<float> {
     static __device__ __forceinline__ float put(float v) { return v; }
 };
 
+// Logits below this magnitude stay finite when multiplied by k2.
+__device__ __forceinline__ float limit_for(float k2) { return 0x1p120f / (k2 > 1.0f ? k2 : 1.0f); }
+
+// A thread's sum over 16 bytes of logits at a time: one fused operation and one
+// exponential per element.  Any element's value m will do as the reference of
+// the sum, since FP32 keeps its relative precision far above and below 1: the
+// first finite vector gives it, and a sum that grows past 2^60 moves it up.  So
+// no maximum is formed element by element.  A sum that overflowed in one step,
+// or a reference outside (-limit, limit), sends the row to scan_any (no
+// ordinary row goes there).
+struct Running {
+    float m;           // reference; -limit: none yet
+    uint64_t nb2, s2;  // minus the reference times k2, twice; two sums of 2^(z k2 - m k2)
+
+    __device__ __forceinline__ Running(float limit, float k2) : m(-limit), nb2(pair2(limit * k2, limit * k2)), s2(0ull)
+    {
+    }
+    template <int NE>
+    __device__ __forceinline__ void add(const float (&v)[NE], float k2, float limit)
+    {
+        if (m == -limit) {
+            float first = v[0];
+#pragma unroll
+            for (int e = 1; e < NE; e++)
+                first = fmaxf(first, v[e]);
+            if (!(first > m)) {
+                // nothing above -limit: no addend unless the whole row is like that; a NaN stays one
+#pragma unroll
+                for (int e = 0; e < NE; e++)
+                    if (v[e] != v[e])
+                        s2 = pair2(v[e], 0.0f);
+                return;
+            }
+            m = first;
+            nb2 = pair2(-m * k2, -m * k2);
+        }
+        const uint64_t kk = pair2(k2, k2);
+        uint64_t part = 0ull;
+#pragma unroll
+        for (int e = 0; e < NE; e += 2) {
+            const float2 x = split2(fma2(pair2(v[e], v[e + 1]), kk, nb2));
+            part = add2(part, pair2(ex2(x.x), ex2(x.y)));
+        }
+        s2 = add2(s2, part);
+        const float2 s = split2(s2);
+        if (s.x + s.y > 0x1p60f) {
+            m += 60.0f / k2;
+            nb2 = pair2(-m * k2, -m * k2);
+            s2 = pair2(s.x * 0x1p-60f, s.y * 0x1p-60f);
+        }
+    }
+    __device__ __forceinline__ MaxSum result() const
+    {
+        const float2 s = split2(s2);
+        const float sum = s.x + s.y;
+        return {sum == __uint_as_float(0x7F800000u) ? sum : m, sum};
+    }
+};
+
+// Whether a block's references and sums, from Running, stand for its row.
+__device__ __forceinline__ bool usable(float m, float limit) { return fabsf(m) < limit; }
+
+// (max, sum) of the elements get(j), any magnitudes: every difference before
+// the scaling.
+template <typename F>
+__device__ __forceinline__ MaxSum scan_any(int begin, int end, int stride, float k2, F get)
+{
+    MaxSum r = {neg_inf(), 0.0f};
+    for (int i = begin; i < end; i += stride) {
+        const float v = get(i);
+        if (v > r.m) {
+            r.s *= ex2((r.m - v) * k2);
+            r.m = v;
+        }
+        r.s += ex2((v - finite_or_zero(r.m)) * k2);
+    }
+    return r;
+}
+
+// The gradient of the entries that are not named, cu 2^((z - bu) k2 - lu): c
+// q_v P, or with a rest class c (P q_r - p_r) u_v with u the softmax over them
+// alone, so that a q_r below FP32's range costs nothing.  A bf16 gradient takes
+// |cu| into the exponent (one rounding of an argument of at most a few hundred:
+// 2^-16 relative, far below bf16's 2^-9) and its sign into the conversion.
+template <typename T>
+struct GradScale {
+    static constexpr bool kFold = sizeof(T) == 2;
+    float cu, bu, lu, k2, off;
+    bool plain, negative;
+
+    __device__ __forceinline__ GradScale(const DistillArgs &a, float c, MaxSum all, MaxSum total, float mass,
+                                         float rest_p, float log2_total, float log2_rest, float k2_)
+        : k2(k2_)
+    {
+        // a rest without any mass (all.s = 0) has no gradient
+        const bool none = a.tail && all.s == 0.0f && total.s != 0.0f;
+        bu = finite_or_zero(a.tail ? all.m : total.m);
+        lu = a.tail ? (none ? 0.0f : lg2(all.s)) : log2_total;
+        cu = a.tail ? c * (mass * ex2(log2_rest) - rest_p) : c * mass;
+        plain = fabsf(bu) < limit_for(k2);
+        negative = cu < 0.0f;
+        if (kFold) {
+            lu -= lg2(fabsf(cu));
+        }
+        off = plain ? fmaf(bu, k2, lu) : 0.0f;
+    }
+    template <bool kPlain, bool kNeg>
+    __device__ __forceinline__ uint4 apply(float (&v)[Vec<T>::N]) const
+    {
+        const uint64_t kk = pair2(k2, k2), no = pair2(-off, -off);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; e += 2) {
+            float2 x;
+            if (kPlain)
+                x = split2(fma2(pair2(v[e], v[e + 1]), kk, no));
+            else
+                x = make_float2((v[e] - bu) * k2 - lu, (v[e + 1] - bu) * k2 - lu);
+            v[e] = ex2(x.x);
+            v[e + 1] = ex2(x.y);
+            if (!kFold) {
+                v[e] *= cu;
+                v[e + 1] *= cu;
+            } else if (kNeg) {
+                v[e] = -v[e];
+                v[e + 1] = -v[e + 1];
+            }
+        }
+        return Vec<T>::pack(v);
+    }
+    // f(plain, negative): the variant of apply, chosen once a row
+    template <typename F>
+    __device__ __forceinline__ void choose(bool fast, F f) const
+    {
+        if (fast && plain && kFold && negative)
+            f(std::true_type(), std::true_type());
+        else if (fast && plain)
+            f(std::true_type(), std::false_type());
+        else if (kFold && negative)
+            f(std::false_type(), std::true_type());
+        else
+            f(std::false_type(), std::false_type());
+    }
+};
+
+__device__ __forceinline__ int64_t entry_index(const DistillArgs &a, int64_t at)
+{
+    return a.idx64 ? reinterpret_cast<const int64_t *>(a.idx)[at]
+                   : (int64_t)reinterpret_cast<const int32_t *>(a.idx)[at];
+}
+
+__device__ __forceinline__ float entry_value(const DistillArgs &a, int64_t at)
+{
+    return a.val_fp32 ? reinterpret_cast<const float *>(a.val)[at]
+                      : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.val)[at]);
+}
+
 // One row per cluster of C CTAs; CTA `rank` takes logits [rank L, rank L + L).
-template <typename T, bool kGrad>
+// kEntries: teacher entries a thread holds.
+template <typename T, bool kGrad, int kEntries>
 __global__ void __launch_bounds__(kDsThreads)
     distill_kernel(const __grid_constant__ DistillArgs a, int C, int64_t L)
 {
     constexpr int NE = Vec<T>::N;
     extern __shared__ __align__(16) uint8_t s_raw[];
-    __shared__ MaxSum s_w[3][kDsWarps];
-    __shared__ float s_f[kDsWarps];
+    __shared__ __align__(16) float4 s_m[3][kDsWarps / 4], s_s[4][kDsWarps / 4], s_f[kDsWarps / 4];
     __shared__ __align__(16) float4 s_x[8];   // each CTA's (max, sum) of the unnamed and of the named logits
     __shared__ __align__(16) float4 s_l[8];   // each CTA's share of the loss (rank 0's copy is used)
-    __shared__ int s_seen;
     __shared__ __align__(8) uint64_t s_bar;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -181,125 +371,103 @@ __global__ void __launch_bounds__(kDsThreads)
     const int len = (int)(len64 < 0 ? 0 : len64 < L ? len64 : L);
 
     // the slice sits at the address modulo 16 that it has in global memory
-    const T *zrow = reinterpret_cast<const T *>(a.z) + row * a.ldz;
-    const T *zs = zrow + v0;
+    const T *zs = reinterpret_cast<const T *>(a.z) + row * a.ldz + v0;
     const int sh = (int)(((uintptr_t)zs & 15u) / sizeof(T));
     T *s_z = reinterpret_cast<T *>(s_raw);     // element i of the slice at s_z[sh + i]
+    const int nvec = len > 0 ? (sh + len + NE - 1) / NE : 0;
+    T *dzs = kGrad ? reinterpret_cast<T *>(a.dz) + row * a.lddz + v0 : nullptr;
+    const int shd = kGrad ? (int)(((uintptr_t)dzs & 15u) / sizeof(T)) : 0;
+
+    // 16 bytes of dz at elements i0 .. i0 + NE - 1 of the slice, those that exist
+    auto store = [&](int i0, uint4 u) {
+        if (sh == shd && i0 >= 0 && i0 + NE <= len) {
+            *reinterpret_cast<uint4 *>(dzs + i0) = u;
+        } else {
+            const T *v = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int e = 0; e < NE; e++)
+                if (i0 + e >= 0 && i0 + e < len)
+                    dzs[i0 + e] = v[e];
+        }
+    };
+    auto store_zeros = [&]() {
+        for (int j = tid; j < nvec; j += kDsThreads)
+            store(j * NE - sh, make_uint4(0u, 0u, 0u, 0u));
+        if (a.loss && rank == 0 && tid == 0)
+            a.loss[row] = 0.0f;
+    };
+    if (w == 0.0f) {  // the logits are not looked at; a NaN weight counts as a weight
+        if (kGrad)
+            store_zeros();
+        else if (rank == 0 && tid == 0)
+            a.loss[row] = 0.0f;
+        return;       // the whole cluster: nobody has touched a peer
+    }
 
     if (tid == 0) {
         mbar_init(&s_bar, 1);
         mbar_fence_init();
-        s_seen = 0;
+        if (len > 0) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(zs - sh);
+            const uint32_t bytes = (uint32_t)(((int64_t)(sh + len) * (int)sizeof(T)) & ~15);
+            mbar_arrive_expect_tx(&s_bar, bytes);
+            for (uint32_t o = 0; o < bytes; o += 32768)
+                bulk_g2s(s_raw + o, src + o, min(32768u, bytes - o), &s_bar);
+        }
     }
-    __syncthreads();
-    if (C > 1)
-        cluster_arrive();  // matched below: every CTA of the cluster runs before anyone writes to it
+    // the last partial 16 bytes of the slice are not copied: one thread an element
+    const int cut = (sh + len) & ~(NE - 1);
+    T last = Vec<T>::put(neg_inf());
+    if (tid < NE && cut + tid >= sh && cut + tid < sh + len)
+        last = zs[cut + tid - sh];
 
-    const bool on = w != 0.0f;  // a NaN weight counts as a weight
-    if (on && tid == 0 && len > 0) {
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(zs - sh);
-        const uint32_t bytes = (uint32_t)(((int64_t)(sh + len) * (int)sizeof(T)) & ~15);
-        mbar_arrive_expect_tx(&s_bar, bytes);
-        for (uint32_t o = 0; o < bytes; o += 32768)
-            bulk_g2s(s_raw + o, src + o, min(32768u, bytes - o), &s_bar);
-    }
-
-    // ---- the teacher's entries: four a thread, every CTA reads them all
-    int idx[kDsEntries];    // in the vocabulary; -1: unused
-    float lp[kDsEntries];   // log p_j (base e), -inf for an unused slot
+    // ---- the teacher's entries: every CTA reads them all
+    int idx[kEntries];      // in the vocabulary; -1: unused
+    float lp[kEntries];     // teacher value, later log p_j (base e); -inf for an unused slot
     int seen = 0;           // entries that count: used ones (rest class), or ones with mass (renormalised)
     const float inv_tau = a.inv_tau, k2 = inv_tau * kLog2e;
-    MaxSum t = {neg_inf(), 0.0f};
+    MaxSum t = {a.tail ? 0.0f : neg_inf(), 0.0f};
 #pragma unroll
-    for (int e = 0; e < kDsEntries; e++) {
+    for (int e = 0; e < kEntries; e++) {
         const int j = tid + e * kDsThreads;
         idx[e] = -1;
         lp[e] = neg_inf();
-        if (on && j < a.k) {
+        if (j < a.k) {
             const int64_t at = row * a.k + j;
-            const int64_t i = a.idx64 ? reinterpret_cast<const int64_t *>(a.idx)[at]
-                                      : (int64_t)reinterpret_cast<const int32_t *>(a.idx)[at];
+            const int64_t i = entry_index(a, at);
+            const float tv = entry_value(a, at);
             if (i >= a.V) {
                 if (a.ctl && rank == 0)
                     record_status(a.ctl, NVFP4_ERR_INDEX);
             } else if (i >= 0) {
                 idx[e] = (int)i;
-            }
-            if (idx[e] >= 0) {
-                const float tv = a.val_fp32 ? reinterpret_cast<const float *>(a.val)[at]
-                                            : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.val)[at]);
                 lp[e] = tv;
                 seen += a.tail || tv != neg_inf();
                 // with a rest class only the plain sum of exp(t_j) is wanted: base 0
-                t = merge(t, a.tail ? MaxSum{0.0f, ex2(tv * kLog2e)} : MaxSum{tv, 1.0f}, k2);
+                t = a.tail ? MaxSum{0.0f, t.s + ex2(tv * kLog2e)} : merge(t, MaxSum{tv, 1.0f}, k2);
             }
         }
     }
-    if (seen)
-        atomicAdd(&s_seen, seen);
-    t = block_merge(t, k2, s_w[0], warp, lane);   // also orders s_seen
-    const bool live = on && s_seen != 0;
-    float mass = 1.0f, rest_p = 0.0f;
-    if (a.tail) {
-        const float sum = t.m == neg_inf() ? 0.0f : t.s;
-        // a NaN sum stays a NaN; a teacher that names the whole vocabulary leaves no rest
-        rest_p = sum > 1.0f || s_seen >= a.V ? 0.0f : 1.0f - sum;
-        mass = sum + rest_p;
-    } else {
-        const float base = finite_or_zero(t.m), log_s = logf(t.s);
-#pragma unroll
-        for (int e = 0; e < kDsEntries; e++)
-            lp[e] = (lp[e] - base) * inv_tau - log_s;
-    }
+    __syncthreads();       // the barrier is initialised
+    if (C > 1)
+        cluster_arrive();  // matched below: every CTA of the cluster runs before anyone writes to it
+    if (len > 0 && !mbar_wait(&s_bar, 0) && a.ctl)
+        record_status(a.ctl, NVFP4_ERR_TIMEOUT);
 
-    T *dzs = kGrad ? reinterpret_cast<T *>(a.dz) + row * a.lddz + v0 : nullptr;
-    const int shd = kGrad ? (int)(((uintptr_t)dzs & 15u) / sizeof(T)) : 0;
-    const int nvec = len > 0 ? (sh + len + NE - 1) / NE : 0;
-
-    bool ok = true;
-    if (on && len > 0) {
-        ok = mbar_wait(&s_bar, 0);   // also for rows that turn out empty: the copy lands in this CTA's memory
-        if (!ok && a.ctl)
-            record_status(a.ctl, NVFP4_ERR_TIMEOUT);
-    }
-    if (!live) {
-        // weight 0 or no teacher entry: loss 0 and gradient 0, whatever the logits hold
-        if (kGrad) {
-            for (int j = tid; j < nvec; j += kDsThreads) {
-                const int i0 = j * NE - sh;
-                if (sh == shd && i0 >= 0 && i0 + NE <= len) {
-                    *reinterpret_cast<uint4 *>(dzs + i0) = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < NE; e++)
-                        if (i0 + e >= 0 && i0 + e < len)
-                            dzs[i0 + e] = Vec<T>::put(0.0f);
-                }
-            }
-        }
-        if (a.loss && rank == 0 && tid == 0)
-            a.loss[row] = 0.0f;
-        if (C > 1)
-            cluster_wait();
-        return;
-    }
-
-    // elements of the first and last 16 bytes outside the slice: -inf; the
-    // last partial 16 bytes were not copied
-    if (tid < 2 * NE && len > 0) {
-        const int i = tid < NE ? tid - sh : (((sh + len) & ~(NE - 1)) + tid - NE) - sh;
-        if (tid < NE ? i < 0 : true) {
-            const bool in = i >= 0 && i < len;
-            s_z[sh + i] = in ? zs[i] : Vec<T>::put(neg_inf());
-        }
+    // elements of the first and last 16 bytes outside the slice: -inf
+    if (tid < NE && len > 0) {
+        if (tid < sh)
+            s_z[tid] = Vec<T>::put(neg_inf());
+        if (cut + tid >= sh)
+            s_z[cut + tid] = last;
     }
     __syncthreads();
 
     // ---- logits of this CTA's named entries, then (rest class) their slots out of the sum
-    float zn[kDsEntries];
+    float zn[kEntries];
     MaxSum named = {neg_inf(), 0.0f};
 #pragma unroll
-    for (int e = 0; e < kDsEntries; e++) {
+    for (int e = 0; e < kEntries; e++) {
         const int64_t i = idx[e] - v0;
         zn[e] = 0.0f;
         if (idx[e] < 0 || i < 0 || i >= len) {
@@ -313,63 +481,117 @@ __global__ void __launch_bounds__(kDsThreads)
     if (a.tail) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kDsEntries; e++)
+        for (int e = 0; e < kEntries; e++)
             if (idx[e] >= 0)
                 s_z[sh + idx[e] - v0] = Vec<T>::put(neg_inf());
         __syncthreads();
     }
 
     // ---- one pass: running maximum and sum
-    MaxSum all = {neg_inf(), 0.0f};
+    const float limit = limit_for(k2);
+    Running run(limit, k2);
     for (int j = tid; j < nvec; j += kDsThreads) {
         float v[NE];
         Vec<T>::unpack(*reinterpret_cast<const uint4 *>(s_raw + (size_t)j * 16), v);
-        float m = v[0];
-#pragma unroll
-        for (int e = 1; e < NE; e++)
-            m = fmaxf(m, v[e]);
-        if (m > all.m) {
-            all.s *= ex2((all.m - m) * k2);
-            all.m = m;
-        }
-        const float base = finite_or_zero(all.m);
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < NE; e++)
-            s += ex2((v[e] - base) * k2);
-        all.s += s;
+        run.add(v, k2, limit);
     }
-    all = block_merge(all, k2, s_w[1], warp, lane);
-    if (a.tail)
-        named = block_merge(named, k2, s_w[2], warp, lane);
+    MaxSum all = run.result();
+
+    // ---- over the block: maxima first, then sums at the common maximum, in a fixed order
+    {
+        const float m1 = a.tail ? warp_max(named.m) : warp_max(t.m);
+        float ma, mb;
+        for (int again = 0;; again++) {
+            const float m0 = warp_max(all.m);
+            if (lane == 0) {
+                reinterpret_cast<float *>(s_m[0])[warp] = m0;
+                reinterpret_cast<float *>(s_m[1])[warp] = m1;
+            }
+            __syncthreads();
+            ma = over_warps_max(s_m[0]);
+            mb = over_warps_max(s_m[1]);
+            if (again || usable(ma, limit))
+                break;
+            __syncthreads();   // every thread has read s_m
+            all = scan_any(tid, len, kDsThreads, k2, [&](int i) { return Vec<T>::get(s_z[sh + i]); });
+        }
+        all = {ma, warp_sum(sum_at(all, ma, k2))};
+        if (a.tail)
+            named = {mb, warp_sum(sum_at(named, mb, k2))};
+        else
+            t = {mb, sum_at(t, mb, k2)};
+        const float st = warp_sum(t.s), sn = warp_sum((float)seen);
+        if (lane == 0) {
+            reinterpret_cast<float *>(s_s[0])[warp] = all.s;
+            reinterpret_cast<float *>(s_s[1])[warp] = named.s;
+            reinterpret_cast<float *>(s_s[2])[warp] = st;
+            reinterpret_cast<float *>(s_s[3])[warp] = sn;
+        }
+        __syncthreads();
+        all.s = over_warps_sum(s_s[0]);
+        if (a.tail)
+            named.s = over_warps_sum(s_s[1]);
+        t.s = over_warps_sum(s_s[2]);
+        seen = (int)over_warps_sum(s_s[3]);   // at most 1024: exact
+    }
     if (C > 1) {
         cluster_wait();
         if (tid < C)
             st_cluster_f4(smem_addr(&s_x[rank]), (uint32_t)tid, make_float4(all.m, all.s, named.m, named.s));
         __syncwarp();
         cluster_arrive();
+    }
+
+    // ---- the teacher's distribution
+    float mass = 1.0f, rest_p = 0.0f;
+    if (a.tail) {
+        // a NaN sum stays a NaN; a teacher that names the whole vocabulary leaves no rest
+        rest_p = t.s > 1.0f || seen >= a.V ? 0.0f : 1.0f - t.s;
+        mass = t.s + rest_p;
+    } else {
+        const float base = finite_or_zero(t.m), log_s = lg2(t.s) * kLn2;
+#pragma unroll
+        for (int e = 0; e < kEntries; e++)
+            lp[e] = (lp[e] - base) * inv_tau - log_s;
+    }
+
+    if (C > 1) {
         cluster_wait();
-        all = {s_x[0].x, s_x[0].y};
-        named = {s_x[0].z, s_x[0].w};
-        for (int i = 1; i < C; i++) {
-            all = merge(all, MaxSum{s_x[i].x, s_x[i].y}, k2);
-            if (a.tail)
-                named = merge(named, MaxSum{s_x[i].z, s_x[i].w}, k2);
+        float ma = neg_inf(), mn = neg_inf();
+        for (int i = 0; i < C; i++) {
+            ma = fmaxf(ma, s_x[i].x);
+            mn = fmaxf(mn, s_x[i].z);
         }
+        float sa = 0.0f, sn = 0.0f;
+        for (int i = 0; i < C; i++) {
+            sa += sum_at(MaxSum{s_x[i].x, s_x[i].y}, ma, k2);
+            if (a.tail)
+                sn += sum_at(MaxSum{s_x[i].z, s_x[i].w}, mn, k2);
+        }
+        all = {ma, sa};
+        if (a.tail)
+            named = {mn, sn};
+    }
+    if (seen == 0) {
+        // no teacher entry: loss 0 and gradient 0, whatever the logits hold
+        if (kGrad)
+            store_zeros();
+        else if (rank == 0 && tid == 0)
+            a.loss[row] = 0.0f;
+        return;
     }
     // log2 q_v = (z_v - total.m) k2 - log2_total; a row of nothing but -inf has
     // total.s = 0 and gives NaN
     const MaxSum total = a.tail ? merge(all, named, k2) : all;
-    const float base = finite_or_zero(total.m), log2_total = log2f(total.s);
-    constexpr float kLn2 = 0.6931471805599453f;
+    const float base = finite_or_zero(total.m), log2_total = lg2(total.s);
     // log2 of q_r, the share of the entries that are not named
-    const float log2_rest = (all.m - base) * k2 + log2f(all.s) - log2_total;
+    const float log2_rest = (all.m - base) * k2 + lg2(all.s) - log2_total;
 
     // ---- this CTA's share of the loss, sent to rank 0 while the gradient is written
     if (a.loss) {
         float l = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kDsEntries; e++) {
+        for (int e = 0; e < kEntries; e++) {
             if (idx[e] >= 0) {
                 const float p = ex2(lp[e] * kLog2e);
                 if (p != 0.0f)
@@ -378,13 +600,10 @@ __global__ void __launch_bounds__(kDsThreads)
         }
         l = warp_sum(l);
         if (lane == 0)
-            s_f[warp] = l;
+            reinterpret_cast<float *>(s_f)[warp] = l;
         __syncthreads();
         if (tid == 0) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kDsWarps; i++)
-                sum += s_f[i];
+            const float sum = over_warps_sum(s_f);
             if (C > 1)
                 st_cluster_f4(smem_addr(&s_l[rank]), 0u, make_float4(sum, 0.0f, 0.0f, 0.0f));
             else
@@ -398,32 +617,17 @@ __global__ void __launch_bounds__(kDsThreads)
     if (kGrad) {
         const float g = a.grad_loss ? a.grad_loss[a.grad_rows ? row : 0] : 1.0f;
         const float c = g * w * a.tau;
-        // Entries not named: c q_v P, or with a rest class c (P q_r - p_r) u_v with
-        // u the softmax over them alone, so that a q_r below FP32's range costs
-        // nothing.  A rest without any mass (all.s = 0) has no gradient.
-        const bool none = a.tail && all.s == 0.0f && total.s != 0.0f;
-        const float bu = a.tail ? finite_or_zero(all.m) : base;
-        const float lu = a.tail ? (none ? 0.0f : log2f(all.s)) : log2_total;
-        const float cu = a.tail ? c * (mass * ex2(log2_rest) - rest_p) : c * mass;
-        for (int j = tid; j < nvec; j += kDsThreads) {
-            float v[NE];
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(s_raw + (size_t)j * 16), v);
-#pragma unroll
-            for (int e = 0; e < NE; e++)
-                v[e] = cu * ex2((v[e] - bu) * k2 - lu);
-            const int i0 = j * NE - sh;
-            if (sh == shd && i0 >= 0 && i0 + NE <= len) {
-                *reinterpret_cast<uint4 *>(dzs + i0) = Vec<T>::pack(v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < NE; e++)
-                    if (i0 + e >= 0 && i0 + e < len)
-                        dzs[i0 + e] = Vec<T>::put(v[e]);
+        const GradScale<T> scale(a, c, all, total, mass, rest_p, log2_total, log2_rest, k2);
+        scale.choose(true, [&](auto plain, auto neg) {
+            for (int j = tid; j < nvec; j += kDsThreads) {
+                float v[NE];
+                Vec<T>::unpack(*reinterpret_cast<const uint4 *>(s_raw + (size_t)j * 16), v);
+                store(j * NE - sh, scale.template apply<decltype(plain)::value, decltype(neg)::value>(v));
             }
-        }
+        });
         __syncthreads();   // the named entries are written over what the pass above stored
 #pragma unroll
-        for (int e = 0; e < kDsEntries; e++)
+        for (int e = 0; e < kEntries; e++)
             if (idx[e] >= 0)
                 dzs[idx[e] - v0] = Vec<T>::put(c * (mass * ex2((zn[e] - base) * k2 - log2_total) - ex2(lp[e] * kLog2e)));
     }
@@ -434,12 +638,430 @@ __global__ void __launch_bounds__(kDsThreads)
         for (int i = 0; i < C; i++)
             l += s_l[i].x;
         if (a.tail && rest_p != 0.0f)
-            l += rest_p * (logf(rest_p) - log2_rest * kLn2);
+            l += rest_p * (lg2(rest_p) * kLn2 - log2_rest * kLn2);
         a.loss[row] = l * w * a.tau * a.tau;
     }
 }
 
+// ---------------------------------------------------------------- many long rows
+// Two CTAs per SM, persistent over the rows, a row each.  A cluster per row
+// spends more on starting clusters and waiting for the slowest CTA than on the
+// logits (4096 rows of 131072 bf16 logits: 500 us, 63 % of the copy bandwidth);
+// here a row's chunks pass through a ring in shared memory twice (424 us,
+// 75 %).  The chunks that the ring still holds after the first pass are used
+// from there, the ones before them come again from L2, which holds the rest of
+// 304 rows of 256 KB.  One warp copies, the others are consumers.  One CTA of
+// 1024 threads per SM was slower (475 us): its reductions and the turn from one
+// pass to the other leave the SM without work, which the other CTA fills here.
+// What bounds it now is issue: about 50 instructions per 8 logits and pass.
+constexpr int kDtThreads = 512, kDtPerSm = 2, kDtWarps = kDtThreads / 32 - 1, kDtConsumers = 32 * kDtWarps;
+constexpr int kDtEach = 4;                       // 16-byte vectors of a chunk that a consumer takes
+constexpr int kDtVecs = kDtEach * kDtConsumers;
+constexpr int kDtChunk = kDtVecs * 16;           // 30720 bytes
+constexpr int kDtMaxSlots = 3;
+constexpr int kDtSmem = 113 * 1024 - 1200;       // dynamic shared memory of one of two CTAs
+
+__device__ __forceinline__ void bulk_g2s_hint(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t pol)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(pol)
+        : "memory");
+}
+
+// One value per consumer warp -> combined in a fixed order, for every thread
+// (called by whole warps).
+__device__ __forceinline__ float over_consumers_max(const float *s_w, int lane) { return warp_max(s_w[lane]); }
+__device__ __forceinline__ float over_consumers_sum(const float *s_w, int lane) { return warp_sum(s_w[lane]); }
+
 template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kDtThreads, kDtPerSm)
+    distill_stream_kernel(const __grid_constant__ DistillArgs a, const int slots)
+{
+    constexpr int NE = Vec<T>::N;
+    extern __shared__ __align__(16) uint8_t s_ring[];  // slots chunks, then one bit per logit (rest class)
+    __shared__ float s_m[2][32], s_s[4][32], s_f[32];
+    __shared__ __align__(8) uint64_t full[kDtMaxSlots], empty[kDtMaxSlots];
+    uint32_t *s_bits = reinterpret_cast<uint32_t *>(s_ring + slots * kDtChunk);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < slots; i++) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kDtWarps);
+        }
+        mbar_fence_init();
+    }
+    if (a.tail) {
+        const int words = (int)((a.V + NE + 31) / 32);
+        for (int i = tid; i < words; i += kDtThreads)
+            s_bits[i] = 0u;
+    }
+    if (tid < 32) {  // values of each reduction that no warp writes
+        s_m[0][tid] = s_m[1][tid] = neg_inf();
+        for (int i = 0; i < 4; i++)
+            s_s[i][tid] = 0.0f;
+        s_f[tid] = 0.0f;
+    }
+    __syncthreads();
+
+    // chunks of a row, and the first one that the ring still holds after the first pass
+    const T *z = reinterpret_cast<const T *>(a.z);
+    auto shift = [&](int64_t row) { return (int)(((uintptr_t)(z + row * a.ldz) & 15u) / sizeof(T)); };
+    auto vectors = [&](int sh) { return (int)((sh + a.V + NE - 1) / NE); };
+    uint32_t load = 0;  // copies so far, in the order both sides agree on: copy i uses slot i % slots
+
+    if (warp == kDtWarps) {
+        if (lane == 0) {
+            const uint64_t drop = l2_policy_evict_first();
+            bool ok = true;
+            for (int64_t row = blockIdx.x; row < a.T && ok; row += gridDim.x) {
+                if (a.weight && a.weight[row] == 0.0f)
+                    continue;
+                const int sh = shift(row), n = (vectors(sh) + kDtVecs - 1) / kDtVecs;
+                const int kept = kGrad ? max(0, n - slots) : n;
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(z + row * a.ldz - sh);
+                const int64_t total = (int64_t)((sh + a.V) * (int64_t)sizeof(T)) & ~15LL;
+                for (int i = 0; i < n + (kGrad ? kept : 0) && ok; i++, load++) {
+                    const int c = i < n ? i : i - n, slot = load % slots;
+                    if (load >= (uint32_t)slots && !mbar_wait(&empty[slot], (load / slots - 1) & 1)) {
+                        if (a.ctl)
+                            record_status(a.ctl, NVFP4_ERR_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    const int64_t at = (int64_t)c * kDtChunk;
+                    const uint32_t bytes = (uint32_t)max((int64_t)0, min((int64_t)kDtChunk, total - at));
+                    mbar_arrive_expect_tx(&full[slot], bytes);
+                    if (bytes) {
+                        // chunks that will be read once more stay in L2
+                        if (c < kept && i < n && kGrad)
+                            bulk_g2s(s_ring + slot * kDtChunk, src + at, bytes, &full[slot]);
+                        else
+                            bulk_g2s_hint(s_ring + slot * kDtChunk, src + at, bytes, &full[slot], drop);
+                    }
+                }
+            }
+        }
+        return;
+    }
+
+    const float inv_tau = a.inv_tau, k2 = inv_tau * kLog2e, limit = limit_for(k2);
+    const int V = (int)a.V;
+    int slot = 0;             // of the next copy
+    uint32_t phase = 0;       // and its barrier's parity
+    bool ok = true;
+    auto next = [&]() {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    auto release = [&](int at) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&empty[at]);
+    };
+    // A row's weight, this thread's teacher entry and the student's logit there
+    // are three dependent reads: they are issued a row ahead, the logit after
+    // the first pass.
+    struct Entry {
+        float w = 0.0f, lp = neg_inf(), zn = 0.0f;
+        int idx = -1;
+    };
+    auto entry_of = [&](int64_t row) {
+        Entry e;
+        if (row < a.T) {
+            e.w = a.weight ? a.weight[row] : 1.0f;
+            if (tid < a.k) {
+                const int64_t at = row * a.k + tid, i = entry_index(a, at);
+                e.lp = entry_value(a, at);
+                if (i >= a.V && e.w != 0.0f && a.ctl)
+                    record_status(a.ctl, NVFP4_ERR_INDEX);
+                e.idx = i >= 0 && i < a.V ? (int)i : -1;
+            }
+        }
+        return e;
+    };
+    auto logit_of = [&](Entry &e, int64_t row) {
+        if (e.idx >= 0 && e.w != 0.0f)
+            e.zn = Vec<T>::get(z[row * a.ldz + e.idx]);
+        else
+            e.lp = neg_inf();
+    };
+    Entry ahead = entry_of(blockIdx.x);
+    logit_of(ahead, blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const Entry now = ahead;
+        ahead = entry_of(row + gridDim.x);
+        const float w = now.w;
+        const int sh = shift(row), nvec = vectors(sh), n = (nvec + kDtVecs - 1) / kDtVecs;
+        const T *zr = z + row * a.ldz;
+        T *dzr = kGrad ? reinterpret_cast<T *>(a.dz) + row * a.lddz : nullptr;
+        const bool aligned = kGrad && sh == (int)(((uintptr_t)dzr & 15u) / sizeof(T));
+        // vectors [j0, j1) lie in the row; one before and one after may do so in part
+        // (no copy covers the latter) and are done apart, by consumers 0 and 32
+        const int j0 = sh ? 1 : 0, j1 = (sh + V) / NE;
+        const int odd = tid == 0 && sh ? 0 : tid == 32 && nvec > j1 && nvec - 1 >= j0 ? nvec - 1 : -1;
+        auto store_each = [&](int j, uint4 u) {
+            const T *v = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int e = 0; e < NE; e++) {
+                const int i = j * NE - sh + e;
+                if (i >= 0 && i < V)
+                    dzr[i] = v[e];
+            }
+        };
+        auto store = [&](int j, uint4 u) {
+            if (aligned && j >= j0 && j < j1)
+                *reinterpret_cast<uint4 *>(dzr + j * NE - sh) = u;
+            else
+                store_each(j, u);
+        };
+        if (w == 0.0f) {  // the logits are not looked at
+            if (kGrad)
+                for (int j = tid; j < nvec; j += kDtConsumers)
+                    store(j, make_uint4(0u, 0u, 0u, 0u));
+            if (a.loss && tid == 0)
+                a.loss[row] = 0.0f;
+            logit_of(ahead, row + gridDim.x);
+            continue;
+        }
+
+        const int idx = now.idx;
+        const float zn = now.zn;
+        float lp = now.lp;
+        if (a.tail && idx >= 0)
+            atomicOr(&s_bits[(sh + idx) >> 5], 1u << ((sh + idx) & 31));
+        if (a.tail)
+            named_sync(1, kDtConsumers);
+
+        // vector j element by element: -inf outside the row
+        auto odd_vector = [&](int j, float (&v)[NE]) {
+#pragma unroll
+            for (int e = 0; e < NE; e++) {
+                const int i = j * NE - sh + e;
+                v[e] = i < 0 || i >= V ? neg_inf() : Vec<T>::get(zr[i]);
+            }
+        };
+
+        // without the named entries (rest class)
+        auto leave_out = [&](int j, float (&v)[NE]) {
+            const uint32_t bits = s_bits[(j * NE) >> 5] >> ((j * NE) & 31) & ((1u << NE) - 1u);
+            if (bits) {
+#pragma unroll
+                for (int e = 0; e < NE; e++)
+                    if (bits >> e & 1)
+                        v[e] = neg_inf();
+            }
+        };
+
+        // ---- first pass: running maximum and sum
+        const int kept = kGrad ? max(0, n - slots) : n;   // chunks released after this pass
+        Running run(limit, k2);
+        int slot2 = 0;                                     // where the chunks that stay begin
+        for (int c = 0; c < n; c++, next()) {
+            if (c == kept)
+                slot2 = slot;
+            ok = ok && mbar_wait(&full[slot], phase);
+            const uint8_t *at = s_ring + slot * kDtChunk;
+            // a chunk wholly inside the row needs no checks
+            auto sum_chunk = [&](auto inside) {
+#pragma unroll
+                for (int u = 0; u < kDtEach; u++) {
+                    const int local = tid + u * kDtConsumers, j = c * kDtVecs + local;
+                    if (decltype(inside)::value || (j >= j0 && j < j1)) {
+                        float v[NE];
+                        Vec<T>::unpack(*reinterpret_cast<const uint4 *>(at + local * 16), v);
+                        if (a.tail)
+                            leave_out(j, v);
+                        run.add(v, k2, limit);
+                    }
+                }
+            };
+            if (c * kDtVecs >= j0 && (c + 1) * kDtVecs <= j1)
+                sum_chunk(std::true_type());
+            else
+                sum_chunk(std::false_type());
+            if (c < kept)
+                release(slot);
+        }
+        if (odd >= 0) {
+            float v[NE];
+            odd_vector(odd, v);
+            if (a.tail)
+                leave_out(odd, v);
+            run.add(v, k2, limit);
+        }
+        MaxSum all = run.result();
+
+        logit_of(ahead, row + gridDim.x);
+
+        // ---- over the consumers: maxima first, then sums at the common maximum, in a fixed order
+        const bool mine = idx >= 0;
+        MaxSum named = {neg_inf(), 0.0f}, t = {neg_inf(), 0.0f};
+        if (mine) {
+            if (a.tail) {
+                named = {zn, zn == neg_inf() ? 0.0f : 1.0f};
+                t.s = ex2(lp * kLog2e);  // only the plain sum is wanted
+            } else {
+                t = {lp, 1.0f};
+            }
+        }
+        {
+            const bool teach = warp * 32 < a.k;   // this warp holds entries
+            const float m1 = teach ? warp_max(a.tail ? named.m : t.m) : neg_inf();
+            float ma, mb;
+            for (int again = 0;; again++) {
+                const float m0 = warp_max(all.m);
+                if (lane == 0) {
+                    s_m[0][warp] = m0;
+                    s_m[1][warp] = m1;
+                }
+                named_sync(1, kDtConsumers);
+                ma = over_consumers_max(s_m[0], lane);
+                mb = over_consumers_max(s_m[1], lane);
+                if (again || usable(ma, limit))
+                    break;
+                named_sync(1, kDtConsumers);   // every thread has read s_m
+                all = scan_any(tid, V, kDtConsumers, k2, [&](int i) {
+                    return a.tail && (s_bits[(sh + i) >> 5] >> ((sh + i) & 31) & 1) ? neg_inf() : Vec<T>::get(zr[i]);
+                });
+            }
+            const float sa = warp_sum(sum_at(all, ma, k2));
+            float sn = 0.0f, st = 0.0f, cnt = 0.0f;
+            if (teach) {
+                sn = warp_sum(sum_at(named, mb, k2));
+                st = warp_sum(a.tail ? t.s : sum_at(t, mb, k2));
+                cnt = warp_sum(mine && (a.tail || lp != neg_inf()) ? 1.0f : 0.0f);
+            }
+            if (lane == 0) {
+                s_s[0][warp] = sa;
+                s_s[1][warp] = sn;
+                s_s[2][warp] = st;
+                s_s[3][warp] = cnt;
+            }
+            named_sync(1, kDtConsumers);
+            if (a.tail && mine)
+                s_bits[(sh + idx) >> 5] = 0u;   // every thread is done with the bits
+            all = {ma, over_consumers_sum(s_s[0], lane)};
+            if (a.tail)
+                named = {mb, over_consumers_sum(s_s[1], lane)};
+            t = {mb, over_consumers_sum(s_s[2], lane)};
+        }
+        const int seen = (int)over_consumers_sum(s_s[3], lane);   // at most 480: exact
+        float mass = 1.0f, rest_p = 0.0f;
+        if (a.tail) {
+            // a NaN sum stays a NaN; a teacher that names the whole vocabulary leaves no rest
+            rest_p = t.s > 1.0f || seen >= a.V ? 0.0f : 1.0f - t.s;
+            mass = t.s + rest_p;
+        } else {
+            lp = (lp - finite_or_zero(t.m)) * inv_tau - lg2(t.s) * kLn2;
+        }
+        // log2 q_v = (z_v - base) k2 - log2_total; a row of nothing but -inf gives NaN
+        const MaxSum total = a.tail ? merge(all, named, k2) : all;
+        const float base = finite_or_zero(total.m), log2_total = lg2(total.s);
+        const float log2_rest = (all.m - base) * k2 + lg2(all.s) - log2_total;
+        const float p = mine ? ex2(lp * kLog2e) : 0.0f;
+        if (a.loss) {
+            const float l = warp_sum(p != 0.0f ? p * (lp - ((zn - base) * inv_tau - log2_total * kLn2)) : 0.0f);
+            if (lane == 0)
+                s_f[warp] = l;
+        }
+
+        // ---- second pass: the chunks in the ring, then the earlier ones again
+        if (kGrad) {
+            const float g = a.grad_loss ? a.grad_loss[a.grad_rows ? row : 0] : 1.0f;
+            const float c0 = g * w * a.tau;
+            const GradScale<T> scale(a, c0, all, total, mass, rest_p, log2_total, log2_rest, k2);
+            // fast: whole vectors to 16-byte boundaries
+            auto pass = [&](auto fast, auto neg) {
+                constexpr bool kFast = decltype(fast)::value, kNeg = decltype(neg)::value;
+                if (odd >= 0) {
+                    float v[NE];
+                    odd_vector(odd, v);
+                    store_each(odd, seen ? scale.template apply<kFast, kNeg>(v) : make_uint4(0u, 0u, 0u, 0u));
+                }
+                for (int i = 0; i < n; i++) {
+                    const bool stays = i < n - kept;
+                    const int c = stays ? kept + i : i - (n - kept), at = stays ? slot2 : slot;
+                    if (!stays)
+                        ok = ok && mbar_wait(&full[slot], phase);
+                    const uint8_t *src = s_ring + at * kDtChunk + tid * 16;
+                    const int j = c * kDtVecs + tid;
+                    if (kFast && c * kDtVecs >= j0 && (c + 1) * kDtVecs <= j1) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(dzr + (int64_t)j * NE - sh);
+#pragma unroll
+                        for (int u = 0; u < kDtEach; u++) {
+                            float v[NE];
+                            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(src + u * kDtConsumers * 16), v);
+                            dst[u * kDtConsumers] = scale.template apply<kFast, kNeg>(v);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < kDtEach; u++) {
+                            const int ju = j + u * kDtConsumers;
+                            if (ju >= j0 && ju < j1) {
+                                float v[NE];
+                                Vec<T>::unpack(*reinterpret_cast<const uint4 *>(src + u * kDtConsumers * 16), v);
+                                const uint4 g4 = scale.template apply<kFast, kNeg>(v);
+                                // without a teacher entry the gradient is 0, whatever the logits hold
+                                if (kFast)
+                                    *reinterpret_cast<uint4 *>(dzr + (int64_t)ju * NE - sh) = g4;
+                                else
+                                    store_each(ju, seen ? g4 : make_uint4(0u, 0u, 0u, 0u));
+                            }
+                        }
+                    }
+                    release(at);
+                    if (!stays)
+                        next();
+                    else if (++slot2 == slots)
+                        slot2 = 0;
+                }
+            };
+            scale.choose(aligned && seen != 0, pass);
+            named_sync(1, kDtConsumers);  // the named entries are written over what the pass above stored
+            if (mine && seen)
+                dzr[idx] = Vec<T>::put(c0 * (mass * ex2((zn - base) * k2 - log2_total) - p));
+        } else {
+            named_sync(1, kDtConsumers);
+        }
+        if (a.loss && warp == 0) {
+            float l = over_consumers_sum(s_f, lane);
+            if (a.tail && rest_p != 0.0f)
+                l += rest_p * (lg2(rest_p) * kLn2 - log2_rest * kLn2);
+            if (lane == 0)
+                a.loss[row] = seen ? l * w * a.tau * a.tau : 0.0f;
+        }
+    }
+    if (!ok && a.ctl && lane == 0)
+        record_status(a.ctl, NVFP4_ERR_TIMEOUT);
+}
+
+// Shared memory of the stream kernel for V logits of `size` bytes: ring slots
+// beside the bits of a rest class.
+int stream_slots(const DistillArgs &a, size_t size)
+{
+    const int64_t bits = a.tail ? (a.V + (int64_t)(16 / size) + 31) / 32 * 4 : 0;
+    return (int)std::min<int64_t>(kDtMaxSlots, (kDtSmem - bits) / kDtChunk);
+}
+
+template <typename T, bool kGrad>
+cudaError_t run_distill_stream(const DistillArgs &a, int slots, cudaStream_t s, const DeviceInfo &dev)
+{
+    const size_t bits = a.tail ? (size_t)(a.V + (int64_t)(16 / sizeof(T)) + 31) / 32 * 4 : 0;
+    const size_t smem = (size_t)slots * kDtChunk + bits;
+    cudaError_t e = cudaFuncSetAttribute(distill_stream_kernel<T, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    distill_stream_kernel<T, kGrad><<<(unsigned)std::min<int64_t>(a.T, kDtPerSm * dev.num_sms), kDtThreads, smem, s>>>(a, slots);
+    return cudaGetLastError();
+}
+
+template <typename T, bool kGrad, int kEntries>
 cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
     // Cluster size: the smallest power of two whose slices are at most 40 KB,
@@ -448,12 +1070,12 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
     // more CTAs, down to slices of 4 KB.
     const int64_t row_bytes = a.V * (int64_t)sizeof(T);
     int C = 1;
-    while (C < 8 && (row_bytes > C * 40960LL || (a.T * C * 2 <= dev.num_sms && row_bytes > C * 8192LL)))
+    while (C < 8 && (row_bytes > C * 73728LL || (a.T * C * 2 <= dev.num_sms && row_bytes > C * 8192LL)))
         C *= 2;
     constexpr int NE = Vec<T>::N;
     const int64_t L = ((a.V + C - 1) / C + NE - 1) / NE * NE;
     const size_t smem = (size_t)L * sizeof(T) + 32;
-    cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, kGrad, kEntries>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kDistillMaxSlice + 32);
     if (e != cudaSuccess)
         return e;
@@ -469,7 +1091,19 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<T, kGrad>, a, C, L);
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, kGrad, kEntries>, a, C, L);
+}
+
+// One entry a thread for up to 256 of them, else four: most teachers keep fewer
+// than 256, and the other three's registers and branches cost every thread.
+template <typename T, bool kGrad>
+cudaError_t run_distill_k(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    static_assert(kDistillMaxK == 4 * kDsThreads, "entries per thread");
+    const int slots = stream_slots(a, sizeof(T));
+    if (a.V * (int64_t)sizeof(T) > 98304 && a.T >= dev.num_sms && a.k <= kDtConsumers && slots >= 2)
+        return run_distill_stream<T, kGrad>(a, slots, s, dev);
+    return a.k <= kDsThreads ? run_distill<T, kGrad, 1>(a, s, dev) : run_distill<T, kGrad, 4>(a, s, dev);
 }
 
 }  // namespace
@@ -477,8 +1111,8 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
 cudaError_t launch_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
     if (a.dz)
-        return a.z_fp32 ? run_distill<float, true>(a, s, dev) : run_distill<__nv_bfloat16, true>(a, s, dev);
-    return a.z_fp32 ? run_distill<float, false>(a, s, dev) : run_distill<__nv_bfloat16, false>(a, s, dev);
+        return a.z_fp32 ? run_distill_k<float, true>(a, s, dev) : run_distill_k<__nv_bfloat16, true>(a, s, dev);
+    return a.z_fp32 ? run_distill_k<float, false>(a, s, dev) : run_distill_k<__nv_bfloat16, false>(a, s, dev);
 }
 
 }  // namespace nvfp4

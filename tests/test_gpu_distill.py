@@ -283,3 +283,61 @@ def test_refusals(nv):
     with pytest.raises(nv.NVFP4Error) as e:
         nv.distill_topk_loss(z, idx, val, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == nv.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,V,k", [(torch.bfloat16, 60001, 40), (torch.bfloat16, 150001, 64),
+                                       (torch.float32, 40003, 300), (torch.float32, 131072, 992),
+                                       (torch.float32, 25001, 1), (torch.bfloat16, 140000, 1000)])
+def test_many_long_rows(nv, dtype, V, k, tail):
+    """As many rows as SMs and more, rows longer than an SM's shared memory among them; masked rows, empty rows and
+    unusual logits on the way.  Sampled rows against the definition, the others against the same rows alone."""
+    T = 333
+    z, idx, val = _case(T, V, k, dtype, V + k, tail)
+    nan, inf = float("nan"), float("inf")
+    w = torch.linspace(0.5, 2, T, device="cuda")
+    w[::7] = 0.0
+    z[7] = nan                                  # weight 0
+    idx[8] = -1
+    z[9, 5] = nan
+    z[10, 17:V - 40] = -inf
+    z[11] = torch.finfo(dtype).min
+    z[12] = -inf
+    if k > 1:
+        idx[13, 1:] = -1
+        val[13, 1:] = nan
+        val[15, 1:] = -inf
+    g = torch.linspace(-1, 1, T, device="cuda")
+    loss, dz = nv.distill_topk_loss_grad(z, idx, val, tail=tail, row_weight=w, grad_loss=g)
+    assert torch.equal(torch.nan_to_num(loss, 3.0),
+                       torch.nan_to_num(nv.distill_topk_loss(z, idx, val, tail=tail, row_weight=w), 3.0))
+    zc = z.clone()
+    l2, d2 = nv.distill_topk_loss_grad(zc, idx, val, tail=tail, row_weight=w, grad_loss=g, out=zc)
+    same = lambda a, b: torch.equal(torch.nan_to_num(a, 3.0), torch.nan_to_num(b, 3.0))  # noqa: E731
+    assert same(l2, loss) and same(d2, dz)
+    rows = [0, 1, 7, 8, 9, 10, 11, 12, 13, 15, 100, 153, 154, 305, 306, 331, 332]
+    z64, i64, t64 = ref.to64(z[rows]), idx[rows].cpu().numpy(), ref.to64(val[rows])
+    w64, g64 = ref.to64(w[rows]), ref.to64(g[rows])
+    rl, rd = ref.distill(z64, i64, t64, 1.0, tail, w64, g64)
+    lt, dt = _tol(z64, i64, t64, 1.0, tail, w64, g64)
+    gl, gd = ref.to64(loss[rows]), ref.to64(dz[rows])
+    assert np.array_equal(np.isnan(gl), np.isnan(rl)) and np.array_equal(np.isinf(gl), np.isinf(rl))
+    fin = np.isfinite(rl)
+    assert (np.abs(gl - rl)[fin] <= lt[fin] + 1e-37).all()
+    assert np.array_equal(np.isnan(gd), np.isnan(rd))
+    ok = ~np.isnan(rd)
+    if dtype == torch.bfloat16:
+        dt = dt + 2.0 ** -8 * np.abs(np.nan_to_num(rd))
+    assert (np.abs(gd - rd)[ok] <= dt[ok] + 1e-37).all()
+
+
+def test_many_long_rows_of_odd_stride(nv):
+    z, idx, val = _case(200, 70001, 30, torch.bfloat16, 5, True, ld=70013)
+    out = torch.empty(200, 70005, dtype=torch.bfloat16, device="cuda")[:, :70001]
+    loss, dz = nv.distill_topk_loss_grad(z, idx, val, tail=True, out=out)
+    rows = [0, 1, 2, 3, 5, 151, 152, 199]
+    z64, i64, t64 = ref.to64(z[rows]), idx[rows].cpu().numpy(), ref.to64(val[rows])
+    rl, rd = ref.distill(z64, i64, t64, 1.0, True)
+    lt, dt = _tol(z64, i64, t64, 1.0, True, None, None)
+    assert (np.abs(ref.to64(loss[rows]) - rl) <= lt).all()
+    assert (np.abs(ref.to64(dz[rows]) - rd) <= dt + 2.0 ** -8 * np.abs(rd) + 1e-37).all()
