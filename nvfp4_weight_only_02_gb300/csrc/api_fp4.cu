@@ -1,6 +1,7 @@
 // api_fp4.cu -- extern "C" entry points of the 4-bit activation operators
 // (MXFP4 quantiser, W4A4 product and layer) and of the distillation loss:
 // argument checks on the host, then launches on the caller's stream.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -130,7 +131,7 @@ size_t nvfp4_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (!operand_ok(M, K) || !operand_ok(N, K) || !tiles_ok(M, N))
         return 0;
-    return kCtlBytes;
+    return align256(kWsHeaderBytes);   // scratch always starts behind the counters, which other calls count on
 }
 
 nvfp4_status nvfp4_w4a4_gemm(nvfp4_fp4_format format, const uint8_t *a_codes, const uint8_t *a_scales,
@@ -171,7 +172,7 @@ size_t nvfp4_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (nvfp4_w4a4_workspace_bytes(M, N, K) == 0 || !tiles_ok(M, K))
         return 0;
-    return kCtlBytes + align256(code_bytes(M, K)) + align256(scale_bytes(M, K, 32));
+    return nvfp4_w4a4_workspace_bytes(M, N, K) + align256(code_bytes(M, K)) + align256(scale_bytes(M, K, 32));
 }
 
 nvfp4_status nvfp4_mx_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, int64_t M, int64_t N, int64_t K,
@@ -189,16 +190,25 @@ nvfp4_status nvfp4_mx_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, in
     if (ws_bytes < need)
         return NVFP4_ERR_WORKSPACE;
     NVFP4_TRY_DEVICE(dev);
-    uint8_t *ws = (uint8_t *)workspace;
-    MxQuantArgs q = quant_args(x, x_dtype, M, K, ldx);
-    q.codes = ws + kCtlBytes;
-    q.scales = q.codes + align256(code_bytes(M, K));
-    const cudaError_t e = launch_mx_quantize(q, (cudaStream_t)stream);
-    if (e != cudaSuccess)
-        return NVFP4_ERR_CUDA;
     W4A4Args a = {};
-    a.a_codes = q.codes;
-    a.a_scales = q.scales;
+    if (w4a4_takes_tokens(M, N, K, *dev)) {
+        a.x = x;
+        a.x_fp32 = x_dtype == NVFP4_OUT_FP32;
+        a.ldx = ldx;
+    } else {
+        MxQuantArgs q = quant_args(x, x_dtype, M, K, ldx);
+        q.codes = (uint8_t *)workspace + nvfp4_w4a4_workspace_bytes(M, N, K);
+        q.scales = q.codes + align256(code_bytes(M, K));
+        // behind a product that streams weights the quantiser may start early (16 tokens: 10.9 us a call and
+        // 12.4 without, N = 18944, K = 3584); the tile kernel then starts late (1024 tokens: 34.9 and 31.6)
+        q.overlap = M <= 64;
+        const cudaError_t e = launch_mx_quantize(q, (cudaStream_t)stream);
+        if (e != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        a.a_codes = q.codes;
+        a.a_scales = q.scales;
+        a.after_quantise = true;
+    }
     a.w_codes = w_codes;
     a.w_scales = w_scales;
     a.M = M;
@@ -207,7 +217,6 @@ nvfp4_status nvfp4_mx_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, in
     a.y = y;
     a.y_fp32 = y_dtype == NVFP4_OUT_FP32;
     a.ctl = (uint32_t *)workspace;
-    a.after_quantise = true;
     return from_cuda(launch_w4a4(a, (cudaStream_t)stream, *dev));
 }
 
@@ -217,7 +226,7 @@ size_t nvfp4_mx_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K)
     if (M < 1 || M > kMaxDim - 31 || nvfp4_w4a4_workspace_bytes(M, K, N) == 0 ||
         nvfp4_w4a4_workspace_bytes(N, K, up32(M)) == 0 || K % 32 != 0 || !tiles_ok(M, N))
         return 0;
-    return kCtlBytes + align256(code_bytes(M, N)) + align256(scale_bytes(M, N, 32)) +
+    return nvfp4_w4a4_workspace_bytes(M, N, K) + align256(code_bytes(M, N)) + align256(scale_bytes(M, N, 32)) +
            align256(code_bytes(N, up32(M))) + align256(scale_bytes(N, up32(M), 32));
 }
 
@@ -241,7 +250,7 @@ nvfp4_status nvfp4_mx_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int6
         return NVFP4_ERR_WORKSPACE;
     NVFP4_TRY_DEVICE(dev);
     cudaStream_t s = (cudaStream_t)stream;
-    uint8_t *at = (uint8_t *)workspace + kCtlBytes;
+    uint8_t *at = (uint8_t *)workspace + nvfp4_w4a4_workspace_bytes(M, N, K);
     MxQuantArgs q = quant_args(dy, dy_dtype, M, N, lddy);
     uint8_t *codes = at, *scales = codes + align256(code_bytes(M, N));
     uint8_t *codes_t = scales + align256(scale_bytes(M, N, 32));

@@ -1,22 +1,27 @@
 // gemm_w4a4.cu -- Y (M x N) = s_a s_w A W^T with both operands in 4 bits, on
 // the block-scaled tensor-core instructions (tcgen05, FP32 accumulators in
-// TMEM).
+// TMEM): few tokens.
 //
 // Both operands are E2M1 codes, row-major along the contraction, with a scale
 // per block of 32 (MXFP4: E8M0) or 16 (NVFP4: E4M3) in tiles of 128 rows x 4
 // blocks.  The instruction multiplies the codes of 64 elements, applies both
 // scales and accumulates in FP32, so nothing is dequantised on the way.
 //
-// A CTA takes 128 weight rows as the MMA's M side and up to 128 tokens as its
-// N side, so that few tokens cost few columns; the contraction is split over
-// the CTAs of a cluster when there are fewer tiles than SMs, and the shares
-// are added in rank order through distributed shared memory.  Codes come by
-// TMA (128-byte swizzle, zero fill outside), scale tiles by bulk copies; one
-// thread copies scales to TMEM and issues the MMAs.
+// What bounds few tokens is the weights' bytes.  A CTA takes 128 weight rows as
+// the MMA's M side and the tokens as its N side, so that few tokens cost few
+// columns; K is split over the CTAs of a cluster when there are fewer tiles
+// than CTA places, and the shares are added in rank order through distributed
+// shared memory.  Codes come by TMA (128-byte swizzle, zero fill outside),
+// scale tiles by bulk copies; one thread copies scales to TMEM and issues the
+// MMAs.  Up to 4 tokens are quantised by the CTAs themselves (each the part of
+// K that it multiplies) while the first weights are on their way: a kernel of
+// its own costs a launch and 2 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
+#include "mx_codec.cuh"
 #include "sm100.cuh"
 
 namespace nvfp4 {
@@ -25,145 +30,182 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kWsThreads = 192;  // warps 0-3: epilogue, 4: copies, 5: MMA
+constexpr int kWsThreads = 192;  // warps 0-3: tokens and epilogue, 4: copies, 5: MMA
 constexpr int kWsRows = 128;     // weight rows per CTA
 constexpr int kWsK = 256;        // elements of K per stage (128 bytes of codes a row)
+constexpr int kWsSmem = 113 * 1024;  // two CTAs share an SM
+constexpr int kWsMaxStages = 6;
 
 struct W4A4Params {
     const uint8_t *a_scales, *w_scales;
     const float *a_ts, *w_ts;
-    int M, N;
+    const void *x;  // unquantised tokens (M x K, ldx between rows)
+    int64_t ldx;
+    int M, N, K;
     int ksteps;   // stages over the whole K
     int ktiles;   // scale tiles along K
-    int mtiles;
+    int mtiles;   // tiles of tokens
     int split;    // CTAs of a cluster that share a tile's K
+    int stages;
+    int early;    // the weights were complete before the kernel before this one started
     void *y;
     int y_fp32;
     uint32_t *ctl;
 };
 
-template <bool kNv, int NT>
+// Tokens as the kernel gets them: quantised, or bf16 / FP32 to be quantised here.
+enum Tokens { kCodes, kBf16, kFp32 };
+
+template <bool kNv, int NT, Tokens kTok>
 struct WsShape {
     static constexpr int kTiles = kNv ? 4 : 2;                    // scale tiles per stage and operand
     static constexpr int kScaleBytes = kTiles * 512;
-    static constexpr int kStageBytes = kWsRows * 128 + NT * 128 + 2 * kScaleBytes;
-    // two CTAs share an SM (227 KB)
-    static constexpr int kStages = 112000 / kStageBytes < 5 ? 112000 / kStageBytes : 5;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
+    static constexpr int kWBytes = kWsRows * 128 + kScaleBytes, kXBytes = NT * 128 + kScaleBytes;
+    static constexpr bool kOwn = kTok != kCodes;                  // tokens quantised here stay for all stages
+    static constexpr int kFixed = 1024 + 256;
     static constexpr int kAccCols = NT < 64 ? 64 : NT;
     static constexpr int kSfCols = 2 * kTiles * 4;                // one stage's scales of both operands
-    static constexpr int kTmemCols = kAccCols + 2 * kSfCols <= 128 ? 128 : 256;
+    static constexpr int kSfBufs = kNv && NT <= 64 ? 2 : 4;       // stages whose scales fit beside the accumulator
+    static constexpr int kTmemCols = kAccCols + kSfBufs * kSfCols <= 128 ? 128 : 256;
+    static_assert(kAccCols + kSfBufs * kSfCols <= kTmemCols, "TMEM");
+    // ring stages beside `nk` stages of own tokens; 0: they do not fit
+    static int stages(int nk)
+    {
+        const int room = kWsSmem - kFixed - (kOwn ? nk * kXBytes : 0);
+        const int fit = room / (kOwn ? kWBytes : kWBytes + kXBytes);
+        return std::max(0, std::min({fit, kWsMaxStages, std::max(nk, 2)}));
+    }
+    static size_t smem(int nk, int stages)
+    {
+        const size_t ring = (size_t)stages * (kOwn ? kWBytes : kWBytes + kXBytes) + (kOwn ? (size_t)nk * kXBytes : 0);
+        return kFixed + std::max(ring, (size_t)NT * 512);   // the ring also holds the shares of a split K
+    }
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank)
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t local, uint32_t rank)
 {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(local), "r"(rank)
-                 : "memory");
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(local), "r"(rank)
+        : "memory");
     return v;
 }
 
-template <bool kNv, int NT>
-__global__ void __launch_bounds__(kWsThreads)
+template <bool kNv, int NT, Tokens kTok>
+__global__ void __launch_bounds__(kWsThreads, 2)
     w4a4_stream_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                        const W4A4Params p)
 {
-    using S = WsShape<kNv, NT>;
-    constexpr int kStages = S::kStages;
+    using S = WsShape<kNv, NT, kTok>;
+    const int kStages = p.stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ __align__(8) uint64_t full[kWsMaxStages], empty[kWsMaxStages], acc_full[1], x_full[1];
+    __shared__ uint32_t s_tmem;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = blockIdx.x / p.split, nt = tile / p.mtiles, mt = tile % p.mtiles;   // weight rows, tokens
+    const int ks0 = (int)((int64_t)p.ksteps * rank / p.split), ks1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);
+    const int nk = ks1 - ks0;
+    const int nx = S::kOwn ? (p.ksteps + p.split - 1) / p.split : kStages;  // token stages in shared memory
+
     uint8_t *sW = smem, *sX = sW + kStages * kWsRows * 128;
-    uint8_t *sWs = sX + kStages * NT * 128, *sXs = sWs + kStages * S::kScaleBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sXs + kStages * S::kScaleBytes);
-    uint64_t *empty = full + kStages, *acc_full = empty + kStages;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_full + 1);
+    uint8_t *sWs = sX + nx * NT * 128, *sXs = sWs + kStages * S::kScaleBytes;
     float *red = reinterpret_cast<float *>(smem);  // [NT][128], once the ring is drained
 
-    const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
+        mbar_init(x_full, 128);
         mbar_fence_init();
     }
     if (warp == 5) {
-        tmem_alloc(s_tmem, S::kTmemCols);
+        tmem_alloc(&s_tmem, S::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
-
-    const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
-    const int tile = blockIdx.x / p.split, nt = tile / p.mtiles, mt = tile % p.mtiles;
-    const int ks0 = (int)((int64_t)p.ksteps * rank / p.split), ks1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);
-    const int nk = ks1 - ks0;
+    const uint32_t tmem = s_tmem;
 
     if (warp == 4) {
         const uint8_t *wsc = p.w_scales + (size_t)nt * p.ktiles * 512;
-        const uint8_t *xsc = p.a_scales + (size_t)(mt * NT / 128) * p.ktiles * 512;
+        const uint8_t *xsc = p.a_scales + (size_t)mt * p.ktiles * 512;   // more than one: 128 tokens each
         auto scale_bytes = [&](int ks) { return (uint32_t)min(S::kTiles, p.ktiles - ks * S::kTiles) * 512u; };
         auto load_w = [&](int i, int st) {
             const int ks = ks0 + i;
             const uint32_t sb = scale_bytes(ks);
-            mbar_arrive_expect_tx(&full[st], (kWsRows + NT) * 128 + 2 * sb);
+            mbar_arrive_expect_tx(&full[st], (kWsRows + (S::kOwn ? 0 : NT)) * 128 + (S::kOwn ? 1 : 2) * sb);
             tma_load_2d(sW + st * kWsRows * 128, &tmap_w, &full[st], ks * 128, nt * kWsRows);
             bulk_g2s(sWs + st * S::kScaleBytes, wsc + (size_t)ks * S::kScaleBytes, sb, &full[st]);
         };
         auto load_x = [&](int i, int st) {
+            if (S::kOwn)
+                return;
             const int ks = ks0 + i;
             tma_load_2d(sX + st * NT * 128, &tmap_a, &full[st], ks * 128, mt * NT);
             bulk_g2s(sXs + st * S::kScaleBytes, xsc + (size_t)ks * S::kScaleBytes, scale_bytes(ks), &full[st]);
         };
-        // weights do not depend on the kernel before this one: they start first
+        // Before the kernels ahead in the stream are complete, the weights may be
+        // brought on their way: into shared memory where nothing that can still
+        // run writes them (p.early), else into L2 only.
         const int head = min(nk, kStages);
-        for (int i = 0; i < head; i++) {
-            if (elect_one())
-                load_w(i, i);
-            __syncwarp();
-        }
-        pdl_wait();
-        for (int i = 0; i < head; i++) {
-            if (elect_one())
-                load_x(i, i);
-            __syncwarp();
-        }
-        for (int i = head; i < nk; i++) {
-            const int st = i % kStages;
-            if (!mbar_wait_warp(&empty[st], (i / kStages + 1) & 1)) {
-                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
-                break;
+        if (elect_one()) {
+            for (int i = 0; i < head; i++) {
+                if (p.early)
+                    load_w(i, i);
+                else
+                    tma_prefetch_2d(&tmap_w, (ks0 + i) * 128, nt * kWsRows);
             }
-            if (elect_one()) {
+            pdl_wait();
+            pdl_launch_dependents();
+            for (int i = 0; i < head; i++) {
+                if (!p.early)
+                    load_w(i, i);
+                load_x(i, i);
+            }
+            int st = 0;
+            uint32_t ph = 0;
+            for (int i = head; i < nk; i++) {
+                if (!mbar_wait(&empty[st], ph)) {
+                    record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                    break;
+                }
                 load_w(i, st);
                 load_x(i, st);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
-            __syncwarp();
         }
     } else if (warp == 5) {
         constexpr uint32_t id0 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 0);
         constexpr uint32_t id2 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 2);
-        for (int i = 0; i < nk; i++) {
-            const int st = i % kStages;
-            // the MMAs that read this half of the scale columns (two stages ago) are done, and this stage's
-            // operands have landed
-            if ((i >= 2 && !mbar_wait_warp(&empty[(i - 2) % kStages], ((i - 2) / kStages) & 1)) ||
-                !mbar_wait_warp(&full[st], (i / kStages) & 1)) {
-                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
-                break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
+        if (elect_one()) {
+            bool ok = !S::kOwn || mbar_wait(x_full, 0);
+            int st = 0, st2 = kStages - S::kSfBufs, sf = 0;  // st2: the stage kSfBufs steps ago
+            uint32_t ph = 0, ph2 = 1;
+            for (int i = 0; i < nk && ok; i++) {
+                // the MMAs that read these scale columns (kSfBufs stages ago) are done, which a ring of no more
+                // stages implies, and this stage's operands have landed
+                ok = (kStages <= S::kSfBufs || i < S::kSfBufs || mbar_wait(&empty[st2], ph2)) &&
+                     mbar_wait(&full[st], ph);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const int sx = S::kOwn ? i : st;
                 const uint64_t wd = smem_desc_sw128(smem_addr(sW + st * kWsRows * 128));
-                const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * NT * 128));
+                const uint64_t xd = smem_desc_sw128(smem_addr(sX + sx * NT * 128));
                 const uint64_t wsd = smem_desc_scales(smem_addr(sWs + st * S::kScaleBytes));
-                const uint64_t xsd = smem_desc_scales(smem_addr(sXs + st * S::kScaleBytes));
-                const uint32_t sfw = tmem + S::kAccCols + (i & 1) * S::kSfCols, sfx = sfw + S::kTiles * 4;
+                const uint64_t xsd = smem_desc_scales(smem_addr(sXs + sx * S::kScaleBytes));
+                const uint32_t sfw = tmem + S::kAccCols + sf * S::kSfCols, sfx = sfw + S::kTiles * 4;
                 const int tiles = min(S::kTiles, p.ktiles - (ks0 + i) * S::kTiles);
 #pragma unroll
                 for (int t = 0; t < S::kTiles; t++) {
@@ -180,36 +222,87 @@ __global__ void __launch_bounds__(kWsThreads)
                                         sfx + 4 * t, (i | j) != 0);
                 }
                 mma_commit(&empty[st]);
+                if (i + 1 == nk)
+                    mma_commit(acc_full);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                if (++sf == S::kSfBufs)
+                    sf = 0;
+                if (++st2 == kStages) {
+                    st2 = 0;
+                    ph2 ^= 1;
+                }
             }
-            __syncwarp();
-        }
-        if (elect_one())
-            mma_commit(acc_full);
-        __syncwarp();
-    } else {
-        if (!mbar_wait_warp(acc_full, 0)) {
-            if (threadIdx.x == 0)
+            if (!ok)
                 record_status(p.ctl, NVFP4_ERR_TIMEOUT);
         }
+    } else {
+        pdl_wait();
+        if (S::kOwn) {
+            // ---------------- this CTA's part of the tokens, quantised into the swizzled layout of a TMA copy:
+            // four lanes a block of 32, eight elements each
+            using T = typename std::conditional<kTok == kFp32, float, __nv_bfloat16>::type;
+            const T *x = reinterpret_cast<const T *>(p.x);
+            const int per = nk * (kWsK / 8), items = p.M * per;   // groups of eight elements, per token and in all
+            constexpr int kU = kTok == kFp32 ? 3 : 6;             // loads in flight
+            for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < items; i0 += 128 * kU) {
+                Raw8<T> raw[kU];
+#pragma unroll
+                for (int u = 0; u < kU; u++) {
+                    const int i = i0 + 128 * u, m = i / per, k = ks0 * kWsK + (i - m * per) * 8;
+                    raw[u].zero();
+                    if (i < items && k < p.K)
+                        raw[u].load(x + (int64_t)m * p.ldx + k);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; u++) {
+                    const int i = i0 + 128 * u, m = i / per, g = i - m * per;
+                    uint32_t a = raw[u].amax_bits();
+                    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                    const uint32_t byte = e8m0_of(a);
+                    uint32_t q = 0u;
+                    if (byte != 255u) {
+                        float v[8];
+                        raw[u].floats(v);
+                        const float inv = e8m0_inverse(byte);
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            v[e] = __fmul_rn(v[e], inv);
+                        q = e2m1_encode8(v);
+                    }
+                    if (i < items) {
+                        const int ks = g / (kWsK / 8), kb = g % (kWsK / 8) * 4;   // stage, byte of its row
+                        *reinterpret_cast<uint32_t *>(sX + ks * NT * 128 + m * 128 + (((kb >> 4) ^ (m & 7)) << 4) +
+                                                      (kb & 15)) = q;
+                        if ((lane & 3) == 0)
+                            sXs[ks * S::kScaleBytes + (kb >> 6) * 512 + m * 16 + (kb >> 4 & 3)] = (uint8_t)byte;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(x_full);
+        }
+        if (!mbar_wait_warp(acc_full, 0) && threadIdx.x == 0)
+            record_status(p.ctl, NVFP4_ERR_TIMEOUT);
         tc_fence_after();
     }
     __syncwarp();
 
     // one after the other: the product of two small tensor scales may underflow
     const float s_a = p.a_ts ? *p.a_ts : 1.0f, s_w = p.w_ts ? *p.w_ts : 1.0f;
-    const int n = nt * kWsRows + threadIdx.x;
-    auto store = [&](int col, float v) {
-        const int m = mt * NT + col;
-        if (m < p.M && n < p.N) {
-            v = __fmul_rn(__fmul_rn(v, s_a), s_w);
-            if (p.y_fp32)
-                reinterpret_cast<float *>(p.y)[(size_t)m * p.N + n] = v;
-            else
-                reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)m * p.N + n] = __float2bfloat16_rn(v);
-        }
+    auto store = [&](int m, int n, float v) {
+        v = __fmul_rn(__fmul_rn(v, s_a), s_w);
+        if (p.y_fp32)
+            reinterpret_cast<float *>(p.y)[(size_t)m * p.N + n] = v;
+        else
+            reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)m * p.N + n] = __float2bfloat16_rn(v);
     };
     if (warp < 4) {
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const int n = nt * kWsRows + threadIdx.x;
         constexpr int kChunk = NT < 32 ? NT : 32;
         for (int c = 0; c < NT; c += 32) {
             uint32_t v[32];
@@ -217,25 +310,44 @@ __global__ void __launch_bounds__(kWsThreads)
             tmem_ld32_finish(v);
 #pragma unroll
             for (int i = 0; i < kChunk; i++) {
-                if (p.split == 1)
-                    store(c + i, __uint_as_float(v[i]));
-                else
+                const int m = mt * NT + c + i;
+                if (p.split > 1)
                     red[(c + i) * 128 + threadIdx.x] = __uint_as_float(v[i]);
+                else if (m < p.M && n < p.N)
+                    store(m, n, __uint_as_float(v[i]));
             }
         }
     }
     if (p.split > 1) {
+        // ---------------- the tokens' columns are shared out; four weight rows a thread
         __syncthreads();
         cluster_sync();
-        if (warp < 4) {
-            const int c0 = NT * rank / p.split, c1 = NT * (rank + 1) / p.split;
-            for (int c = c0; c < c1; c++) {
-                const uint32_t at = smem_addr(&red[c * 128 + threadIdx.x]);
-                float v = 0.0f;
-                for (int r = 0; r < p.split; r++)
-                    v += ld_cluster_f32(at, (uint32_t)r);
-                store(c, v);
+        const int cols = min(NT, p.M - mt * NT);
+        const int c0 = cols * rank / p.split, c1 = cols * (rank + 1) / p.split;
+        for (int i = threadIdx.x; i < (c1 - c0) * 32; i += kWsThreads) {
+            const int c = c0 + i / 32, r4 = i % 32 * 4;
+            const uint32_t at = smem_addr(&red[c * 128 + r4]);
+            float4 part[8];
+#pragma unroll
+            for (int r = 0; r < 8; r++)
+                if (r < p.split)
+                    part[r] = ld_cluster_f4(at, (uint32_t)r);
+            float4 v = part[0];
+#pragma unroll
+            for (int r = 1; r < 8; r++) {
+                if (r < p.split) {
+                    v.x += part[r].x;
+                    v.y += part[r].y;
+                    v.z += part[r].z;
+                    v.w += part[r].w;
+                }
             }
+            const float vv[4] = {v.x, v.y, v.z, v.w};
+            const int n = nt * kWsRows + r4;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (n + e < p.N)
+                    store(mt * NT + c, n + e, vv[e]);
         }
         __syncwarp();
         cluster_sync();
@@ -248,16 +360,24 @@ __global__ void __launch_bounds__(kWsThreads)
     }
 }
 
-template <bool kNv, int NT>
+// K is split while the tiles leave CTA places free: two per SM, at most 8 CTAs to a cluster.
+int split_for(int64_t tiles, int64_t K, const DeviceInfo &dev)
+{
+    const int64_t ksteps = (K + kWsK - 1) / kWsK;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({8, ksteps, 2 * dev.num_sms / tiles}));
+}
+
+template <bool kNv, int NT, Tokens kTok>
 cudaError_t run_stream(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {
-    using S = WsShape<kNv, NT>;
+    using S = WsShape<kNv, NT, kTok>;
     CUtensorMap tw, ta;
     cudaError_t e = encode_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w_codes, (uint64_t)a.K / 2,
                                          (uint64_t)a.N, (uint64_t)a.K / 2, 128, kWsRows, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess)
-        e = encode_tensor_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a_codes, (uint64_t)a.K / 2, (uint64_t)a.M,
-                                 (uint64_t)a.K / 2, 128, NT, CU_TENSOR_MAP_SWIZZLE_128B);
+        e = S::kOwn ? (ta = tw, cudaSuccess)
+                    : encode_tensor_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a_codes, (uint64_t)a.K / 2,
+                                           (uint64_t)a.M, (uint64_t)a.K / 2, 128, NT, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
     W4A4Params p;
@@ -265,56 +385,81 @@ cudaError_t run_stream(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
     p.w_scales = a.w_scales;
     p.a_ts = a.a_ts;
     p.w_ts = a.w_ts;
+    p.x = a.x;
+    p.ldx = a.ldx;
     p.M = (int)a.M;
     p.N = (int)a.N;
+    p.K = (int)a.K;
     p.ksteps = (int)((a.K + kWsK - 1) / kWsK);
     const int64_t per_tile = kNv ? 64 : 128;
     p.ktiles = (int)((a.K + per_tile - 1) / per_tile);
     p.mtiles = (int)((a.M + NT - 1) / NT);
+    const int64_t tiles = (int64_t)p.mtiles * ((a.N + kWsRows - 1) / kWsRows);
+    p.split = split_for(tiles, a.K, dev);
+    const int nk = (p.ksteps + p.split - 1) / p.split;
+    p.stages = S::stages(nk);
+    p.early = a.after_quantise ? 1 : 0;
     p.y = a.y;
     p.y_fp32 = a.y_fp32 ? 1 : 0;
     p.ctl = a.ctl;
-    const int64_t tiles = (int64_t)p.mtiles * ((a.N + kWsRows - 1) / kWsRows);
-    // two CTAs per SM: split K while the tiles leave room
-    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, p.ksteps, 2 * dev.num_sms / tiles}));
-    e = cudaFuncSetAttribute(w4a4_stream_kernel<kNv, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = cudaFuncSetAttribute(w4a4_stream_kernel<kNv, NT, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWsSmem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
     cfg.blockDim = dim3(kWsThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = S::smem(nk, p.stages);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.after_quantise ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, w4a4_stream_kernel<kNv, NT>, tw, ta, p);
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, w4a4_stream_kernel<kNv, NT, kTok>, tw, ta, p);
 }
 
 template <bool kNv>
 cudaError_t run_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {
     if (a.M <= 16)
-        return run_stream<kNv, 16>(a, s, dev);
+        return run_stream<kNv, 16, kCodes>(a, s, dev);
     if (a.M <= 32)
-        return run_stream<kNv, 32>(a, s, dev);
+        return run_stream<kNv, 32, kCodes>(a, s, dev);
+    // More tokens go to the tile kernel, 256 x 256 at a time on 76 pairs of CTAs
+    // (100 tokens: 11.3 us by tiles and 12.3 streamed at N = 18944, K = 3584; 64:
+    // 11.4 and 10.8), unless there are few such tiles with long sums: only the
+    // stream splits K (256 tokens at N = 3584, K = 18944: 27 and 16 us; 512: 27
+    // and 24; at K = 3584: 8.8 and 9.4).
+    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+    const bool long_sums = big * 5 <= dev.num_sms && a.K >= 32 * kWsK && a.M <= 512;
     if (a.M <= 64)
-        return run_stream<kNv, 64>(a, s, dev);
-    if (a.M <= 128)
-        return run_stream<kNv, 128>(a, s, dev);
+        return run_stream<kNv, 64, kCodes>(a, s, dev);
+    if (long_sums)
+        return run_stream<kNv, 128, kCodes>(a, s, dev);
     return launch_w4a4_tile(a, s, dev);
 }
 
 }  // namespace
 
+bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev)
+{
+    // 4 tokens: 10.2 us in one kernel, 11.0 with a quantiser of its own (N = 18944, K = 3584);
+    // 8: 11.9 and 11.2, since every CTA quantises them again
+    if (M > 4)
+        return false;
+    const int64_t ksteps = (K + kWsK - 1) / kWsK, split = split_for((N + kWsRows - 1) / kWsRows, K, dev), nk = (ksteps + split - 1) / split;
+    // at least three stages of weights beside the tokens
+    return nk <= 64 && WsShape<false, 16, kBf16>::stages((int)nk) >= std::min<int64_t>(3, std::max<int64_t>(nk, 2));
+}
+
 cudaError_t launch_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {
+    if (a.x)
+        return a.x_fp32 ? run_stream<false, 16, kFp32>(a, s, dev) : run_stream<false, 16, kBf16>(a, s, dev);
     return a.nvfp4 ? run_w4a4<true>(a, s, dev) : run_w4a4<false>(a, s, dev);
 }
 

@@ -42,7 +42,7 @@ struct TileParams {
 template <bool kNv, int BN>
 struct TlShape {
     static constexpr int kTiles = kNv ? 4 : 2;                 // scale tiles per stage and 128 rows
-    static constexpr int kBRowTiles = BN / 128;
+    static constexpr int kBRowTiles = (BN + 127) / 128;         // scale tiles over B's rows
     static constexpr int kABytes = 128 * 128, kBBytes = BN / 2 * 128;
     static constexpr int kSaBytes = kTiles * 512, kSbBytes = kBRowTiles * kTiles * 512;
     static constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
@@ -52,11 +52,15 @@ struct TlShape {
     static constexpr size_t kSmem = kFixed + (size_t)kStages * kStageBytes;
     static constexpr int kSfA = kTiles * 4, kSfB = kTiles * kBRowTiles * 4, kSf = kSfA + kSfB;
     static constexpr int kTmemCols = 512;
-    // columns: accumulator 0 at 0, accumulator 1 at BN - kShared, then two stages' scales
-    static constexpr int kFree = 2 * BN + 2 * kSf - kTmemCols;
-    static constexpr int kShared = kFree > 0 ? (kFree + 31) / 32 * 32 : 0;
+    // columns: accumulator 0 at 0, accumulator 1 at BN - kShared, then the scales of kSfBufs stages.  An MMA's
+    // completion is known about 800 cycles after its issue, 1.5 stages' worth of MMAs at 256 columns: with two
+    // stages' scales in TMEM every stage took 640 cycles whatever its width.
+    static constexpr int kSfBufs = kNv ? 3 : 4;
+    static constexpr int kOver = 2 * BN + kSfBufs * kSf - kTmemCols;
+    static constexpr int kShared = kOver > 64 ? (kOver + 31) / 32 * 32 : kOver > 0 ? 64 : 0;
     static constexpr int kAcc1 = BN - kShared, kSfCol = 2 * BN - kShared;
-    static_assert(kSfCol + 2 * kSf <= kTmemCols && kShared >= 64, "TMEM; each half of the epilogue has a shared chunk");
+    static_assert(kSfCol + kSfBufs * kSf <= kTmemCols && kSfBufs < kStages && (kShared == 0 || kShared >= 64),
+                  "TMEM; each half of the epilogue has a shared chunk");
 };
 
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
@@ -178,8 +182,8 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
     uint8_t *sA = smem, *sB = sA + kStages * S::kABytes, *sOut = sB + kStages * S::kBBytes;
     uint8_t *sSa = sOut + kTlEpiWarps * kTlStoreBytes, *sSb = sSa + kStages * S::kSaBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(sSb + kStages * S::kSbBytes);
-    uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 1;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 1);
+    uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 2;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,8 +193,10 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 2 * kTlEpiWarps);
+        mbar_init(&acc_full[0], 1);
+        mbar_init(&acc_full[1], 1);
+        mbar_init(&acc_empty[0], 2 * kTlEpiWarps);
+        mbar_init(&acc_empty[1], 2 * kTlEpiWarps);
         *s_abort = 0;
         mbar_fence_init();
     }
@@ -202,6 +208,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     pdl_wait();
+    pdl_launch_dependents();
 
     const int cid = (int)cluster_id_x(), ncl = (int)cluster_count_x();
     const int ntot = p.mpairs * p.ntiles;
@@ -213,85 +220,89 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
 
     if (warp == kTlEpiWarps) {
         // ---------------- copies: this CTA's half of each operand
-        uint32_t it = 0;
-        for (int t = cid; t < ntot && !aborted(); t += ncl) {
-            int mp, nt;
-            tile_at(t, p.mpairs, p.ntiles, mp, nt);
-            const int mt = 2 * mp + crank;
-            for (int ks = 0; ks < p.ksteps; ks++, it++) {
-                const int st = it % kStages;
-                if (!mbar_wait_warp(&empty[st], ((it / kStages) & 1) ^ 1)) {
-                    fail();
-                    break;
-                }
-                if (elect_one()) {
+        if (elect_one()) {
+            uint32_t it = 0;
+            for (int t = cid; t < ntot && !*s_abort; t += ncl) {
+                int mp, nt;
+                tile_at(t, p.mpairs, p.ntiles, mp, nt);
+                const int mt = 2 * mp + crank;
+                for (int ks = 0; ks < p.ksteps; ks++, it++) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1)) {
+                        fail();
+                        break;
+                    }
                     const uint32_t bar = cluster_addr(&full[st], 0);
                     if (crank == 0)
                         mbar_arrive_expect_tx(&full[st], 2 * S::kStageBytes);
                     tma_load_2d_pair(sA + st * S::kABytes, &tm_a, bar, ks * 128, mt * 128);
                     tma_load_2d_pair(sB + st * S::kBBytes, &tm_b, bar, ks * 128, nt * BN + crank * (BN / 2));
                     tma_load_3d_pair(sSa + st * S::kSaBytes, &tm_sa, bar, 0, ks * S::kTiles, mt);
-                    tma_load_3d_pair(sSb + st * S::kSbBytes, &tm_sb, bar, 0, ks * S::kTiles, nt * S::kBRowTiles);
+                    tma_load_3d_pair(sSb + st * S::kSbBytes, &tm_sb, bar, 0, ks * S::kTiles, nt * BN / 128);
                 }
-                __syncwarp();
+            }
+            // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
+            for (int k = 0; k < kStages && !*s_abort; k++) {
+                const uint32_t i2 = it + k;
+                if (i2 >= (uint32_t)kStages && !mbar_wait(&empty[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
+                    fail();
             }
         }
-        // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
-        for (int k = 0; k < kStages && !aborted(); k++) {
-            const uint32_t i2 = it + k;
-            if (i2 >= (uint32_t)kStages && !mbar_wait_warp(&empty[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
-                fail();
-        }
     } else if (warp == kTlEpiWarps + 1) {
-        // ---------------- MMA, by the pair's leader
-        if (crank == 0) {
+        // ---------------- MMA, by one thread of the pair's leader.  What this loop takes per stage bounds
+        // narrow tiles: 460 cycles, 100 less than with all lanes in it and votes.
+        if (crank == 0 && elect_one()) {
             constexpr uint32_t id0 = idesc_fp4(256, BN, kNv ? 0 : 1, 0), id2 = idesc_fp4(256, BN, kNv ? 0 : 1, 2);
             uint32_t it = 0, lt = 0;
-            for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
-                // the shared columns of the accumulator before this one have been read
-                if (lt > 0 && !mbar_wait_warp(acc_empty, (lt - 1) & 1)) {
+            for (int t = cid; t < ntot && !*s_abort; t += ncl, lt++) {
+                int mp, nt;
+                tile_at(t, p.mpairs, p.ntiles, mp, nt);
+                // the shared columns of the accumulator before this one have been read, or without
+                // shared columns the accumulator that this tile takes (barriers for each accumulator:
+                // either side may be two tiles ahead of the other)
+                if (S::kShared ? lt >= 1 && !mbar_wait(&acc_empty[0], (lt - 1) & 1)
+                               : lt >= 2 && !mbar_wait(&acc_empty[lt & 1], (lt / 2 - 1) & 1)) {
                     fail();
                     break;
                 }
                 tc_fence_after();
                 const uint32_t acc = tmem + (lt & 1 ? S::kAcc1 : 0);
+                // 192 rows: every other tile begins in the middle of a scale tile, two columns on
+                const uint32_t sb_off = (uint32_t)(nt * BN % 128) / 32;
                 bool ok = true;
                 for (int ks = 0; ks < p.ksteps; ks++, it++) {
                     const int st = it % kStages;
-                    // the MMAs that read this half of the scale columns (two stages ago) are done, and this
-                    // stage's operands have landed
-                    if ((it >= 2 && !mbar_wait_warp(&empty[(it - 2) % kStages], ((it - 2) / kStages) & 1)) ||
-                        !mbar_wait_warp(&full[st], (it / kStages) & 1)) {
+                    // the MMAs that read these scale columns (kSfBufs stages ago) are done, and this stage's
+                    // operands have landed
+                    constexpr uint32_t kB = S::kSfBufs;
+                    if ((it >= kB && !mbar_wait(&empty[(it - kB) % kStages], ((it - kB) / kStages) & 1)) ||
+                        !mbar_wait(&full[st], (it / kStages) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t ad = smem_desc_sw128(smem_addr(sA + st * S::kABytes));
-                        const uint64_t bd = smem_desc_sw128(smem_addr(sB + st * S::kBBytes));
-                        const uint64_t sad = smem_desc_scales(smem_addr(sSa + st * S::kSaBytes));
-                        const uint64_t sbd = smem_desc_scales(smem_addr(sSb + st * S::kSbBytes));
-                        const uint32_t sfa = tmem + S::kSfCol + (it & 1) * S::kSf, sfb = sfa + S::kSfA;
+                    const uint64_t ad = smem_desc_sw128(smem_addr(sA + st * S::kABytes));
+                    const uint64_t bd = smem_desc_sw128(smem_addr(sB + st * S::kBBytes));
+                    const uint64_t sad = smem_desc_scales(smem_addr(sSa + st * S::kSaBytes));
+                    const uint64_t sbd = smem_desc_scales(smem_addr(sSb + st * S::kSbBytes));
+                    const uint32_t sfa = tmem + S::kSfCol + it % S::kSfBufs * S::kSf, sfb = sfa + S::kSfA;
 #pragma unroll
-                        for (int k = 0; k < S::kTiles; k++) {
-                            tmem_cp_scales_pair(sfa + 4 * k, sad + k * 32);
+                    for (int k = 0; k < S::kTiles; k++) {
+                        tmem_cp_scales_pair(sfa + 4 * k, sad + k * 32);
 #pragma unroll
-                            for (int r = 0; r < S::kBRowTiles; r++)
-                                tmem_cp_scales_pair(sfb + 4 * (k * S::kBRowTiles + r),
-                                                    sbd + (r * S::kTiles + k) * 32);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const int k = kNv ? j : j / 2;
-                            const uint32_t sa = sfa + 4 * k, sb = sfb + 4 * k * S::kBRowTiles;
-                            mma_fp4_pair<kNv>(acc, ad + 2 * j, bd + 2 * j, !kNv && (j & 1) ? id2 : id0, sa, sb,
-                                              (ks | j) != 0);
-                        }
-                        mma_commit_pair(&empty[st]);
-                        if (ks + 1 == p.ksteps)
-                            mma_commit_pair(acc_full);
+                        for (int r = 0; r < S::kBRowTiles; r++)
+                            tmem_cp_scales_pair(sfb + 4 * (k * S::kBRowTiles + r), sbd + (r * S::kTiles + k) * 32);
                     }
-                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int k = kNv ? j : j / 2;
+                        const uint32_t sa = sfa + 4 * k, sb = sfb + 4 * k * S::kBRowTiles + sb_off;
+                        mma_fp4_pair<kNv>(acc, ad + 2 * j, bd + 2 * j, !kNv && (j & 1) ? id2 : id0, sa, sb,
+                                          (ks | j) != 0);
+                    }
+                    mma_commit_pair(&empty[st]);
+                    if (ks + 1 == p.ksteps)
+                        mma_commit_pair(&acc_full[lt & 1]);
                 }
                 if (!ok) {
                     fail();
@@ -304,15 +315,15 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
         // that both accumulators use first
         constexpr int kChunks = BN / 32, kSharedChunks = S::kShared / 32;
         const int quad = warp & 3, half = warp >> 2;
-        const uint32_t bar = cluster_addr(acc_empty, 0);
+        const uint32_t bar0 = cluster_addr(&acc_empty[0], 0), bar1 = cluster_addr(&acc_empty[1], 0);
         uint8_t *out = sOut + warp * kTlStoreBytes;
         const float s_a = p.a_ts ? *p.a_ts : 1.0f, s_w = p.w_ts ? *p.w_ts : 1.0f;
         const bool scaled = p.a_ts || p.w_ts;
-        uint32_t lt = 0;
+        uint32_t lt = 0, stores = 0;
         for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
             int mp, nt;
             tile_at(t, p.mpairs, p.ntiles, mp, nt);
-            if (!mbar_wait_warp(acc_full, lt & 1)) {
+            if (!mbar_wait_warp(&acc_full[lt & 1], (lt >> 1) & 1)) {
                 fail();
                 break;
             }
@@ -329,12 +340,13 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                 tmem_ld32_finish(v);
                 if (i + 1 < kChunks / 2)
                     tmem_ld32_start(acc + (first + half + 2 * (i + 1)) % kChunks * 32, buf[(i + 1) & 1]);
-                if (half + 2 * i < kSharedChunks && half + 2 * i + 2 >= kSharedChunks) {
-                    // this warp's part of the shared columns is in registers
+                if (S::kShared ? half + 2 * i < kSharedChunks && half + 2 * i + 2 >= kSharedChunks
+                               : i + 1 == kChunks / 2) {
+                    // this warp's part of the shared columns (of all) is in registers
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive_cluster(bar);
+                        mbar_arrive_cluster(S::kShared || !(lt & 1) ? bar0 : bar1);
                 }
                 const int n0 = nt * BN + (first + half + 2 * i) % kChunks * 32;
                 if (m0 >= p.M || n0 >= p.N)
@@ -356,7 +368,8 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                             *reinterpret_cast<uint4 *>(at + lane * 128 + ((q ^ (lane & 7)) * 16)) =
                                 make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     } else {
-                        at += (i & 1) * (kTlStoreBytes / 2);
+                        // the other half may still be read by the store before
+                        at += (stores++ & 1) * (kTlStoreBytes / 2);
                         if (lane == 0)
                             bulk_wait_read<1>();
                         __syncwarp();
@@ -460,15 +473,39 @@ cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.after_quantise ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, w4a4_tile_kernel<kNv, BN>, ta, tb, tsa, tsb, ty, p);
+}
+
+// Width of the tiles: the one whose waves of pairs take least.  A stage of 256
+// elements of K takes 0.28 us at 256 columns (bound by the copies into shared
+// memory), 0.23 at 192 and 128 (by the issuing thread), a tile about 0.7 us
+// besides.  2048 x 3584 x 18944: 50.4 us in 112 tiles of 256, 39.6 in 152 of 192.
+template <bool kNv>
+cudaError_t run_widths(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    const int widths[3] = {256, 192, 128};
+    const double per_stage[3] = {0.28, 0.23, 0.23};
+    const int64_t ksteps = (a.K + 255) / 256, pairs = dev.num_sms / 2;
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < 3; i++) {
+        const int64_t tiles = ((a.M + 255) / 256) * ((a.N + widths[i] - 1) / widths[i]);
+        const double t = (double)((tiles + pairs - 1) / pairs) * (ksteps * per_stage[i] + 0.7);
+        if (i == 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    return best == 0 ? run_tile<kNv, 256>(a, s, dev) : best == 1 ? run_tile<kNv, 192>(a, s, dev)
+                                                                 : run_tile<kNv, 128>(a, s, dev);
 }
 
 }  // namespace
 
 cudaError_t launch_w4a4_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {
-    return a.nvfp4 ? run_tile<true, 256>(a, s, dev) : run_tile<false, 256>(a, s, dev);
+    return a.nvfp4 ? run_widths<true>(a, s, dev) : run_widths<false>(a, s, dev);
 }
 
 }  // namespace nvfp4

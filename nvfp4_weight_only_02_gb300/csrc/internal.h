@@ -116,6 +116,7 @@ struct MxQuantArgs {
     uint16_t *values;             // bf16, rows x cols
     uint8_t *codes_t, *scales_t;  // blocks along the columns, transposed
     uint16_t *values_t;           // bf16, rows x cols
+    bool overlap;                 // its launch overlaps the end of the kernel before it
 };
 cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
@@ -128,6 +129,9 @@ struct W4A4Args {
     bool nvfp4;                    // blocks of 16 with E4M3 scales (else 32, E8M0)
     const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
     const float *a_ts, *w_ts;      // tensor scales or null (1)
+    const void *x;                 // tokens to be quantised on the way (M x K, ldx) instead of a_codes, or null
+    bool x_fp32;
+    int64_t ldx;
     int64_t M, N, K;
     void *y;
     bool y_fp32;
@@ -135,7 +139,9 @@ struct W4A4Args {
     bool after_quantise;           // launched right behind the quantiser of A on the same stream
 };
 cudaError_t launch_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
-// Its variant for many tokens (csrc/gemm_w4a4_tile.cu).
+// Whether launch_w4a4 takes unquantised tokens (MXFP4) of these sizes.
+bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev);
+// The variant for many tokens (csrc/gemm_w4a4_tile.cu).
 cudaError_t launch_w4a4_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
 // Tiled scales (row_tiles x ktiles tiles of 512 bytes) as a tensor map whose
 // box is box_rows x box_k tiles, in that order in shared memory.

@@ -260,10 +260,10 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int abf)
            ((uint32_t)(M >> 4) << 24);
 }
 
-// True in one lane of a converged warp.  A warp that issues tcgen05 or TMA
-// instructions runs its loop with all lanes and elects one at the instruction:
-// the compiler then keeps descriptors in uniform registers, where a loop that
-// only lane 0 entered moves every operand there again for each instruction.
+// True in one lane of a converged warp.  Loops that issue tcgen05 or TMA
+// instructions are entered by the elected lane: the compiler then keeps
+// descriptors in uniform registers, where in a loop that `lane == 0` entered
+// it moves every operand there again for each instruction.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;

@@ -225,3 +225,58 @@ def test_refusals(nv):
     with pytest.raises(nv.NVFP4Error) as e:
         nv.mx_linear(torch.zeros(16, 80, dtype=torch.bfloat16, device="cuda")[:, 4:68], w)
     assert e.value.status == nv.ERR_ALIGNMENT
+
+
+LONG = [(70, 130, 4128), (129, 513, 8192), (300, 520, 18944), (1000, 1030, 4352), (260, 3584, 6144), (65, 4000, 16384)]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M,N,K", LONG)
+def test_long_contractions_of_few_tiles(nv, fmt, M, N, K):
+    a, a64, sa = _operand(nv, fmt, M, K, M + K)
+    w, w64, sw = _operand(nv, fmt, N, K, N + 3 * K)
+    y = nv.w4a4_gemm(a, w)
+    _check_product(y, a64, w64, sa * sw, K)
+    assert torch.equal(nv.w4a4_gemm(a, w, out_dtype=torch.bfloat16), y.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("K", [32, 96, 512])
+@pytest.mark.parametrize("M,N", [(2048, 8192), (5000, 5408), (300, 40000), (16384, 2312), (1111, 12345)])
+def test_many_tiles_of_short_contractions(nv, M, N, K):
+    """Tiles that follow one another quickly: every element of both output types against the definition, in FP64 on
+    the device (the operands' values come from the dequantiser, which has its own test)."""
+    g = torch.Generator("cuda").manual_seed(M)
+    a = nv.mx_quantize(torch.randn(M, K, device="cuda", generator=g)).row
+    w = nv.mx_quantize(torch.randn(N, K, device="cuda", generator=g)).row
+    a64, w64 = a.dequantize().double(), w.dequantize().double()
+    want, bound = a64 @ w64.t(), (K + 64) * 2.0 ** -23 * (a64.abs() @ w64.abs().t()) + 1e-38
+    y = nv.w4a4_gemm(a, w)
+    assert ((y.double() - want).abs() <= bound).all()
+    assert torch.equal(nv.w4a4_gemm(a, w, out_dtype=torch.bfloat16), y.bfloat16())
+
+
+def test_one_workspace_for_calls_of_all_sizes(nv):
+    """The counters are at zero after every call, whatever its size, and results do not depend on the calls before."""
+    sizes = [(300, 520, 18944), (3, 512, 4096), (129, 513, 8192), (64, 256, 512), (700, 700, 704), (1, 128, 8192)]
+    g = torch.Generator().manual_seed(2)
+    xs = [torch.randn(m, k, generator=g).bfloat16().cuda() for m, n, k in sizes]
+    ws_ = [nv.mx_quantize(torch.randn(n, k, generator=g).cuda()).row for m, n, k in sizes]
+    alone = [nv.mx_linear(x, w) for x, w in zip(xs, ws_)]
+    ws = nv.new_workspace(max(nv.nvfp4_mx_linear_workspace_bytes(*s) for s in sizes))
+    for r in range(6):
+        for i in (range(6) if r % 2 else reversed(range(6))):
+            assert torch.equal(nv.mx_linear(xs[i], ws_[i], workspace=ws), alone[i])
+            assert not ws[:256 + 4 * 8192].any()
+    assert nv.nvfp4_get_device_status(ws) == nv.OK
+
+
+def test_large_product(nv):
+    """2048 x 3584 x 18944 on sampled rows and columns."""
+    M, N, K = 2048, 3584, 18944
+    a, a64, sa = _operand(nv, "nv", M, K, 1)
+    w, w64, sw = _operand(nv, "nv", N, K, 2)
+    y = nv.w4a4_gemm(a, w)
+    rows = np.random.default_rng(0).choice(M, 200, replace=False)
+    cols = np.random.default_rng(1).choice(N, 300, replace=False)
+    _check_product(y[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()], a64[rows], w64[cols], sa * sw, K)
+    assert torch.equal(y, nv.w4a4_gemm(a, w))
