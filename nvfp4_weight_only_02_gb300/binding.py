@@ -523,7 +523,7 @@ class _Fp4Operand:
         cols = 2 * half
         # tiles of 128 rows x 4 blocks, 512 bytes each
         tiles = (rows + 127) // 128 * ((cols // self.block + 3) // 4)
-        if cols % self.block or rows == 0 or cols == 0 or tuple(scales.shape) != (512 * tiles,):
+        if cols % self.block or tiles == 0 or scales.dim() != 1 or scales.numel() != 512 * tiles:
             raise ValueError(f"scales must hold {512 * tiles} bytes in one dimension, and codes whole blocks of "
                              f"{self.block}")
         if tensor_scale is not None:
@@ -553,6 +553,13 @@ class MxOperand(_Fp4Operand):
 
     def __init__(self, codes, scales):
         super().__init__(codes, scales)
+
+    @classmethod
+    def _made(cls, codes, scales, rows, cols):
+        """Of buffers allocated here, whose checks would only take time."""
+        op = cls.__new__(cls)
+        op.codes, op.scales, op.tensor_scale, op.rows, op.cols = codes, scales, None, rows, cols
+        return op
 
     def dequantize(self, dtype=torch.float32):
         out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
@@ -589,6 +596,7 @@ def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values
     rows, cols, ld, dt = _matrix(x, "x")
     dev = x.device
     q = qs = qt = qts = v = vt = None
+    rows32 = (rows + 31) // 32 * 32
     if rowwise:
         if codes:
             q = torch.empty((rows, cols // 2), dtype=_U8, device=dev)
@@ -597,13 +605,14 @@ def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values
             v = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
     if colwise:
         if codes:
-            qt = torch.empty((cols, (rows + 31) // 32 * 16), dtype=_U8, device=dev)
+            qt = torch.empty((cols, rows32 // 2), dtype=_U8, device=dev)
             qts = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=_U8, device=dev)
         if values:
             vt = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
     _call("nvfp4_mx_quantize", x.data_ptr(), dt, rows, cols, ld, _addr(q), _addr(qs), _addr(v), _addr(qt), _addr(qts),
           _addr(vt), _raw_stream())
-    return MxQuantized(None if q is None else MxOperand(q, qs), None if qt is None else MxOperand(qt, qts), v, vt)
+    return MxQuantized(None if q is None else MxOperand._made(q, qs, rows, cols),
+                       None if qt is None else MxOperand._made(qt, qts, cols, rows32), v, vt)
 
 
 def nvfp4_w4a4_workspace_bytes(M: int, N: int, K: int) -> int:

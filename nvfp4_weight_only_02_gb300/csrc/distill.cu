@@ -1053,8 +1053,7 @@ cudaError_t run_distill_stream(const DistillArgs &a, int slots, cudaStream_t s, 
 {
     const size_t bits = a.tail ? (size_t)(a.V + (int64_t)(16 / sizeof(T)) + 31) / 32 * 4 : 0;
     const size_t smem = (size_t)slots * kDtChunk + bits;
-    cudaError_t e = cudaFuncSetAttribute(distill_stream_kernel<T, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    cudaError_t e = allow_smem<distill_stream_kernel<T, kGrad>>(kDtSmem, dev);
     if (e != cudaSuccess)
         return e;
     distill_stream_kernel<T, kGrad><<<(unsigned)std::min<int64_t>(a.T, kDtPerSm * dev.num_sms), kDtThreads, smem, s>>>(a, slots);
@@ -1075,8 +1074,7 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
     constexpr int NE = Vec<T>::N;
     const int64_t L = ((a.V + C - 1) / C + NE - 1) / NE * NE;
     const size_t smem = (size_t)L * sizeof(T) + 32;
-    cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, kGrad, kEntries>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kDistillMaxSlice + 32);
+    cudaError_t e = allow_smem<distill_kernel<T, kGrad, kEntries>>(kDistillMaxSlice + 32, dev);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

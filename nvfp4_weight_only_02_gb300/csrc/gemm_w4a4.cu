@@ -263,16 +263,9 @@ __global__ void __launch_bounds__(kWsThreads, 2)
                     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
                     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
                     const uint32_t byte = e8m0_of(a);
-                    uint32_t q = 0u;
-                    if (byte != 255u) {
-                        float v[8];
-                        raw[u].floats(v);
-                        const float inv = e8m0_inverse(byte);
-#pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            v[e] = __fmul_rn(v[e], inv);
-                        q = e2m1_encode8(v);
-                    }
+                    float v[8];
+                    raw[u].floats(v);
+                    const uint32_t q = byte != 255u ? e2m1_encode8_scaled(v, e8m0_inverse(byte)) : 0u;
                     if (i < items) {
                         const int ks = g / (kWsK / 8), kb = g % (kWsK / 8) * 4;   // stage, byte of its row
                         *reinterpret_cast<uint32_t *>(sX + ks * NT * 128 + m * 128 + (((kb >> 4) ^ (m & 7)) << 4) +
@@ -402,7 +395,7 @@ cudaError_t run_stream(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
     p.y = a.y;
     p.y_fp32 = a.y_fp32 ? 1 : 0;
     p.ctl = a.ctl;
-    e = cudaFuncSetAttribute(w4a4_stream_kernel<kNv, NT, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWsSmem);
+    e = allow_smem<w4a4_stream_kernel<kNv, NT, kTok>>(kWsSmem, dev);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -52,10 +52,9 @@ struct TlShape {
     static constexpr size_t kSmem = kFixed + (size_t)kStages * kStageBytes;
     static constexpr int kSfA = kTiles * 4, kSfB = kTiles * kBRowTiles * 4, kSf = kSfA + kSfB;
     static constexpr int kTmemCols = 512;
-    // columns: accumulator 0 at 0, accumulator 1 at BN - kShared, then the scales of kSfBufs stages.  An MMA's
-    // completion is known about 800 cycles after its issue, 1.5 stages' worth of MMAs at 256 columns: with two
-    // stages' scales in TMEM every stage took 640 cycles whatever its width.
-    static constexpr int kSfBufs = kNv ? 3 : 4;
+    // columns: accumulator 0 at 0, accumulator 1 at BN - kShared, then two stages' scales (more would take
+    // columns from the accumulators: 343 us instead of 334 at 16384 x 18944 x 3584)
+    static constexpr int kSfBufs = 2;
     static constexpr int kOver = 2 * BN + kSfBufs * kSf - kTmemCols;
     static constexpr int kShared = kOver > 64 ? (kOver + 31) / 32 * 32 : kOver > 0 ? 64 : 0;
     static constexpr int kAcc1 = BN - kShared, kSfCol = 2 * BN - kShared;
@@ -447,8 +446,7 @@ cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
                                              a.y_fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)
                       : (ty = ta, cudaSuccess);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(w4a4_tile_kernel<kNv, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)S::kSmem);
+        e = allow_smem<w4a4_tile_kernel<kNv, BN>>(S::kSmem, dev);
     if (e != cudaSuccess)
         return e;
     TileParams p;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/nvfp4.h"
 
 namespace nvfp4 {
@@ -17,6 +19,21 @@ struct DeviceInfo {
     int fused_quant_blocks = 0;            // grid of the fused dynamic quantiser (0: unavailable)
     bool stream_ok = false;                // the streaming decode kernel fits on this device
 };
+
+// Lets a kernel take `bytes` of dynamic shared memory (always the same number
+// for a kernel): a call once per kernel and device.
+template <auto kKernel>
+inline cudaError_t allow_smem(size_t bytes, const DeviceInfo &dev)
+{
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << dev.device;
+    if (done.load(std::memory_order_relaxed) & bit)
+        return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Cached per-device facts; nullptr (and *st set) when the device is unusable.
 const DeviceInfo *device_info(nvfp4_status *st);
@@ -118,7 +135,7 @@ struct MxQuantArgs {
     uint16_t *values_t;           // bf16, rows x cols
     bool overlap;                 // its launch overlaps the end of the kernel before it
 };
-cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s);
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev);
 cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
                                  bool fp32, cudaStream_t s, const DeviceInfo &dev);
 cudaError_t launch_tile_scales(const uint8_t *in, int64_t rows, int64_t nb, uint8_t *out, cudaStream_t s,

@@ -32,25 +32,32 @@ __device__ __forceinline__ float2 pair_floats(uint32_t v)
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 __device__ __forceinline__ float2 pair_floats(float2 v) { return v; }
-__device__ __forceinline__ void pair_amax(uint32_t v, uint32_t &m0, uint32_t &m1)
-{
-    m0 = max(m0, (v << 16) & 0x7FFFFFFFu);
-    m1 = max(m1, v & 0x7FFF0000u);
-}
-__device__ __forceinline__ void pair_amax(float2 v, uint32_t &m0, uint32_t &m1)
-{
-    m0 = max(m0, __float_as_uint(v.x) & 0x7FFFFFFFu);
-    m1 = max(m1, __float_as_uint(v.y) & 0x7FFFFFFFu);
-}
+// Running largest magnitudes of the two columns, and their bits as FP32 in the end.
+struct PairMax16 {
+    uint32_t m = 0u;
+    __device__ __forceinline__ void add(uint32_t v) { m = __vmaxu2(m, v & 0x7FFF7FFFu); }
+    __device__ __forceinline__ uint2 bits() const { return make_uint2(m << 16, m & 0xFFFF0000u); }
+};
+struct PairMax32 {
+    uint2 m = {0u, 0u};
+    __device__ __forceinline__ void add(float2 v)
+    {
+        m.x = max(m.x, __float_as_uint(v.x) & 0x7FFFFFFFu);
+        m.y = max(m.y, __float_as_uint(v.y) & 0x7FFFFFFFu);
+    }
+    __device__ __forceinline__ uint2 bits() const { return m; }
+};
 template <typename T>
 struct PairOf;
 template <>
 struct PairOf<__nv_bfloat16> {
     using type = uint32_t;
+    using amax = PairMax16;
 };
 template <>
 struct PairOf<float> {
     using type = float2;
+    using amax = PairMax32;
 };
 
 // One 128 x 128 tile per block, read once.  Row direction: four lanes hold a
@@ -105,14 +112,7 @@ __global__ void __launch_bounds__(kMqThreads)
             if (cok && r < rows) {
                 float v[8];
                 raw[i].floats(v);
-                uint32_t q = 0u;
-                if (byte != 255u) {
-                    const float inv = e8m0_inverse(byte);
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        v[e] = __fmul_rn(v[e], inv);
-                    q = e2m1_encode8(v);
-                }
+                const uint32_t q = byte != 255u ? e2m1_encode8_scaled(v, e8m0_inverse(byte)) : 0u;
                 if (codes)
                     *reinterpret_cast<uint32_t *>(codes + r * (cols / 2) + (c0 + c8) / 2) = q;
                 if (values)
@@ -132,13 +132,13 @@ __global__ void __launch_bounds__(kMqThreads)
     if (r0 + rb * 32 < rows && c0 + c < cols) {
         using P = typename PairOf<T>::type;
         P v[32];
-        uint32_t m0 = 0u, m1 = 0u;
+        typename PairOf<T>::amax amax;
 #pragma unroll
         for (int i = 0; i < 32; i++) {
             v[i] = *reinterpret_cast<const P *>(s_tile + (rb * 32 + i) * kMqTile + c);
-            pair_amax(v[i], m0, m1);
+            amax.add(v[i]);
         }
-        const uint32_t b0 = e8m0_of(m0), b1 = e8m0_of(m1);
+        const uint32_t b0 = e8m0_of(amax.bits().x), b1 = e8m0_of(amax.bits().y);
         s_sct[(c & 31) * 16 + (c >> 5) * 4 + rb] = (uint8_t)b0;
         s_sct[((c + 1) & 31) * 16 + (c >> 5) * 4 + rb] = (uint8_t)b1;
         const float i0 = b0 == 255u ? 0.0f : e8m0_inverse(b0), i1 = b1 == 255u ? 0.0f : e8m0_inverse(b1);
@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(kMqThreads)
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const float2 f = pair_floats(v[8 * g + e]);
-                f0[e] = __fmul_rn(f.x, i0);
-                f1[e] = __fmul_rn(f.y, i1);
+                f0[e] = f.x;
+                f1[e] = f.y;
             }
-            q0[g] = b0 == 255u ? 0u : e2m1_encode8(f0);
-            q1[g] = b1 == 255u ? 0u : e2m1_encode8(f1);
+            q0[g] = b0 == 255u ? 0u : e2m1_encode8_scaled(f0, i0);
+            q1[g] = b1 == 255u ? 0u : e2m1_encode8_scaled(f1, i1);
         }
         if (codes_t) {
             uint8_t *dst = codes_t + (c0 + c) * (rows32 / 2) + (r0 + rb * 32) / 2;
@@ -235,13 +235,12 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t *__restr
 }
 
 template <typename T, bool kRow, bool kCol>
-cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s)
+cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
     const int64_t tiles = ((a.rows + kMqTile - 1) / kMqTile) * ((a.cols + kMqTile - 1) / kMqTile);
     const size_t smem = kCol ? sizeof(T) * kMqTile * kMqTile : 0;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(mx_quantize_kernel<T, kRow, kCol>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_smem<mx_quantize_kernel<T, kRow, kCol>>(smem, dev);
         if (e != cudaSuccess)
             return e;
     }
@@ -260,12 +259,12 @@ cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s)
 }
 
 template <typename T>
-cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s)
+cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
     const bool row = a.codes || a.values, col = a.codes_t || a.values_t;
-    return row && col ? run_quantize<T, true, true>(a, s)
-           : row      ? run_quantize<T, true, false>(a, s)
-                      : run_quantize<T, false, true>(a, s);
+    return row && col ? run_quantize<T, true, true>(a, s, dev)
+           : row      ? run_quantize<T, true, false>(a, s, dev)
+                      : run_quantize<T, false, true>(a, s, dev);
 }
 
 unsigned grid_for(int64_t n, const DeviceInfo &dev)
@@ -276,9 +275,9 @@ unsigned grid_for(int64_t n, const DeviceInfo &dev)
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s)
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
-    return a.x_fp32 ? run_quantize_dirs<float>(a, s) : run_quantize_dirs<__nv_bfloat16>(a, s);
+    return a.x_fp32 ? run_quantize_dirs<float>(a, s, dev) : run_quantize_dirs<__nv_bfloat16>(a, s, dev);
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
