@@ -487,12 +487,14 @@ def _call(name, *args):
 
 def _matrix(t, name):
     """Checks a 2-D CUDA matrix whose rows are contiguous; returns (rows, cols, row stride in elements, type code)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    code = _out_code(t.dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    rows, cols = t.shape
+    code = _DTYPE_CODE.get(t.dtype)
+    shape = t.shape
+    if code is None or not t.is_cuda or len(shape) != 2:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _out_code(t.dtype, name)
+        raise ValueError(f"{name} must have 2 dimensions, got {len(shape)}")
+    rows, cols = shape
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
@@ -682,15 +684,22 @@ def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, d
 
 
 # ------------------------------------------------------------------ distillation
+_INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
 def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, loss, dz, workspace):
     """The C entry point on tensors; loss or dz may be None (see include/nvfp4.h)."""
     T, V, ldz, zdt = _matrix(z, "z")
     tdt = _out_code(teacher.dtype, "teacher")
-    if index.dtype not in (torch.int32, torch.int64) or index.dim() != 2:
+    ib = _INDEX_BYTES.get(index.dtype)
+    shape = index.shape
+    if ib is None or len(shape) != 2:
         raise ValueError("index must be a 2-dimensional int32 or int64 tensor")
-    k = index.shape[1]
-    _need(index, index.dtype, (T, k), "index")
-    _need(teacher, teacher.dtype, (T, k), "teacher")
+    k = shape[1]
+    if shape[0] != T or teacher.shape != shape or not (index.is_cuda and teacher.is_cuda) or \
+            not (index.is_contiguous() and teacher.is_contiguous()):
+        raise ValueError(f"index and teacher must be contiguous CUDA tensors of one shape ({T}, k), got "
+                         f"{tuple(shape)} and {tuple(teacher.shape)}")
     if row_weight is not None:
         _need(row_weight, _F32, (T,), "row_weight")
     ng = 0
@@ -704,10 +713,9 @@ def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_lo
         rows, cols, lddz, ddt = _matrix(dz, "dz")
         if ddt != zdt or rows != T or cols != V:
             raise ValueError("dz must have z's type and shape")
-    nws = 0 if workspace is None else workspace.numel()
-    _call("nvfp4_distill_topk", z.data_ptr(), zdt, T, V, ldz, index.data_ptr(), index.element_size(),
-          teacher.data_ptr(), tdt, k, temperature, 1 if tail else 0, _addr(row_weight), _addr(grad_loss), ng,
-          _addr(loss), _addr(dz), lddz, _addr(workspace), nws, _raw_stream())
+    _call("nvfp4_distill_topk", z.data_ptr(), zdt, T, V, ldz, index.data_ptr(), ib, teacher.data_ptr(), tdt, k,
+          temperature, 1 if tail else 0, _addr(row_weight), _addr(grad_loss), ng, _addr(loss), _addr(dz), lddz,
+          _addr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream())
 
 
 def distill_topk_loss(z, index, teacher, temperature=1.0, tail=False, row_weight=None, workspace=None):
@@ -724,7 +732,7 @@ def distill_topk_loss_grad(z, index, teacher, temperature=1.0, tail=False, row_w
     """(loss (T,), dz (T, V)) in one pass over z; dz = grad_loss (T values, one, or None for 1) times d loss / d z.
     out: where dz goes (z itself for an update in place)."""
     loss = torch.empty(z.shape[0], dtype=torch.float32, device=z.device)
-    dz = out if out is not None else torch.empty(z.shape, dtype=z.dtype, device=z.device)
+    dz = out if out is not None else torch.empty_like(z, memory_format=torch.contiguous_format)
     nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, loss, dz, workspace)
     return loss, dz
 
@@ -732,6 +740,6 @@ def distill_topk_loss_grad(z, index, teacher, temperature=1.0, tail=False, row_w
 def distill_topk_grad(z, index, teacher, grad_loss=None, temperature=1.0, tail=False, row_weight=None, out=None,
                       workspace=None):
     """dz alone, for a backward pass whose incoming gradient was not known with the loss."""
-    dz = out if out is not None else torch.empty(z.shape, dtype=z.dtype, device=z.device)
+    dz = out if out is not None else torch.empty_like(z, memory_format=torch.contiguous_format)
     nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, None, dz, workspace)
     return dz
