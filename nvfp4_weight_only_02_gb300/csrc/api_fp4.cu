@@ -35,7 +35,7 @@ size_t code_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (size_t)(c
 // tiles of 128 x 128 in one launch
 bool tiles_ok(int64_t rows, int64_t cols)
 {
-    return ((rows + 127) / 128) * ((cols + 127) / 128) <= (1LL << 30);
+    return ((rows + 127) / 128) * ((cols + 127) / 128) <= (1LL << 29);
 }
 
 nvfp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
@@ -102,6 +102,7 @@ nvfp4_status nvfp4_mx_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows,
         !opt_aligned(values_bf16) || !opt_aligned(codes_t) || !opt_aligned(scales_t) || !opt_aligned(values_t_bf16))
         return NVFP4_ERR_ALIGNMENT;
     NVFP4_TRY_DEVICE(dev);
+    (void)dev;
     MxQuantArgs a = quant_args(x, x_dtype, rows, cols, ld);
     a.codes = codes;
     a.scales = scales;
@@ -109,7 +110,7 @@ nvfp4_status nvfp4_mx_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows,
     a.codes_t = codes_t;
     a.scales_t = scales_t;
     a.values_t = (uint16_t *)values_t_bf16;
-    return from_cuda(launch_mx_quantize(a, (cudaStream_t)stream, *dev));
+    return from_cuda(launch_mx_quantize(a, (cudaStream_t)stream));
 }
 
 nvfp4_status nvfp4_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
@@ -201,7 +202,7 @@ nvfp4_status nvfp4_mx_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, in
         // behind a product that streams weights the quantiser may start early (16 tokens: 10.9 us a call and
         // 12.4 without, N = 18944, K = 3584); the tile kernel then starts late (1024 tokens: 34.9 and 31.6)
         q.overlap = M <= 64;
-        const cudaError_t e = launch_mx_quantize(q, (cudaStream_t)stream, *dev);
+        const cudaError_t e = launch_mx_quantize(q, (cudaStream_t)stream);
         if (e != cudaSuccess)
             return NVFP4_ERR_CUDA;
         a.a_codes = q.codes;
@@ -262,7 +263,7 @@ nvfp4_status nvfp4_mx_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int6
         q.codes_t = codes_t;
         q.scales_t = scales_t;
     }
-    cudaError_t e = launch_mx_quantize(q, s, *dev);
+    cudaError_t e = launch_mx_quantize(q, s);
     W4A4Args a = {};
     a.ctl = (uint32_t *)workspace;
     a.after_quantise = true;

@@ -262,10 +262,8 @@ __global__ void __launch_bounds__(kWsThreads, 2)
                     uint32_t a = raw[u].amax_bits();
                     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
                     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                    const uint32_t byte = e8m0_of(a);
-                    float v[8];
-                    raw[u].floats(v);
-                    const uint32_t q = byte != 255u ? e2m1_encode8_scaled(v, e8m0_inverse(byte)) : 0u;
+                    uint32_t byte;
+                    const uint32_t q = raw[u].encode(a, byte);
                     if (i < items) {
                         const int ks = g / (kWsK / 8), kb = g % (kWsK / 8) * 4;   // stage, byte of its row
                         *reinterpret_cast<uint32_t *>(sX + ks * NT * 128 + m * 128 + (((kb >> 4) ^ (m & 7)) << 4) +
@@ -444,7 +442,8 @@ bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev)
     // 8: 11.9 and 11.2, since every CTA quantises them again
     if (M > 4)
         return false;
-    const int64_t ksteps = (K + kWsK - 1) / kWsK, split = split_for((N + kWsRows - 1) / kWsRows, K, dev), nk = (ksteps + split - 1) / split;
+    const int64_t ksteps = (K + kWsK - 1) / kWsK, split = split_for((N + kWsRows - 1) / kWsRows, K, dev);
+    const int64_t nk = (ksteps + split - 1) / split;
     // at least three stages of weights beside the tokens
     return nk <= 64 && WsShape<false, 16, kBf16>::stages((int)nk) >= std::min<int64_t>(3, std::max<int64_t>(nk, 2));
 }

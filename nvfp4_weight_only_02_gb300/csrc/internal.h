@@ -135,7 +135,7 @@ struct MxQuantArgs {
     uint16_t *values_t;           // bf16, rows x cols
     bool overlap;                 // its launch overlaps the end of the kernel before it
 };
-cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
                                  bool fp32, cudaStream_t s, const DeviceInfo &dev);
 cudaError_t launch_tile_scales(const uint8_t *in, int64_t rows, int64_t nb, uint8_t *out, cudaStream_t s,

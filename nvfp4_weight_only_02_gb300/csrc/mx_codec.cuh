@@ -83,8 +83,8 @@ template <>
 struct Raw8<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = ld_stream_u4(p); }
+    __device__ __forceinline__ void store_shared(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
     __device__ __forceinline__ void floats(float (&v)[8]) const
     {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -93,6 +93,25 @@ struct Raw8<__nv_bfloat16> {
             v[2 * i] = __uint_as_float(w[i] << 16);
             v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
+    }
+    // Codes under the scale that the block's largest magnitude gives; its byte
+    __device__ __forceinline__ uint32_t encode(uint32_t amax, uint32_t &byte) const
+    {
+        byte = e8m0_of(amax);
+        // 2^(127 - byte) twice; the products are exact (or far below the smallest code)
+        const uint32_t f = (254u - byte) * 0x00800080u;
+        const __nv_bfloat162 ff = *reinterpret_cast<const __nv_bfloat162 *>(&f);
+        const uint4 u = make_uint4(mul(a.x, ff), mul(a.y, ff), mul(a.z, ff), mul(a.w, ff));
+        Raw8 scaled;
+        scaled.a = u;
+        float v[8];
+        scaled.floats(v);
+        return byte == 255u ? 0u : e2m1_encode8(v);
+    }
+    static __device__ __forceinline__ uint32_t mul(uint32_t x, __nv_bfloat162 f)
+    {
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), f);
+        return *reinterpret_cast<const uint32_t *>(&y);
     }
     __device__ __forceinline__ uint32_t amax_bits() const
     {
@@ -109,18 +128,25 @@ struct Raw8<float> {
         a = ld_stream_u4(p);
         b = ld_stream_u4(p + 4);
     }
-    __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void store(float *p) const
+    __device__ __forceinline__ void store_shared(float *p) const
     {
         reinterpret_cast<uint4 *>(p)[0] = a;
         reinterpret_cast<uint4 *>(p)[1] = b;
     }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void floats(float (&v)[8]) const
     {
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 8; i++)
             v[i] = __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ uint32_t encode(uint32_t amax, uint32_t &byte) const
+    {
+        byte = e8m0_of(amax);
+        float v[8];
+        floats(v);
+        return byte == 255u ? 0u : e2m1_encode8_scaled(v, e8m0_inverse(byte));
     }
     __device__ __forceinline__ uint32_t amax_bits() const
     {

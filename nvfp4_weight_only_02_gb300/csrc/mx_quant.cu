@@ -23,167 +23,208 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kMqTile = 128;     // rows and columns of a block's tile: one scale tile in each direction
+constexpr int kMqRows = 128;      // rows of a tile
+
+// What depends on the input's type.  A tile is 128 rows of 256 bytes: 128 bf16
+// columns (one scale tile in each direction) or 64 FP32 ones (half of one).  In
+// the column direction a thread takes kPer neighbouring columns of 32 rows.
+template <typename T>
+struct MqShape;
+template <>
+struct MqShape<__nv_bfloat16> {
+    static constexpr int kCols = 128, kPer = 2;
+    using Word = uint32_t;       // kPer columns of a row
+    uint32_t m = 0u;             // running largest magnitudes
+    __device__ __forceinline__ void add(uint32_t v) { m = __vmaxu2(m, v & 0x7FFF7FFFu); }
+    __device__ __forceinline__ uint32_t amax_bits(int i) const { return i ? m & 0xFFFF0000u : m << 16; }
+    static __device__ __forceinline__ float value(uint32_t v, int i)
+    {
+        return __uint_as_float(i ? v & 0xFFFF0000u : v << 16);
+    }
+};
+template <>
+struct MqShape<float> {
+    static constexpr int kCols = 64, kPer = 1;
+    using Word = float;
+    uint32_t m = 0u;
+    __device__ __forceinline__ void add(float v) { m = max(m, __float_as_uint(v) & 0x7FFFFFFFu); }
+    __device__ __forceinline__ uint32_t amax_bits(int) const { return m; }
+    static __device__ __forceinline__ float value(float v, int) { return v; }
+};
+
+struct MqParams {
+    int64_t rows, cols;
+    int64_t ctiles;   // tiles along a row
+    uint8_t *codes, *scales, *codes_t, *scales_t;
+    uint16_t *values, *values_t;
+};
+
+// One read of x for both directions, a tile a CTA: 16 bytes a thread and row
+// at a time, all of them on their way before the first is used.  Row direction,
+// from registers: four lanes hold a block of 32 (eight elements each), so codes
+// and values are coalesced.  Column direction: the tile goes through shared
+// memory, a thread takes its columns of a 32-row block; the codes return there
+// too and leave as 64 contiguous bytes a column.  Rows and columns outside the
+// matrix are zeros, so padding bytes of the scale tiles come out as 0 by
+// themselves.
+//
+// What bounds it: 2 (4) bytes read and 17/32 written an element and direction.
+// 16384 x 3584 bf16: rows alone 23.2 us (6.4 TB/s, 94 % of the copy rate), with
+// values 41.9 us (94 %); columns alone 30.1 us (73 %); both 37.8 us (70 %), with
+// values 65.9 us (93 %).  8192 x 3584 FP32, both: 32.0 us (68 %).  The column
+// direction is bound by issue: about 15 instructions an element over both.
+// Measured against it, both directions: codes straight from the column pass's
+// registers, 16 bytes a column, 40.9 us; a persistent CTA with tiles brought by
+// TMA 41.5 us (rows 26.2); registers capped for five CTAs an SM 44.5 us.
 constexpr int kMqThreads = 256;
 
-// Two neighbouring columns of one row.
-__device__ __forceinline__ float2 pair_floats(uint32_t v)
-{
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
-__device__ __forceinline__ float2 pair_floats(float2 v) { return v; }
-// Running largest magnitudes of the two columns, and their bits as FP32 in the end.
-struct PairMax16 {
-    uint32_t m = 0u;
-    __device__ __forceinline__ void add(uint32_t v) { m = __vmaxu2(m, v & 0x7FFF7FFFu); }
-    __device__ __forceinline__ uint2 bits() const { return make_uint2(m << 16, m & 0xFFFF0000u); }
-};
-struct PairMax32 {
-    uint2 m = {0u, 0u};
-    __device__ __forceinline__ void add(float2 v)
-    {
-        m.x = max(m.x, __float_as_uint(v.x) & 0x7FFFFFFFu);
-        m.y = max(m.y, __float_as_uint(v.y) & 0x7FFFFFFFu);
-    }
-    __device__ __forceinline__ uint2 bits() const { return m; }
-};
-template <typename T>
-struct PairOf;
-template <>
-struct PairOf<__nv_bfloat16> {
-    using type = uint32_t;
-    using amax = PairMax16;
-};
-template <>
-struct PairOf<float> {
-    using type = float2;
-    using amax = PairMax32;
-};
-
-// One 128 x 128 tile per block, read once.  Row direction: four lanes hold a
-// block of 32 (16 bytes of input each), so loads, codes and values are
-// coalesced.  Column direction: the tile goes through shared memory and a
-// thread takes two neighbouring columns of a 32-row block.  Memory bound: at
-// bf16 input it reads 2 bytes and writes 17/32 bytes an element and direction.
 template <typename T, bool kRow, bool kCol>
 __global__ void __launch_bounds__(kMqThreads)
-    mx_quantize_kernel(const T *__restrict__ x, int64_t rows, int64_t cols, int64_t ld, uint8_t *__restrict__ codes,
-                       uint8_t *__restrict__ scales, uint16_t *__restrict__ values, uint8_t *__restrict__ codes_t,
-                       uint8_t *__restrict__ scales_t, uint16_t *__restrict__ values_t)
+    mx_quantize_kernel(const T *__restrict__ x, const int64_t ld, const MqParams p)
 {
-    extern __shared__ __align__(16) uint8_t s_tile_raw[];
-    __shared__ __align__(16) uint8_t s_sc[512], s_sct[512];
-    T *s_tile = reinterpret_cast<T *>(s_tile_raw);
+    using S = MqShape<T>;
+    constexpr int kCols = S::kCols, kPer = S::kPer, kGroups = kCols / 32;   // 32-column groups of a tile
+    constexpr int kLanes = kCols / 8, kStep = kMqThreads / kLanes;          // lanes to a row, rows at a time
+    constexpr int kIter = kMqRows / kStep;
+    __shared__ __align__(16) T tile[kCol ? kMqRows * kCols : 1];
+    __shared__ uint32_t s_sc[kMqRows], s_sct[kCols];   // the tile's scale bytes, a word a row (column)
+    __shared__ uint4 s_q[kCol ? kCols * 5 : 1];        // the tile's codes in the column direction, 80 bytes a column
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t rows = p.rows, cols = p.cols, rows32 = (rows + 31) / 32 * 32;
+    const int64_t rtiles = (rows + kMqRows - 1) / kMqRows, ktiles = (cols + 127) / 128;
+    const int64_t rt = blockIdx.x / p.ctiles, ct = blockIdx.x % p.ctiles, r0 = rt * kMqRows, c0 = ct * kCols;
+    const int left = (int)min(rows - r0, (int64_t)kMqRows);                 // rows of the tile that exist
     // A product launched behind this kernel starts its weight copies as soon as
     // every block is here; by then all kernels before this one are complete.
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t ctiles = (cols + kMqTile - 1) / kMqTile, rtiles = (rows + kMqTile - 1) / kMqTile;
-    const int64_t rt = blockIdx.x / ctiles, ct = blockIdx.x % ctiles;
-    const int64_t r0 = rt * kMqTile, c0 = ct * kMqTile;
-    if (kCol && tid < 128)
-        reinterpret_cast<uint32_t *>(s_sct)[tid] = 0u;
 
-    const int lr = warp * 2 + (lane >> 4), c8 = (lane & 15) * 8;
+    const int lr = tid / kLanes, c8 = tid % kLanes * 8;
     const bool cok = c0 + c8 < cols;
-    Raw8<T> raw[8];
+    Raw8<T> raw[kIter];
+    const T *src = x + (r0 + lr) * ld + c0 + c8;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int64_t r = r0 + i * 16 + lr;
-        if (cok && r < rows)
-            raw[i].load(x + r * ld + c0 + c8);
-        else
-            raw[i].zero();
+    for (int i = 0; i < kIter; i++) {
+        raw[i].zero();
+        if (cok && i * kStep + lr < left)
+            raw[i].load(src + (int64_t)(i * kStep) * ld);
     }
+    if (kCol) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int rl = i * 16 + lr;
-        const int64_t r = r0 + rl;
-        if (kCol)
-            raw[i].store(s_tile + rl * kMqTile + c8);
-        if (kRow) {
+        for (int i = 0; i < kIter; i++)
+            raw[i].store_shared(tile + (i * kStep + lr) * kCols + c8);
+    }
+    if (kRow) {
+        const int64_t at = (r0 + lr) * cols + c0 + c8, step = kStep * cols;
+        uint8_t *code = p.codes + at / 2;
+        uint16_t *value = p.values + at;
+#pragma unroll
+        for (int i = 0; i < kIter; i++) {
+            const int rl = i * kStep + lr;
             uint32_t m = raw[i].amax_bits();
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint32_t byte = e8m0_of(m);
+            uint32_t byte;
+            const uint32_t q = raw[i].encode(m, byte);
             if ((lane & 3) == 0)
-                s_sc[(rl & 31) * 16 + (rl >> 5) * 4 + (c8 >> 5)] = (uint8_t)byte;
-            if (cok && r < rows) {
-                float v[8];
-                raw[i].floats(v);
-                const uint32_t q = byte != 255u ? e2m1_encode8_scaled(v, e8m0_inverse(byte)) : 0u;
-                if (codes)
-                    *reinterpret_cast<uint32_t *>(codes + r * (cols / 2) + (c0 + c8) / 2) = q;
-                if (values)
-                    *reinterpret_cast<uint4 *>(values + r * cols + c0 + c8) = decode8_bf16(q, e8m0_scale(byte));
+                reinterpret_cast<uint8_t *>(&s_sc[rl])[c8 >> 5] = (uint8_t)byte;
+            if (cok && rl < left) {
+                if (p.codes)
+                    *reinterpret_cast<uint32_t *>(code) = q;
+                if (p.values)
+                    *reinterpret_cast<uint4 *>(value) = decode8_bf16(q, e8m0_scale(byte));
             }
+            code += step / 2;
+            value += step;
         }
     }
-    __syncthreads();
-    if (kRow && scales && tid < 128)
-        reinterpret_cast<uint32_t *>(scales + (rt * ctiles + ct) * 512)[tid] =
-            reinterpret_cast<const uint32_t *>(s_sc)[tid];
-    if (!kCol)
-        return;
-
-    const int64_t rows32 = (rows + 31) / 32 * 32;
-    const int rb = warp & 3, c = (warp >> 2) * 64 + lane * 2;
-    if (r0 + rb * 32 < rows && c0 + c < cols) {
-        using P = typename PairOf<T>::type;
-        P v[32];
-        typename PairOf<T>::amax amax;
+    if (kCol) {
+        __syncthreads();   // the tile is in shared memory
+        const int rb = warp & 3, c = ((warp >> 2) * 32 + lane) * kPer;
+        typename S::Word v[32];
+        S amax;
 #pragma unroll
         for (int i = 0; i < 32; i++) {
-            v[i] = *reinterpret_cast<const P *>(s_tile + (rb * 32 + i) * kMqTile + c);
+            v[i] = *reinterpret_cast<const typename S::Word *>(tile + (rb * 32 + i) * kCols + c);
             amax.add(v[i]);
         }
-        const uint32_t b0 = e8m0_of(amax.bits().x), b1 = e8m0_of(amax.bits().y);
-        s_sct[(c & 31) * 16 + (c >> 5) * 4 + rb] = (uint8_t)b0;
-        s_sct[((c + 1) & 31) * 16 + (c >> 5) * 4 + rb] = (uint8_t)b1;
-        const float i0 = b0 == 255u ? 0.0f : e8m0_inverse(b0), i1 = b1 == 255u ? 0.0f : e8m0_inverse(b1);
-        uint32_t q0[4], q1[4];
+        uint32_t byte[kPer], q[kPer][4];
 #pragma unroll
-        for (int g = 0; g < 4; g++) {
-            float f0[8], f1[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float2 f = pair_floats(v[8 * g + e]);
-                f0[e] = f.x;
-                f1[e] = f.y;
-            }
-            q0[g] = b0 == 255u ? 0u : e2m1_encode8_scaled(f0, i0);
-            q1[g] = b1 == 255u ? 0u : e2m1_encode8_scaled(f1, i1);
-        }
-        if (codes_t) {
-            uint8_t *dst = codes_t + (c0 + c) * (rows32 / 2) + (r0 + rb * 32) / 2;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
-            *reinterpret_cast<uint4 *>(dst + rows32 / 2) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-        }
-        if (values_t) {
-            const float s0 = e8m0_scale(b0), s1 = e8m0_scale(b1);
+        for (int j = 0; j < kPer; j++) {
+            byte[j] = e8m0_of(amax.amax_bits(j));
+            reinterpret_cast<uint8_t *>(&s_sct[c + j])[rb] = (uint8_t)byte[j];
+            const float inv = byte[j] != 255u ? e8m0_inverse(byte[j]) : 0.0f;
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-                uint32_t h0[4], h1[4];
-                e2m1x8_to_h2x4(q0[g], h0);
-                e2m1x8_to_h2x4(q1[g], h1);
+                float f[8];
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float2 a = h2_to_f2(h0[e]), b = h2_to_f2(h1[e]);
-                    const int64_t r = r0 + rb * 32 + 8 * g + 2 * e;
-                    uint16_t *dst = values_t + r * cols + c0 + c;
-                    if (r < rows)
-                        *reinterpret_cast<uint32_t *>(dst) = pack_bf2(__fmul_rn(a.x, s0), __fmul_rn(b.x, s1));
-                    if (r + 1 < rows)
-                        *reinterpret_cast<uint32_t *>(dst + cols) = pack_bf2(__fmul_rn(a.y, s0), __fmul_rn(b.y, s1));
+                for (int e = 0; e < 8; e++)
+                    f[e] = S::value(v[8 * g + e], j);
+                q[j][g] = byte[j] != 255u ? e2m1_encode8_scaled(f, inv) : 0u;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; j++)
+            s_q[(c + j) * 5 + rb] = make_uint4(q[j][0], q[j][1], q[j][2], q[j][3]);
+        if (rb * 32 < left && c0 + c < cols) {
+            if (p.values_t) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    uint32_t h[kPer][4];
+#pragma unroll
+                    for (int j = 0; j < kPer; j++)
+                        e2m1x8_to_h2x4(q[j][g], h[j]);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int rl = rb * 32 + 8 * g + e;
+                        uint16_t *dst = p.values_t + (r0 + rl) * cols + c0 + c;
+                        const float2 a = h2_to_f2(h[0][e / 2]), b = h2_to_f2(h[kPer - 1][e / 2]);
+                        const uint32_t w = pack_bf2(__fmul_rn(e & 1 ? a.y : a.x, e8m0_scale(byte[0])),
+                                                    __fmul_rn(e & 1 ? b.y : b.x, e8m0_scale(byte[kPer - 1])));
+                        if (rl < left) {
+                            if (kPer == 2)
+                                *reinterpret_cast<uint32_t *>(dst) = w;
+                            else
+                                *dst = (uint16_t)w;
+                        }
+                    }
                 }
             }
         }
     }
-    __syncthreads();
-    if (scales_t && tid < 128)
-        reinterpret_cast<uint32_t *>(scales_t + (ct * rtiles + rt) * 512)[tid] =
-            reinterpret_cast<const uint32_t *>(s_sct)[tid];
+    __syncthreads();   // the scale bytes and the column codes are complete
+    if (kCol && p.codes_t) {
+        // 64 contiguous bytes a column, four threads
+        uint8_t *dst = p.codes_t + c0 * (rows32 / 2) + r0 / 2;
+#pragma unroll
+        for (int i = tid; i < kCols * 4; i += kMqThreads) {
+            const int c = i >> 2, rb = i & 3;
+            if (rb * 32 < left && c0 + c < cols)
+                *reinterpret_cast<uint4 *>(dst + c * (rows32 / 2) + rb * 16) = s_q[c * 5 + rb];
+        }
+    }
+    // FP32: this tile's two blocks a row are one half of the scale tile's four
+    const int half = kCols == 128 ? 0 : (int)(ct & 1);
+    const bool alone = kCols != 128 && half == 0 && c0 + kCols >= cols;   // there is no other half
+    if (kRow && p.scales && tid < kMqRows) {
+        const uint32_t w = s_sc[(tid >> 2) + 32 * (tid & 3)];
+        uint8_t *dst = p.scales + (rt * ktiles + c0 / 128) * 512 + tid * 4;
+        if (kCols == 128) {
+            *reinterpret_cast<uint32_t *>(dst) = w;
+        } else {
+            *reinterpret_cast<uint16_t *>(dst + half * 2) = (uint16_t)w;
+            if (alone)
+                *reinterpret_cast<uint16_t *>(dst + 2) = 0;
+        }
+    }
+    if (kCol && p.scales_t && tid >= kMqThreads - kCols) {
+        const int w = tid - (kMqThreads - kCols);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.scales_t + (c0 / 128 * rtiles + rt) * 512) + w / kGroups * 4 +
+                        w % kGroups;
+        dst[half * kGroups] = s_sct[w / kGroups + 32 * (w % kGroups)];
+        if (alone)
+            dst[kGroups] = 0u;
+    }
 }
 
 // Codes and tiled scales -> bf16 or FP32, eight elements a thread (exact).
@@ -235,36 +276,38 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t *__restr
 }
 
 template <typename T, bool kRow, bool kCol>
-cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev)
+cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s)
 {
-    const int64_t tiles = ((a.rows + kMqTile - 1) / kMqTile) * ((a.cols + kMqTile - 1) / kMqTile);
-    const size_t smem = kCol ? sizeof(T) * kMqTile * kMqTile : 0;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = allow_smem<mx_quantize_kernel<T, kRow, kCol>>(smem, dev);
-        if (e != cudaSuccess)
-            return e;
-    }
+    constexpr int kCols = MqShape<T>::kCols;
+    MqParams p;
+    p.rows = a.rows;
+    p.cols = a.cols;
+    p.ctiles = (a.cols + kCols - 1) / kCols;
+    p.codes = a.codes;
+    p.scales = a.scales;
+    p.codes_t = a.codes_t;
+    p.scales_t = a.scales_t;
+    p.values = a.values;
+    p.values_t = a.values_t;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles);
+    cfg.gridDim = dim3((unsigned)((a.rows + kMqRows - 1) / kMqRows * p.ctiles));
     cfg.blockDim = dim3(kMqThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx_quantize_kernel<T, kRow, kCol>, (const T *)a.x, a.rows, a.cols, a.ld, a.codes,
-                              a.scales, a.values, a.codes_t, a.scales_t, a.values_t);
+    return cudaLaunchKernelEx(&cfg, mx_quantize_kernel<T, kRow, kCol>, (const T *)a.x, a.ld, p);
 }
 
 template <typename T>
-cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev)
+cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s)
 {
     const bool row = a.codes || a.values, col = a.codes_t || a.values_t;
-    return row && col ? run_quantize<T, true, true>(a, s, dev)
-           : row      ? run_quantize<T, true, false>(a, s, dev)
-                      : run_quantize<T, false, true>(a, s, dev);
+    return row && col ? run_quantize<T, true, true>(a, s)
+           : row      ? run_quantize<T, true, false>(a, s)
+                      : run_quantize<T, false, true>(a, s);
 }
 
 unsigned grid_for(int64_t n, const DeviceInfo &dev)
@@ -275,9 +318,9 @@ unsigned grid_for(int64_t n, const DeviceInfo &dev)
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s, const DeviceInfo &dev)
+cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s)
 {
-    return a.x_fp32 ? run_quantize_dirs<float>(a, s, dev) : run_quantize_dirs<__nv_bfloat16>(a, s, dev);
+    return a.x_fp32 ? run_quantize_dirs<float>(a, s) : run_quantize_dirs<__nv_bfloat16>(a, s);
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
