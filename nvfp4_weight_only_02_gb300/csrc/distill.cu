@@ -93,7 +93,10 @@ struct MaxSum {
 __device__ __forceinline__ float finite_or_zero(float m) { return m == neg_inf() ? 0.0f : m; }
 
 // s of a MaxSum with its maximum moved to m (which is not below v.m)
-__device__ __forceinline__ float sum_at(MaxSum v, float m, float k2) { return v.s * ex2((v.m - finite_or_zero(m)) * k2); }
+__device__ __forceinline__ float sum_at(MaxSum v, float m, float k2)
+{
+    return v.s * ex2((v.m - finite_or_zero(m)) * k2);
+}
 
 __device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float k2)
 {
@@ -629,7 +632,8 @@ __global__ void __launch_bounds__(kDsThreads)
 #pragma unroll
         for (int e = 0; e < kEntries; e++)
             if (idx[e] >= 0)
-                dzs[idx[e] - v0] = Vec<T>::put(c * (mass * ex2((zn[e] - base) * k2 - log2_total) - ex2(lp[e] * kLog2e)));
+                dzs[idx[e] - v0] =
+                    Vec<T>::put(c * (mass * ex2((zn[e] - base) * k2 - log2_total) - ex2(lp[e] * kLog2e)));
     }
     if (C > 1)
         cluster_wait();
@@ -647,11 +651,11 @@ __global__ void __launch_bounds__(kDsThreads)
 // Two CTAs per SM, persistent over the rows, a row each.  A cluster per row
 // spends more on starting clusters and waiting for the slowest CTA than on the
 // logits (4096 rows of 131072 bf16 logits: 500 us, 63 % of the copy bandwidth);
-// here a row's chunks pass through a ring in shared memory twice (424 us,
-// 75 %).  The chunks that the ring still holds after the first pass are used
+// here a row's chunks pass through a ring in shared memory twice (405 us,
+// 78 %).  The chunks that the ring still holds after the first pass are used
 // from there, the ones before them come again from L2, which holds the rest of
 // 304 rows of 256 KB.  One warp copies, the others are consumers.  One CTA of
-// 1024 threads per SM was slower (475 us): its reductions and the turn from one
+// 1024 threads per SM was slower (475 us against 424 at the time): its reductions and the turn from one
 // pass to the other leave the SM without work, which the other CTA fills here.
 // What bounds it now is issue: about 50 instructions per 8 logits and pass.
 constexpr int kDtThreads = 512, kDtPerSm = 2, kDtWarps = kDtThreads / 32 - 1, kDtConsumers = 32 * kDtWarps;
@@ -664,8 +668,8 @@ constexpr int kDtSmem = 113 * 1024 - 1200;       // dynamic shared memory of one
 __device__ __forceinline__ void bulk_g2s_hint(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t pol)
 {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_addr(dst)),
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
         "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(pol)
         : "memory");
 }
@@ -1056,17 +1060,18 @@ cudaError_t run_distill_stream(const DistillArgs &a, int slots, cudaStream_t s, 
     cudaError_t e = allow_smem<distill_stream_kernel<T, kGrad>>(kDtSmem, dev);
     if (e != cudaSuccess)
         return e;
-    distill_stream_kernel<T, kGrad><<<(unsigned)std::min<int64_t>(a.T, kDtPerSm * dev.num_sms), kDtThreads, smem, s>>>(a, slots);
+    const unsigned grid = (unsigned)std::min<int64_t>(a.T, kDtPerSm * dev.num_sms);
+    distill_stream_kernel<T, kGrad><<<grid, kDtThreads, smem, s>>>(a, slots);
     return cudaGetLastError();
 }
 
 template <typename T, bool kGrad, int kEntries>
 cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
-    // Cluster size: the smallest power of two whose slices are at most 40 KB,
-    // so that four or more CTAs share an SM and one's copies run beside
-    // another's arithmetic; with fewer rows than SMs the row is spread over
-    // more CTAs, down to slices of 4 KB.
+    // Cluster size: the smallest power of two whose slices are at most 72 KB,
+    // so that three CTAs share an SM and one's copies run beside another's
+    // arithmetic; with fewer rows than SMs the row is spread over more CTAs as
+    // long as a slice is longer than 8 KB.
     const int64_t row_bytes = a.V * (int64_t)sizeof(T);
     int C = 1;
     while (C < 8 && (row_bytes > C * 73728LL || (a.T * C * 2 <= dev.num_sms && row_bytes > C * 8192LL)))
@@ -1092,8 +1097,16 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
     return cudaLaunchKernelEx(&cfg, distill_kernel<T, kGrad, kEntries>, a, C, L);
 }
 
-// One entry a thread for up to 256 of them, else four: most teachers keep fewer
-// than 256, and the other three's registers and branches cost every thread.
+// Clusters or the stream: bf16, loss and gradient, clusters / stream in us, rows
+// of 131072 logits: 96 rows 16.0 / 19.4, 152 rows 27.0 / 21.7, 304 rows 44.3 /
+// 35.6, 2432 rows 283 / 256; 2432 rows of 64 KB 54.3 / 79.5, of 96 KB 103.4 /
+// 105.7 (loss alone 64.0 / 55.3).  So the stream takes rows above 96 KB when
+// there is one for every SM, as far as its threads hold the teacher's entries
+// and its ring has two chunks.
+//
+// Within clusters, one entry a thread for up to 256 of them, else four: most
+// teachers keep fewer than 256, and the other three's registers and branches
+// cost every thread.
 template <typename T, bool kGrad>
 cudaError_t run_distill_k(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
