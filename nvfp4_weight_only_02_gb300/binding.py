@@ -537,6 +537,14 @@ class _Fp4Operand:
     def shape(self):
         return self.rows, self.cols
 
+    @property
+    def device(self):
+        return self.codes.device
+
+    def addresses(self):
+        """Of the codes and of the scales."""
+        return self.codes.data_ptr(), self.scales.data_ptr()
+
     @classmethod
     def from_row_major(cls, codes, scales, *tensor_scale):
         """From row-major scales (rows, cols/block), as a checkpoint or nvfp4_quantize has them."""
@@ -556,18 +564,40 @@ class MxOperand(_Fp4Operand):
     def __init__(self, codes, scales):
         super().__init__(codes, scales)
 
-    @classmethod
-    def _made(cls, codes, scales, rows, cols):
-        """Of buffers allocated here, whose checks would only take time."""
-        op = cls.__new__(cls)
-        op.codes, op.scales, op.tensor_scale, op.rows, op.cols = codes, scales, None, rows, cols
-        return op
-
     def dequantize(self, dtype=torch.float32):
-        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
-        _call("nvfp4_mx_dequantize", _addr(self.codes), _addr(self.scales), self.rows, self.cols, _addr(out),
-              _out_code(dtype, "dtype"), _raw_stream())
+        out = torch.empty(self.shape, dtype=dtype, device=self.device)
+        _call("nvfp4_mx_dequantize", *self.addresses(), self.rows, self.cols, _addr(out), _out_code(dtype, "dtype"),
+              _raw_stream())
         return out
+
+
+class _MxMade(MxOperand):
+    """An operand for mx_quantize to fill: one buffer with the codes first, then the scales, 16-byte aligned; the
+    tensors are made when they are asked for."""
+
+    tensor_scale = None
+
+    def __init__(self, rows, cols, device):
+        self.rows, self.cols = rows, cols
+        self._at = (rows * cols // 2 + 15) & ~15
+        self._nscales = (rows + 127) // 128 * ((cols + 127) // 128) * 512
+        self._buffer = torch.empty(self._at + self._nscales, dtype=_U8, device=device)
+
+    def addresses(self):
+        base = self._buffer.data_ptr()
+        return base, base + self._at
+
+    @property
+    def device(self):
+        return self._buffer.device
+
+    @property
+    def codes(self):
+        return self._buffer.as_strided((self.rows, self.cols // 2), (self.cols // 2, 1))
+
+    @property
+    def scales(self):
+        return self._buffer.as_strided((self._nscales,), (1,), self._at)
 
 
 class Nvfp4Operand(_Fp4Operand):
@@ -597,36 +627,35 @@ def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values
     straight-through forward."""
     rows, cols, ld, dt = _matrix(x, "x")
     dev = x.device
-    q = qs = qt = qts = v = vt = None
     rows32 = (rows + 31) // 32 * 32
-    if rowwise:
-        if codes:
-            q = torch.empty((rows, cols // 2), dtype=_U8, device=dev)
-            qs = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=_U8, device=dev)
-        if values:
+    row = col = v = vt = q = qs = qt = qts = None
+    if codes:
+        # a buffer each: what is kept for a backward pass does not hold the other direction
+        if rowwise:
+            row = _MxMade(rows, cols, dev)
+            q, qs = row.addresses()
+        if colwise:
+            col = _MxMade(cols, rows32, dev)
+            qt, qts = col.addresses()
+    if values:
+        if rowwise:
             v = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    if colwise:
-        if codes:
-            qt = torch.empty((cols, rows32 // 2), dtype=_U8, device=dev)
-            qts = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=_U8, device=dev)
-        if values:
+        if colwise:
             vt = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    _call("nvfp4_mx_quantize", x.data_ptr(), dt, rows, cols, ld, _addr(q), _addr(qs), _addr(v), _addr(qt), _addr(qts),
-          _addr(vt), _raw_stream())
-    return MxQuantized(None if q is None else MxOperand._made(q, qs, rows, cols),
-                       None if qt is None else MxOperand._made(qt, qts, cols, rows32), v, vt)
+    _call("nvfp4_mx_quantize", x.data_ptr(), dt, rows, cols, ld, q, qs, _addr(v), qt, qts, _addr(vt), _raw_stream())
+    return MxQuantized(row, col, v, vt)
 
 
 def nvfp4_w4a4_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(load().nvfp4_w4a4_workspace_bytes(M, N, K))
+    return (_lib or load()).nvfp4_w4a4_workspace_bytes(M, N, K)
 
 
 def nvfp4_mx_linear_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(load().nvfp4_mx_linear_workspace_bytes(M, N, K))
+    return (_lib or load()).nvfp4_mx_linear_workspace_bytes(M, N, K)
 
 
 def nvfp4_mx_linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(load().nvfp4_mx_linear_backward_workspace_bytes(M, N, K))
+    return (_lib or load()).nvfp4_mx_linear_backward_workspace_bytes(M, N, K)
 
 
 def w4a4_gemm(a, w, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
@@ -637,11 +666,10 @@ def w4a4_gemm(a, w, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
     if K != w.cols:
         raise ValueError(f"a and w must have the same number of columns, got {K} and {w.cols}")
     ydt = _out_code(out_dtype, "out_dtype")
-    y = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
+    y = torch.empty((M, N), dtype=out_dtype, device=a.device)
     ws = workspace if workspace is not None else new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), y.device)
-    _call("nvfp4_w4a4_gemm", a.format, a.codes.data_ptr(), a.scales.data_ptr(), _addr(a.tensor_scale),
-          w.codes.data_ptr(), w.scales.data_ptr(), _addr(w.tensor_scale), M, N, K, y.data_ptr(), ydt, ws.data_ptr(),
-          ws.numel(), _raw_stream())
+    _call("nvfp4_w4a4_gemm", a.format, *a.addresses(), _addr(a.tensor_scale), *w.addresses(), _addr(w.tensor_scale),
+          M, N, K, y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw_stream())
     return y
 
 
@@ -654,7 +682,7 @@ def mx_linear(x: torch.Tensor, w: MxOperand, out_dtype=torch.float32, workspace=
     N = w.rows
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     ws = workspace if workspace is not None else new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
-    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(), y.data_ptr(), ydt,
+    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, *w.addresses(), y.data_ptr(), ydt,
           ws.data_ptr(), ws.numel(), _raw_stream())
     return y
 
@@ -677,9 +705,10 @@ def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, d
     dw = torch.empty((N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
     ws = workspace if workspace is not None else \
         new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
-    part = lambda o: (None, None) if o is None else (o.codes.data_ptr(), o.scales.data_ptr())  # noqa: E731
-    _call("nvfp4_mx_linear_backward", dy.data_ptr(), dt, ld, M, N, K, *part(x_col), *part(w_col), _addr(dx), xdt,
-          _addr(dw), wdt, ws.data_ptr(), ws.numel(), _raw_stream())
+    xp = (None, None) if x_col is None else x_col.addresses()
+    wp = (None, None) if w_col is None else w_col.addresses()
+    _call("nvfp4_mx_linear_backward", dy.data_ptr(), dt, ld, M, N, K, *xp, *wp, _addr(dx), xdt, _addr(dw), wdt,
+          ws.data_ptr(), ws.numel(), _raw_stream())
     return dx, dw
 
 
