@@ -27,7 +27,7 @@ namespace {
 constexpr int kTlEpiWarps = 8;
 constexpr int kTlThreads = 32 * (kTlEpiWarps + 2);  // + copies, MMA
 constexpr int kTlGroup = 8;                          // raster: pairs of row tiles per group
-constexpr int kTlStoreBytes = 4096;                  // a warp's staging for TMA stores: 32 x 32 FP32, or bf16 twice
+constexpr int kTlStoreBytes = 2048;                  // a warp's staging for TMA stores: 32 rows of 64 bytes
 
 struct TileParams {
     const float *a_ts, *w_ts;
@@ -46,7 +46,7 @@ struct TlShape {
     static constexpr int kABytes = 128 * 128, kBBytes = BN / 2 * 128;
     static constexpr int kSaBytes = kTiles * 512, kSbBytes = kBRowTiles * kTiles * 512;
     static constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
-    static constexpr int kFixed = 1024 + kTlEpiWarps * kTlStoreBytes + 512;
+    static constexpr int kFixed = kTlEpiWarps * kTlStoreBytes + 512;
     static constexpr int kFit = (232448 - kFixed) / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr size_t kSmem = kFixed + (size_t)kStages * kStageBytes;
@@ -159,6 +159,12 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
         : "memory");
 }
 
+__device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // Raster: groups of kTlGroup row-tile pairs, the pair index fastest.
 __device__ __forceinline__ void tile_at(int t, int mpairs, int ntiles, int &mp, int &nt)
 {
@@ -176,8 +182,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
 {
     using S = TlShape<kNv, BN>;
     constexpr int kStages = S::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sA = smem, *sB = sA + kStages * S::kABytes, *sOut = sB + kStages * S::kBBytes;
     uint8_t *sSa = sOut + kTlEpiWarps * kTlStoreBytes, *sSb = sSa + kStages * S::kSaBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(sSb + kStages * S::kSbBytes);
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
         uint8_t *out = sOut + warp * kTlStoreBytes;
         const float s_a = p.a_ts ? *p.a_ts : 1.0f, s_w = p.w_ts ? *p.w_ts : 1.0f;
         const bool scaled = p.a_ts || p.w_ts;
-        uint32_t lt = 0, stores = 0;
+        uint32_t lt = 0;
         for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
             int mp, nt;
             tile_at(t, p.mpairs, p.ntiles, mp, nt);
@@ -357,39 +362,38 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                         v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), s_a), s_w));
                 }
                 if (p.tma_store) {
-                    uint8_t *at = out;
-                    if (p.y_fp32) {
+                    // 64 bytes a row at a time: all of the chunk in bf16, half of it in FP32
+                    auto stage_and_store = [&](const uint4 (&w)[4], int n) {
                         if (lane == 0)
-                            bulk_wait_read<0>();
+                            bulk_wait_read<0>();   // the store before has read the staging
                         __syncwarp();
 #pragma unroll
-                        for (int q = 0; q < 8; q++)
-                            *reinterpret_cast<uint4 *>(at + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                                make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                    } else {
-                        // the other half may still be read by the store before
-                        at += (stores++ & 1) * (kTlStoreBytes / 2);
-                        if (lane == 0)
-                            bulk_wait_read<1>();
+                        for (int q = 0; q < 4; q++)
+                            *reinterpret_cast<uint4 *>(out + lane * 64 + ((q ^ (lane >> 1 & 3)) * 16)) = w[q];
+                        fence_proxy_async_smem();
                         __syncwarp();
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(
-                                    __uint_as_float(v[8 * q + 2 * e]), __uint_as_float(v[8 * q + 2 * e + 1]));
-                                w[e] = *reinterpret_cast<const uint32_t *>(&b);
-                            }
-                            *reinterpret_cast<uint4 *>(at + lane * 64 + ((q ^ (lane >> 1 & 3)) * 16)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
+                        if (lane == 0) {
+                            tma_store_2d(&tm_y, out, n, m0);
+                            bulk_commit();
                         }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tm_y, at, n0, m0);
-                        bulk_commit();
+                    };
+                    uint4 w[4];
+                    if (p.y_fp32) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+#pragma unroll
+                            for (int q = 0; q < 4; q++)
+                                w[q] = make_uint4(v[16 * h + 4 * q], v[16 * h + 4 * q + 1], v[16 * h + 4 * q + 2],
+                                                  v[16 * h + 4 * q + 3]);
+                            if (n0 + 16 * h < p.N)
+                                stage_and_store(w, n0 + 16 * h);
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            w[q] = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                                              pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+                        stage_and_store(w, n0);
                     }
                 } else if (m0 + lane < p.M) {
                     // rows of Y that do not start on 16-byte boundaries
@@ -442,8 +446,8 @@ cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
     if (e == cudaSuccess)
         e = tma_store ? encode_tensor_map_2d(&ty, a.y_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                             a.y, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.N * esize, 32, 32,
-                                             a.y_fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)
+                                             a.y, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.N * esize, 64 / esize, 32,
+                                             CU_TENSOR_MAP_SWIZZLE_64B)
                       : (ty = ta, cudaSuccess);
     if (e == cudaSuccess)
         e = allow_smem<w4a4_tile_kernel<kNv, BN>>(S::kSmem, dev);
