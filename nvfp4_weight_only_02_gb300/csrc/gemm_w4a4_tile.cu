@@ -12,6 +12,18 @@
 //
 // Scales: each CTA loads the scale tiles of its own A rows and of all B rows;
 // the leader's copies to TMEM (cta_group::2) work on both CTAs' memory.
+//
+// What bounds it (16384 x 18944 x 3584, MXFP4: 320 us, 6.9 PFLOP/s; under load
+// for longer the power limit lowers the clock from 2.07 to about 1.85 GHz and it
+// takes 335 to 360).  A tile of 14 stages takes about 9500 cycles: 14 x 516 of
+// MMAs (128 cycles for each 64 elements of K), 700 in which the copies of the
+// next stage are late because the stores of the tile before share their way (no
+// store: 8800), about 450 to hand the accumulator over, the rest in the issuing
+// thread.  Measured and left out: B multicast over two pairs (a quarter less to
+// read from L2, but clusters of four fill 144 of 152 SMs: 334 us), stores spread
+// over the next tile's K loop (no change), no reuse of TMEM columns between the
+// accumulators at 224 columns (fewer operations a byte), five stages with 32 KB
+// for the stores (341 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -73,8 +85,8 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-        "[%2];" ::"r"(smem_addr(dst)),
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
         "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
@@ -480,9 +492,8 @@ cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 }
 
 // Width of the tiles: the one whose waves of pairs take least.  A stage of 256
-// elements of K takes 0.28 us at 256 columns (bound by the copies into shared
-// memory), 0.23 at 192 and 128 (by the issuing thread), a tile about 0.7 us
-// besides.  2048 x 3584 x 18944: 50.4 us in 112 tiles of 256, 39.6 in 152 of 192.
+// elements of K takes 0.28 us at 256 columns (bound by the MMAs), 0.23 at 192
+// and 128 (by the issuing thread), a tile about 0.7 us besides.  2048 x 3584 x 18944: 50.4 us in 112 tiles of 256, 39.6 in 152 of 192.
 template <bool kNv>
 cudaError_t run_widths(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {
