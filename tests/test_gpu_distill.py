@@ -341,3 +341,54 @@ def test_many_long_rows_of_odd_stride(nv):
     lt, dt = _tol(z64, i64, t64, 1.0, True, None, None)
     assert (np.abs(ref.to64(loss[rows]) - rl) <= lt).all()
     assert (np.abs(ref.to64(dz[rows]) - rd) <= dt + 2.0 ** -8 * np.abs(rd) + 1e-37).all()
+
+
+@pytest.mark.parametrize("T,V,k", [(300, 60001, 64), (40, 32000, 8), (17, 999, 300)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_loss_to_the_last_digits(nv, T, V, k, tail):
+    """FP32 logits, loss alone: a logarithm is off by 2^-23 of its size at most, a share and a probability by 2^-21
+    (sums of V terms over threads included), the rest's 1 - sum p by k 2^-24."""
+    z, idx, val = _case(T, V, k, torch.float32, 77, tail=tail)
+    loss, dz = nv.distill_topk_loss_grad(z, idx, val, tail=tail)
+    z64, i64, t64 = ref.to64(z), idx.cpu().numpy().astype(np.int64), ref.to64(val)
+    rl, rd = ref.distill(z64, i64, t64, 1.0, tail, None, None)
+    lq = z64 - z64.max(1, keepdims=True)
+    lq -= np.log(np.exp(lq).sum(1, keepdims=True))
+    named = np.take_along_axis(lq, i64, 1)
+    lp = t64 if tail else t64 - t64.max(1, keepdims=True)
+    if not tail:
+        lp = lp - np.log(np.exp(lp).sum(1, keepdims=True))
+    p = np.exp(lp)
+    tol = (p * (2.0 ** -23 * (np.abs(lp) + np.abs(named)) + 2.0 ** -21)).sum(1)
+    if tail:
+        pr, qr = 1 - p.sum(1), 1 - np.exp(named).sum(1)
+        tol += pr * 2.0 ** -21 + (k * 2.0 ** -24) * (1 + np.abs(np.log(pr / qr)))
+    assert (np.abs(ref.to64(loss) - rl) <= tol).all()
+    # and the gradient as a whole (Euclidean norm): 2^-22 of its own
+    d = ref.to64(dz) - rd
+    assert np.sqrt((d * d).sum()) <= 2.0 ** -22 * np.sqrt((rd * rd).sum())
+
+
+@pytest.mark.parametrize("offset", [0.0, 2700.0, -2900.0, 1.0e4, -1.0e6])
+@pytest.mark.parametrize("T,V", [(5, 3001), (160, 50003)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_logits_far_from_zero(nv, offset, T, V, tail):
+    """A softmax does not see an offset.  Multiples of 1/16 keep their differences exactly beside it, so nothing may
+    be lost: shares within 2^-19, logarithms within 2^-20 of a row's spread."""
+    z, idx, val = _case(T, V, 20, torch.float32, 5, tail=tail)
+    z = torch.round(z * 16) / 16
+    z64 = ref.to64(z)
+    loss, dz = nv.distill_topk_loss_grad(z + offset, idx, val, tail=tail)
+    i64, t64 = idx.cpu().numpy().astype(np.int64), ref.to64(val)
+    rl, rd = ref.distill(z64, i64, t64, 1.0, tail, None, None)
+    q = np.exp(z64 - z64.max(1, keepdims=True))
+    q /= q.sum(1, keepdims=True)
+    p = np.exp(t64 if tail else t64 - t64.max(1, keepdims=True))
+    p = p if tail else p / p.sum(1, keepdims=True)
+    tol = 2.0 ** -19 * q
+    np.put_along_axis(tol, i64, np.take_along_axis(tol, i64, 1) + 2.0 ** -19 * p, 1)
+    rest = 2.0 ** -19 * np.maximum(0, 1 - p.sum(1, keepdims=True)) + 20 * 2.0 ** -23 if tail else 0.0
+    qr = 1 - np.take_along_axis(q, i64, 1).sum(1, keepdims=True)
+    assert (np.abs(ref.to64(dz) - rd) <= tol + rest * q / qr).all()
+    spread = np.ptp(z64, axis=1) + np.abs(t64).max(1)
+    assert (np.abs(ref.to64(loss) - rl) <= 2.0 ** -20 * (4 + spread)).all()
