@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kDsThreads)
     // 16 bytes of dz at elements i0 .. i0 + NE - 1 of the slice, those that exist
     auto store = [&](int i0, uint4 u) {
         if (sh == shd && i0 >= 0 && i0 + NE <= len) {
-            *reinterpret_cast<uint4 *>(dzs + i0) = u;
+            __stcs(reinterpret_cast<uint4 *>(dzs + i0), u);   // nobody reads it here
         } else {
             const T *v = reinterpret_cast<const T *>(&u);
 #pragma unroll
@@ -684,10 +684,11 @@ __global__ void __launch_bounds__(kDsThreads)
 // Two CTAs per SM, persistent over the rows, a row each.  A cluster per row
 // spends more on starting clusters and waiting for the slowest CTA than on the
 // logits (4096 rows of 131072 bf16 logits: 500 us, 63 % of the copy bandwidth);
-// here a row's chunks pass through a ring in shared memory twice (402 us,
-// 79 %).  The chunks that the ring still holds after the first pass are used
+// here a row's chunks pass through a ring in shared memory twice (389 us,
+// 81 %).  The chunks that the ring still holds after the first pass are used
 // from there, the ones before them come again from L2, which holds the rest of
-// 304 rows of 256 KB.  One warp copies, the others are consumers.  One CTA of
+// 304 rows of 256 KB; the gradient is stored to be evicted first, so that it
+// does not push them out (with plain stores 417 us).  One warp copies, the others are consumers.  One CTA of
 // 1024 threads per SM was slower (475 us against 424 at the time): its
 // reductions and the turn from one pass to the other leave the SM without work,
 // which the other CTA fills here.
@@ -1043,7 +1044,7 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                         for (int u = 0; u < kDtEach; u++) {
                             float v[NE];
                             Vec<T>::unpack(*reinterpret_cast<const uint4 *>(src + u * kDtConsumers * 16), v);
-                            dst[u * kDtConsumers] = scale.template apply<kFast, kNeg>(v);
+                            __stcs(dst + u * kDtConsumers, scale.template apply<kFast, kNeg>(v));
                         }
                     } else {
 #pragma unroll 1
@@ -1055,7 +1056,7 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                                 const uint4 g4 = scale.template apply<kFast, kNeg>(v);
                                 // without a teacher entry the gradient is 0, whatever the logits hold
                                 if (kFast)
-                                    *reinterpret_cast<uint4 *>(dzr + (int64_t)ju * NE - sh) = g4;
+                                    __stcs(reinterpret_cast<uint4 *>(dzr + (int64_t)ju * NE - sh), g4);
                                 else
                                     store_each(ju, seen ? g4 : make_uint4(0u, 0u, 0u, 0u));
                             }
@@ -1140,7 +1141,7 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
 
 // Clusters or the stream: bf16, loss and gradient, clusters / stream in us, rows
 // of 131072 logits: 96 rows 16.0 / 19.4, 152 rows 27.0 / 21.7, 304 rows 44.3 /
-// 35.6, 2432 rows 283 / 256; 2432 rows of 64 KB 54.3 / 79.5, of 96 KB 103.4 /
+// 35.6, 2432 rows 283 / 256 (before the stores' hint); 2432 rows of 64 KB 54.3 / 79.5, of 96 KB 103.4 /
 // 105.7 (loss alone 64.0 / 55.3).  So the stream takes rows above 96 KB when
 // there is one for every SM, as far as its threads hold the teacher's entries
 // and its ring has two chunks.
