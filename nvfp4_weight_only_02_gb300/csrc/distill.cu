@@ -1141,8 +1141,9 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
 
 // Clusters or the stream: bf16, loss and gradient, clusters / stream in us, rows
 // of 131072 logits: 96 rows 16.0 / 19.4, 152 rows 27.0 / 21.7, 304 rows 44.3 /
-// 35.6, 2432 rows 283 / 256 (before the stores' hint); 2432 rows of 64 KB 54.3 / 79.5, of 96 KB 103.4 /
-// 105.7 (loss alone 64.0 / 55.3).  So the stream takes rows above 96 KB when
+// 35.6, 2432 rows 283 / 256 (all with plain stores); 2432 rows of 64 KB 54.3 /
+// 79.5, of 96 KB 103.4 / 105.7.  The loss alone, 304 rows: 8 KB 4.0 / 5.0, 64 KB
+// 5.7 / 7.2, 128 KB 16.3 / 10.4.  So the stream takes rows above 96 KB when
 // there is one for every SM, as far as its threads hold the teacher's entries
 // and its ring has two chunks.
 //
