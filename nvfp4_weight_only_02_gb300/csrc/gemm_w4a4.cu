@@ -13,9 +13,9 @@
 // than CTA places, and the shares are added in rank order through distributed
 // shared memory.  Codes come by TMA (128-byte swizzle, zero fill outside),
 // scale tiles by bulk copies; one thread copies scales to TMEM and issues the
-// MMAs.  Up to 4 tokens are quantised by the CTAs themselves (each the part of
-// K that it multiplies) while the first weights are on their way: a kernel of
-// its own costs a launch and 2 us.
+// MMAs.  A few tokens are quantised by the CTAs themselves (each the part of K
+// that it multiplies) while the first weights are on their way: a kernel of its
+// own costs a launch and 1 to 2 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -438,12 +438,17 @@ cudaError_t run_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 
 bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev)
 {
-    // 4 tokens: 10.2 us in one kernel, 11.0 with a quantiser of its own (N = 18944, K = 3584);
-    // 8: 11.9 and 11.2, since every CTA quantises them again
-    if (M > 4)
+    // Every CTA quantises its part of K for all tokens again, so what it takes and how many turns of CTAs do that
+    // decide (bf16, one kernel / with a quantiser of its own, us): N = 18944, K = 3584, split 2: 4 tokens (7168
+    // elements a CTA) 10.4 / 11.2, 8 (14336) 12.0 / 11.2; N = K = 3584, split 8: 12 (6144) 6.2 / 6.5, 16 (8192)
+    // 7.3 / 6.5; N = 27648, K = 5120, one CTA a tile: 1 (5120) 15.4 / 16.6, 4 (20480) 19.8 / 16.8; N = 76032,
+    // K = 3584, two turns: 1 (3584) 26.4 / 27.8, 2 (7168) 29.3 / 28.0.
+    if (M > 16)
         return false;
-    const int64_t ksteps = (K + kWsK - 1) / kWsK, split = split_for((N + kWsRows - 1) / kWsRows, K, dev);
-    const int64_t nk = (ksteps + split - 1) / split;
+    const int64_t tiles = (N + kWsRows - 1) / kWsRows, ksteps = (K + kWsK - 1) / kWsK, split = split_for(tiles, K, dev);
+    const int64_t nk = (ksteps + split - 1) / split, turns = (tiles * split + 2 * dev.num_sms - 1) / (2 * dev.num_sms);
+    if (M * nk * kWsK * turns > 7680)
+        return false;
     // at least three stages of weights beside the tokens
     return nk <= 64 && WsShape<false, 16, kBf16>::stages((int)nk) >= std::min<int64_t>(3, std::max<int64_t>(nk, 2));
 }

@@ -494,7 +494,8 @@ cudaError_t run_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 // Width of the tiles: the one whose waves of pairs take least.  A stage of 256
 // elements of K takes 0.28 us at 256 columns and 0.23 at 192 (bound by the MMAs
 // and, in NVFP4, twelve scale copies beside them), 0.23 at 128 (by the issuing
-// thread), a tile about 0.7 us besides.  2048 x 3584 x 18944: 50.4 us in 112 tiles of 256, 39.6 in 152 of 192.
+// thread), a tile about 0.7 us besides.  2048 x 3584 x 18944: 50.4 us in 112
+// tiles of 256, 39.6 in 152 of 192.
 template <bool kNv>
 cudaError_t run_widths(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {

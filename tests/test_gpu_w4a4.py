@@ -280,3 +280,20 @@ def test_large_product(nv):
     cols = np.random.default_rng(1).choice(N, 300, replace=False)
     _check_product(y[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()], a64[rows], w64[cols], sa * sw, K)
     assert torch.equal(y, nv.w4a4_gemm(a, w))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [2, 3, 5, 9, 15, 16])
+@pytest.mark.parametrize("N,K", [(257, 3616), (129, 96), (40, 32), (1500, 992)])
+def test_few_tokens(nv, M, N, K, dtype):
+    """One kernel or two by the work a CTA has: the same bits either way, and as the quantiser's codes give."""
+    g = torch.Generator().manual_seed(100 * M + K)
+    x = (torch.randn(M, K, generator=g) * torch.exp2(torch.randint(-9, 9, (M, 1), generator=g).float())).to(dtype).cuda()
+    x[M // 2] = 0
+    w = nv.mx_quantize((torch.randn(N, K, generator=g) * 0.1).cuda()).row
+    y = nv.mx_linear(x, w)
+    _check_product(y, ref.mx_round(ref.to64(x)), ref.to64(w.dequantize()), 1.0, K)
+    assert torch.equal(y, nv.w4a4_gemm(nv.mx_quantize(x).row, w))
+    x[M - 1, K - 1] = float("inf")
+    bad = nv.mx_linear(x, w)
+    assert torch.isnan(bad[M - 1]).all() and torch.equal(bad[:M - 1], y[:M - 1])
