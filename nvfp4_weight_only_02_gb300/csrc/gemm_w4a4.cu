@@ -23,6 +23,7 @@
 #include "internal.h"
 #include "mx_codec.cuh"
 #include "sm100.cuh"
+#include "w4a4_shape.h"
 
 namespace nvfp4 {
 
@@ -31,10 +32,6 @@ using namespace sm100;
 namespace {
 
 constexpr int kWsThreads = 192;  // warps 0-3: tokens and epilogue, 4: copies, 5: MMA
-constexpr int kWsRows = 128;     // weight rows per CTA
-constexpr int kWsK = 256;        // elements of K per stage (128 bytes of codes a row)
-constexpr int kWsSmem = 113 * 1024;  // two CTAs share an SM
-constexpr int kWsMaxStages = 6;
 
 struct W4A4Params {
     const uint8_t *a_scales, *w_scales;
@@ -51,35 +48,6 @@ struct W4A4Params {
     void *y;
     int y_fp32;
     uint32_t *ctl;
-};
-
-// Tokens as the kernel gets them: quantised, or bf16 / FP32 to be quantised here.
-enum Tokens { kCodes, kBf16, kFp32 };
-
-template <bool kNv, int NT, Tokens kTok>
-struct WsShape {
-    static constexpr int kTiles = kNv ? 4 : 2;                    // scale tiles per stage and operand
-    static constexpr int kScaleBytes = kTiles * 512;
-    static constexpr int kWBytes = kWsRows * 128 + kScaleBytes, kXBytes = NT * 128 + kScaleBytes;
-    static constexpr bool kOwn = kTok != kCodes;                  // tokens quantised here stay for all stages
-    static constexpr int kFixed = 1024 + 256;
-    static constexpr int kAccCols = NT < 64 ? 64 : NT;
-    static constexpr int kSfCols = 2 * kTiles * 4;                // one stage's scales of both operands
-    static constexpr int kSfBufs = kNv && NT <= 64 ? 2 : 4;       // stages whose scales fit beside the accumulator
-    static constexpr int kTmemCols = kAccCols + kSfBufs * kSfCols <= 128 ? 128 : 256;
-    static_assert(kAccCols + kSfBufs * kSfCols <= kTmemCols, "TMEM");
-    // ring stages beside `nk` stages of own tokens; 0: they do not fit
-    static int stages(int nk)
-    {
-        const int room = kWsSmem - kFixed - (kOwn ? nk * kXBytes : 0);
-        const int fit = room / (kOwn ? kWBytes : kWBytes + kXBytes);
-        return std::max(0, std::min({fit, kWsMaxStages, std::max(nk, 2)}));
-    }
-    static size_t smem(int nk, int stages)
-    {
-        const size_t ring = (size_t)stages * (kOwn ? kWBytes : kWBytes + kXBytes) + (kOwn ? (size_t)nk * kXBytes : 0);
-        return kFixed + std::max(ring, (size_t)NT * 512);   // the ring also holds the shares of a split K
-    }
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t local, uint32_t rank)
