@@ -467,6 +467,9 @@ nvfp4_status nvfp4_mx_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int6
  *     gives it mass, the gradient stays finite.  A NaN or +inf among the
  *     logits, or a row of nothing but -inf, makes the row's loss and gradient
  *     NaN.
+ *   - A device-side wait that gives up makes the loss and gradient of its row
+ *     (and of the rows behind it in the same block) NaN, and is recorded as
+ *     NVFP4_ERR_TIMEOUT when there is a workspace.
  * T >= 1; 1 <= V, a row of at most 1638272 bytes; 1 <= k <= 1024; index_bytes
  * 4 or 8; temperature finite and positive.  z, dz 16-byte aligned as every
  * pointer; ldz, lddz >= V arbitrary. */
@@ -476,6 +479,15 @@ nvfp4_status nvfp4_distill_topk(const void *z, nvfp4_dtype z_dtype, int64_t T, i
                                 const float *row_weight, const float *grad_loss, int64_t grad_loss_count,
                                 float *loss, void *dz, int64_t lddz, void *workspace, size_t ws_bytes,
                                 void *stream);
+
+/* Self-check: nvfp4_distill_topk (contiguous logits, int32 indices, FP32
+ * teacher values, temperature 1, no grad_loss) in which every wait for a copy
+ * gives up at once.  Rows of weight 0 or without an entry give 0 as ever, the
+ * others NaN. */
+nvfp4_status nvfp4_distill_wait_selftest(const void *z, nvfp4_dtype z_dtype, int64_t T, int64_t V,
+                                         const int32_t *index, const float *teacher, int64_t k, int rest_class,
+                                         const float *row_weight, float *loss, void *dz, void *workspace,
+                                         size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -32,6 +32,7 @@ EXPORTS = [
     "nvfp4_w4a16_lora_gemm_list", "nvfp4_tiled_scale_bytes", "nvfp4_tile_scales", "nvfp4_mx_quantize",
     "nvfp4_mx_dequantize", "nvfp4_w4a4_workspace_bytes", "nvfp4_w4a4_gemm", "nvfp4_mx_linear_workspace_bytes",
     "nvfp4_mx_linear", "nvfp4_mx_linear_backward_workspace_bytes", "nvfp4_mx_linear_backward", "nvfp4_distill_topk",
+    "nvfp4_distill_wait_selftest",
 ]
 
 
@@ -107,6 +108,8 @@ def load(build_if_missing: bool = True):
                                               ctypes.c_int, P, ctypes.c_size_t, P]),
             "nvfp4_distill_topk": (st, [P, ctypes.c_int, i64, i64, i64, P, ctypes.c_int, P, ctypes.c_int, i64,
                                         ctypes.c_float, ctypes.c_int, P, P, i64, P, P, i64, P, ctypes.c_size_t, P]),
+            "nvfp4_distill_wait_selftest": (st, [P, ctypes.c_int, i64, i64, P, P, i64, ctypes.c_int, P, P, P, P,
+                                                 ctypes.c_size_t, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -772,3 +775,21 @@ def distill_topk_grad(z, index, teacher, grad_loss=None, temperature=1.0, tail=F
     dz = out if out is not None else torch.empty_like(z, memory_format=torch.contiguous_format)
     nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, None, dz, workspace)
     return dz
+
+
+def nvfp4_distill_wait_selftest(z, index, teacher, tail=False, row_weight=None, loss=None, dz=None, workspace=None):
+    """The distillation kernels with waits that give up at once (see include/nvfp4.h): z (T, V) contiguous."""
+    T, V, ldz, zdt = _matrix(z, "z")
+    k = index.shape[1]
+    _need(z, z.dtype, (T, V), "z")
+    _need(index, torch.int32, (T, k), "index")
+    _need(teacher, _F32, (T, k), "teacher")
+    if row_weight is not None:
+        _need(row_weight, _F32, (T,), "row_weight")
+    if loss is not None:
+        _need(loss, _F32, (T,), "loss")
+    if dz is not None:
+        _need(dz, z.dtype, (T, V), "dz")
+    _call("nvfp4_distill_wait_selftest", z.data_ptr(), zdt, T, V, index.data_ptr(), teacher.data_ptr(), k,
+          1 if tail else 0, _addr(row_weight), _addr(loss), _addr(dz), _addr(workspace),
+          0 if workspace is None else workspace.numel(), _raw_stream())

@@ -56,6 +56,53 @@ MxQuantArgs quant_args(const void *x, nvfp4_dtype dt, int64_t rows, int64_t cols
     return a;
 }
 
+// Checks of nvfp4_distill_topk's arguments; what its launch takes.
+nvfp4_status distill_args(DistillArgs &a, const void *z, nvfp4_dtype z_dtype, int64_t T, int64_t V, int64_t ldz,
+                          const void *index, int index_bytes, const void *teacher, nvfp4_dtype teacher_dtype,
+                          int64_t k, float temperature, int rest_class, const float *row_weight,
+                          const float *grad_loss, int64_t grad_loss_count, float *loss, void *dz, int64_t lddz,
+                          void *workspace, size_t ws_bytes)
+{
+    const float inv_tau = 1.0f / temperature;
+    if (!z || !index || !teacher || (!loss && !dz) || !dtype_ok(z_dtype) || !dtype_ok(teacher_dtype) ||
+        (index_bytes != 4 && index_bytes != 8) || !(temperature > 0.0f) || !std::isfinite(temperature) ||
+        !std::isfinite(inv_tau) || inv_tau == 0.0f || (grad_loss && !dz))
+        return NVFP4_ERR_INVALID_ARG;
+    const int64_t size = z_dtype == NVFP4_OUT_FP32 ? 4 : 2;
+    // 8 CTAs hold a row, each slice rounded up to 16 bytes
+    if (T < 1 || T > (1LL << 27) || V < 1 || V > kMaxDim || V * size > 8 * (kDistillMaxSlice - 16) || ldz < V || k < 1 ||
+        k > kDistillMaxK || (dz && lddz < V) || ldz > (1LL << 40) || (dz && lddz > (1LL << 40)) ||
+        (grad_loss && grad_loss_count != 1 && grad_loss_count != T))
+        return NVFP4_ERR_SHAPE;
+    if (!aligned16(z) || !aligned16(index) || !aligned16(teacher) || !opt_aligned(row_weight) ||
+        !opt_aligned(grad_loss) || !opt_aligned(loss) || !opt_aligned(dz) || !opt_aligned(workspace))
+        return NVFP4_ERR_ALIGNMENT;
+    if (workspace && ws_bytes < kCtlBytes)
+        return NVFP4_ERR_WORKSPACE;
+    a = {};
+    a.z = z;
+    a.z_fp32 = z_dtype == NVFP4_OUT_FP32;
+    a.T = T;
+    a.V = V;
+    a.ldz = ldz;
+    a.idx = index;
+    a.idx64 = index_bytes == 8;
+    a.val = teacher;
+    a.val_fp32 = teacher_dtype == NVFP4_OUT_FP32;
+    a.k = (int)k;
+    a.tau = temperature;
+    a.inv_tau = inv_tau;
+    a.tail = rest_class != 0;
+    a.weight = row_weight;
+    a.grad_loss = grad_loss;
+    a.grad_rows = grad_loss_count == T && T > 1;
+    a.loss = loss;
+    a.dz = dz;
+    a.lddz = lddz;
+    a.ctl = (uint32_t *)workspace;
+    return NVFP4_OK;
+}
+
 }  // namespace
 
 #define NVFP4_TRY_DEVICE(devp)                  \
@@ -301,44 +348,28 @@ nvfp4_status nvfp4_distill_topk(const void *z, nvfp4_dtype z_dtype, int64_t T, i
                                 const float *grad_loss, int64_t grad_loss_count, float *loss, void *dz,
                                 int64_t lddz, void *workspace, size_t ws_bytes, void *stream)
 {
-    const float inv_tau = 1.0f / temperature;
-    if (!z || !index || !teacher || (!loss && !dz) || !dtype_ok(z_dtype) || !dtype_ok(teacher_dtype) ||
-        (index_bytes != 4 && index_bytes != 8) || !(temperature > 0.0f) || !std::isfinite(temperature) ||
-        !std::isfinite(inv_tau) || inv_tau == 0.0f || (grad_loss && !dz))
-        return NVFP4_ERR_INVALID_ARG;
-    const int64_t size = z_dtype == NVFP4_OUT_FP32 ? 4 : 2;
-    // 8 CTAs hold a row, each slice rounded up to 16 bytes
-    if (T < 1 || T > (1LL << 27) || V < 1 || V > kMaxDim || V * size > 8 * (kDistillMaxSlice - 16) || ldz < V || k < 1 ||
-        k > kDistillMaxK || (dz && lddz < V) || ldz > (1LL << 40) || (dz && lddz > (1LL << 40)) ||
-        (grad_loss && grad_loss_count != 1 && grad_loss_count != T))
-        return NVFP4_ERR_SHAPE;
-    if (!aligned16(z) || !aligned16(index) || !aligned16(teacher) || !opt_aligned(row_weight) ||
-        !opt_aligned(grad_loss) || !opt_aligned(loss) || !opt_aligned(dz) || !opt_aligned(workspace))
-        return NVFP4_ERR_ALIGNMENT;
-    if (workspace && ws_bytes < kCtlBytes)
-        return NVFP4_ERR_WORKSPACE;
+    DistillArgs a;
+    const nvfp4_status st = distill_args(a, z, z_dtype, T, V, ldz, index, index_bytes, teacher, teacher_dtype, k,
+                                         temperature, rest_class, row_weight, grad_loss, grad_loss_count, loss, dz,
+                                         lddz, workspace, ws_bytes);
+    if (st != NVFP4_OK)
+        return st;
     NVFP4_TRY_DEVICE(dev);
-    DistillArgs a = {};
-    a.z = z;
-    a.z_fp32 = z_dtype == NVFP4_OUT_FP32;
-    a.T = T;
-    a.V = V;
-    a.ldz = ldz;
-    a.idx = index;
-    a.idx64 = index_bytes == 8;
-    a.val = teacher;
-    a.val_fp32 = teacher_dtype == NVFP4_OUT_FP32;
-    a.k = (int)k;
-    a.tau = temperature;
-    a.inv_tau = inv_tau;
-    a.tail = rest_class != 0;
-    a.weight = row_weight;
-    a.grad_loss = grad_loss;
-    a.grad_rows = grad_loss_count == T && T > 1;
-    a.loss = loss;
-    a.dz = dz;
-    a.lddz = lddz;
-    a.ctl = (uint32_t *)workspace;
+    return from_cuda(launch_distill(a, (cudaStream_t)stream, *dev));
+}
+
+nvfp4_status nvfp4_distill_wait_selftest(const void *z, nvfp4_dtype z_dtype, int64_t T, int64_t V,
+                                         const int32_t *index, const float *teacher, int64_t k, int rest_class,
+                                         const float *row_weight, float *loss, void *dz, void *workspace,
+                                         size_t ws_bytes, void *stream)
+{
+    DistillArgs a;
+    const nvfp4_status st = distill_args(a, z, z_dtype, T, V, V, index, 4, teacher, NVFP4_OUT_FP32, k, 1.0f, rest_class,
+                                         row_weight, nullptr, 0, loss, dz, V, workspace, ws_bytes);
+    if (st != NVFP4_OK)
+        return st;
+    a.give_up = true;
+    NVFP4_TRY_DEVICE(dev);
     return from_cuda(launch_distill(a, (cudaStream_t)stream, *dev));
 }
 

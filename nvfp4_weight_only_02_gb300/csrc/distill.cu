@@ -21,6 +21,9 @@
 // after their logits have been fetched), never as 1 - sum: with a confident
 // student the difference would have no correct digit.  All statistics are
 // FP32; sums have a fixed order, so results do not depend on scheduling.
+//
+// A bounded wait that gives up makes the row NaN, since a call without a
+// workspace has no status word to record it in.
 #include <algorithm>
 #include <type_traits>
 
@@ -87,6 +90,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 }
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
 
 // A maximum m of logits and the sum s of 2^((z - m) k2), k2 = log2(e) / tau.
 // The difference is taken before the scaling where z is so large that z k2
@@ -482,8 +486,12 @@ __global__ void __launch_bounds__(kDsThreads)
     __syncthreads();       // the barrier is initialised
     if (C > 1)
         cluster_arrive();  // matched below: every CTA of the cluster runs before anyone writes to it
-    if (len > 0 && !mbar_wait(&s_bar, 0) && a.ctl)
-        record_status(a.ctl, NVFP4_ERR_TIMEOUT);
+    const bool landed = len <= 0 || (!a.give_up && mbar_wait(&s_bar, 0));
+    if (!landed) {
+        if (a.ctl)
+            record_status(a.ctl, NVFP4_ERR_TIMEOUT);
+        mbar_wait(&s_bar, 0);   // once more: the CTA does not leave with copies on their way
+    }
 
     // elements of the first and last 16 bytes outside the slice: -inf
     if (tid < NE && len > 0) {
@@ -546,7 +554,8 @@ __global__ void __launch_bounds__(kDsThreads)
             __syncthreads();   // every thread has read s_m
             all = scan_any(tid, len, kDsThreads, k2, [&](int i) { return Vec<T>::get(s_z[sh + i]); });
         }
-        all = {ma, warp_sum(sum_at(all, ma, k2))};
+        // a sum of NaN makes the row's loss and gradient NaN, in every CTA
+        all = {ma, warp_sum(landed ? sum_at(all, ma, k2) : quiet_nan())};
         if (a.tail)
             named = {mb, warp_sum(sum_at(named, mb, k2))};
         else
@@ -764,7 +773,7 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                 const int64_t total = (int64_t)((sh + a.V) * (int64_t)sizeof(T)) & ~15LL;
                 for (int i = 0; i < n + (kGrad ? kept : 0) && ok; i++, load++) {
                     const int c = i < n ? i : i - n, slot = load % slots;
-                    if (load >= (uint32_t)slots && !mbar_wait(&empty[slot], (load / slots - 1) & 1)) {
+                    if (load >= (uint32_t)slots && (a.give_up || !mbar_wait(&empty[slot], (load / slots - 1) & 1))) {
                         if (a.ctl)
                             record_status(a.ctl, NVFP4_ERR_TIMEOUT);
                         ok = false;
@@ -782,6 +791,9 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                     }
                 }
             }
+            // consumers that gave up wait no more, but the CTA does not leave with copies on their way
+            for (uint32_t i = load > (uint32_t)slots ? load - slots : 0u; i < load; i++)
+                mbar_wait(&full[i % slots], (i / slots) & 1);
         }
         return;
     }
@@ -790,7 +802,9 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
     const int V = (int)a.V;
     int slot = 0;             // of the next copy
     uint32_t phase = 0;       // and its barrier's parity
-    bool ok = true;
+    // A thread whose wait gave up waits no more, and as lane 0 frees no slot any more, so that no slot is filled before
+    // its last copy has landed: the producer and the other warps give up in turn, and the rows from there on are NaN.
+    bool ok = !a.give_up;
     auto next = [&]() {
         if (++slot == slots) {
             slot = 0;
@@ -799,7 +813,7 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
     };
     auto release = [&](int at) {
         __syncwarp();
-        if (lane == 0)
+        if (lane == 0 && ok)
             mbar_arrive(&empty[at]);
     };
     // A row's weight, this thread's teacher entry and the student's logit there
@@ -968,7 +982,7 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                     return a.tail && (s_bits[(sh + i) >> 5] >> ((sh + i) & 31) & 1) ? neg_inf() : Vec<T>::get(zr[i]);
                 });
             }
-            const float sa = warp_sum(sum_at(all, ma, k2));
+            const float sa = warp_sum(ok ? sum_at(all, ma, k2) : quiet_nan());
             float sn = 0.0f, st = 0.0f, cnt = 0.0f;
             if (teach) {
                 sn = warp_sum(sum_at(named, mb, k2));
@@ -1036,9 +1050,15 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                         ok = ok && mbar_wait(&full[slot], phase);
                     const uint8_t *src = s_ring + at * kDtChunk + tid * 16;
                     const int j = c * kDtVecs + tid;
-                    if (kFast && c * kDtVecs >= j0 && (c + 1) * kDtVecs <= j1) {
+                    if (!ok) {
+                        const uint32_t nan = seen ? (sizeof(T) == 2 ? 0x7FC07FC0u : 0x7FC00000u) : 0u;
+#pragma unroll 1
+                        for (int u = 0; u < kDtEach; u++)
+                            if (j + u * kDtConsumers >= j0 && j + u * kDtConsumers < j1)
+                                store_each(j + u * kDtConsumers, make_uint4(nan, nan, nan, nan));
+                    } else if (kFast && c * kDtVecs >= j0 && (c + 1) * kDtVecs <= j1) {
                         uint4 *dst = reinterpret_cast<uint4 *>(dzr + (int64_t)j * NE - sh);
-// by two: all four need more than the 64 registers of two CTAs, and their spills
+                        // by two: all four need more than the 64 registers of two CTAs, and their spills
                         // cost 475 us instead of 402 at 4096 x 131072
 #pragma unroll 2
                         for (int u = 0; u < kDtEach; u++) {

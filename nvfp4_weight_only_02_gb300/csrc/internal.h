@@ -186,6 +186,7 @@ struct DistillArgs {
     void *dz;                 // T x V (leading dimension lddz) or null
     int64_t lddz;
     uint32_t *ctl;            // status words or null
+    bool give_up;             // self-check: waits for copies give up at once
 };
 cudaError_t launch_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &dev);
 
