@@ -151,13 +151,16 @@ __device__ __forceinline__ void st_cluster_f4(uint32_t local, uint32_t rank, flo
                  : "memory");
 }
 
+// Both by whole warps: lanes that took different ways before come together first.
 __device__ __forceinline__ void cluster_arrive()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -578,7 +581,6 @@ __global__ void __launch_bounds__(kDsThreads)
         cluster_wait();
         if (tid < C)
             st_cluster_f4(smem_addr(&s_x[rank]), (uint32_t)tid, make_float4(all.m, all.s, named.m, named.s));
-        __syncwarp();
         cluster_arrive();
     }
 
@@ -654,7 +656,6 @@ __global__ void __launch_bounds__(kDsThreads)
                 s_l[0].x = sum;
         }
     }
-    __syncwarp();
     if (C > 1)
         cluster_arrive();
 

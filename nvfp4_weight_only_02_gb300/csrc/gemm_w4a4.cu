@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
         constexpr int kChunk = NT < 32 ? NT : 32;
         for (int c = 0; c < NT; c += 32) {
             uint32_t v[32];
+            __syncwarp();   // the stores before may have parted the warp
             tmem_ld32_start(lane_base + c, v);
             tmem_ld32_finish(v);
 #pragma unroll

@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
             for (int i = 0; i < kChunks / 2; i++) {
                 uint32_t(&v)[32] = buf[i & 1];
+                __syncwarp();   // the stores before may have parted the warp
                 tmem_ld32_finish(v);
                 if (i + 1 < kChunks / 2)
                     tmem_ld32_start(acc + (first + half + 2 * (i + 1)) % kChunks * 32, buf[(i + 1) & 1]);
