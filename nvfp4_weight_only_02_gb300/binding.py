@@ -1,6 +1,7 @@
 """Thin ctypes binding of libnvfp4.so (argument marshalling only).
 
-Every function here takes CUDA tensors, checks dtypes and shapes, and passes
+Every function here takes CUDA tensors of the current device, checks devices,
+dtypes and shapes, and passes
 raw device pointers, sizes and the current CUDA stream to the C ABI declared
 in include/nvfp4.h.  All arithmetic happens in the library's CUDA kernels;
 if the library is missing, loading fails loudly: there is no CPU fallback.
@@ -142,9 +143,29 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _need(t, dtype, shape, name):
-    if not t.is_cuda:
+_current = torch._C._cuda_getDevice   # index of the current device
+
+
+def _device_of(t, name):
+    """Index of t's device, which has to be the current one: kernels run on its stream, and an address of another
+    device or of the host would fault there."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _current():
+        raise ValueError(f"{name} must be on the current device, cuda:{_current()}, got cuda:{dev}")
+    return dev
+
+
+def _space(workspace):
+    if workspace is None:
+        return None
+    _device_of(workspace, "workspace")
+    return ctypes.c_void_p(workspace.data_ptr())
+
+
+def _need(t, dtype, shape, name):
+    _device_of(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -165,7 +186,7 @@ def new_workspace(nbytes: int, device=None) -> torch.Tensor:
 
 
 def nvfp4_get_device_status(workspace: torch.Tensor) -> int:
-    return int(load().nvfp4_get_device_status(_ptr(workspace), _stream()))
+    return int(load().nvfp4_get_device_status(_space(workspace), _stream()))
 
 
 # ------------------------------------------------------------------ entry points
@@ -178,7 +199,7 @@ def nvfp4_quantize(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     _need(scales, torch.uint8, (N, K // 16), "scales")
     _need(tensor_scale, torch.float32, (1,), "tensor_scale")
     st = load().nvfp4_quantize(_ptr(w), N, K, _ptr(codes), _ptr(scales), _ptr(tensor_scale),
-                               int(bool(use_given_tensor_scale)), _ptr(workspace),
+                               int(bool(use_given_tensor_scale)), _space(workspace),
                                workspace.numel(), _stream())
     _check(st, "nvfp4_quantize")
 
@@ -219,7 +240,7 @@ def nvfp4_w4a16_lora_gemm(x: torch.Tensor, codes: torch.Tensor, scales: torch.Te
     st = load().nvfp4_w4a16_lora_gemm(
         _ptr(x), M, N, K, _ptr(codes), _ptr(scales), _ptr(tensor_scale), _ptr(lora_a),
         _ptr(lora_b), r, float(lora_scale), _ptr(noise), _ptr(y),
-        OUT_FP32 if y.dtype == torch.float32 else OUT_BF16, _ptr(workspace), workspace.numel(),
+        OUT_FP32 if y.dtype == torch.float32 else OUT_BF16, _space(workspace), workspace.numel(),
         _stream())
     _check(st, "nvfp4_w4a16_lora_gemm")
 
@@ -263,7 +284,7 @@ def nvfp4_gemm_list_workspace_bytes(entries) -> int:
 def nvfp4_w4a16_lora_gemm_list(entries, workspace: torch.Tensor):
     """Independent projections of one token count in one call (see _projection_array for an entry)."""
     arr, M, r, ydt = _projection_array(entries)
-    st = load().nvfp4_w4a16_lora_gemm_list(arr, len(entries), M, r, ydt, _ptr(workspace), workspace.numel(),
+    st = load().nvfp4_w4a16_lora_gemm_list(arr, len(entries), M, r, ydt, _space(workspace), workspace.numel(),
                                            _stream())
     _check(st, "nvfp4_w4a16_lora_gemm_list")
 
@@ -275,7 +296,7 @@ def nvfp4_round_scales(scale_param: torch.Tensor, tensor_scale: torch.Tensor,
     _need(scales, torch.uint8, (N, KB), "scales")
     _need(tensor_scale, torch.float32, (1,), "tensor_scale")
     st = load().nvfp4_round_scales(_ptr(scale_param), _ptr(tensor_scale), N, KB * 16,
-                                   _ptr(scales), _ptr(workspace), workspace.numel(), _stream())
+                                   _ptr(scales), _space(workspace), workspace.numel(), _stream())
     _check(st, "nvfp4_round_scales")
 
 
@@ -302,7 +323,7 @@ def nvfp4_scale_qlora_gemm(x: torch.Tensor, codes: torch.Tensor, scale_param: to
     st = load().nvfp4_scale_qlora_gemm(
         _ptr(x), M, N, K, _ptr(codes), _ptr(scale_param), _ptr(tensor_scale), _ptr(scales),
         _ptr(lora_a), _ptr(lora_b), r, float(lora_scale), _ptr(noise), _ptr(y),
-        OUT_FP32 if y.dtype == torch.float32 else OUT_BF16, _ptr(workspace), workspace.numel(),
+        OUT_FP32 if y.dtype == torch.float32 else OUT_BF16, _space(workspace), workspace.numel(),
         _stream())
     _check(st, "nvfp4_scale_qlora_gemm")
 
@@ -315,7 +336,7 @@ def nvfp4_encode_debug(x: torch.Tensor, which: int) -> torch.Tensor:
 
 
 def nvfp4_wait_selftest(workspace: torch.Tensor, which: int):
-    _check(load().nvfp4_wait_selftest(_ptr(workspace), int(which), _stream()), "nvfp4_wait_selftest")
+    _check(load().nvfp4_wait_selftest(_space(workspace), int(which), _stream()), "nvfp4_wait_selftest")
 
 
 def nvfp4_quotient_check(sig_lo: int, sig_hi: int) -> int:
@@ -382,7 +403,7 @@ def nvfp4_w4a16_lora_gemm_dgrad(dy: torch.Tensor, codes: torch.Tensor, scales: t
     st = load().nvfp4_w4a16_lora_gemm_dgrad(
         _ptr(dy), M, N, K, _ptr(codes), _ptr(scales), _ptr(tensor_scale), _ptr(lora_a),
         _ptr(lora_b), r, float(lora_scale), _ptr(noise), _ptr(dx),
-        OUT_FP32 if dx.dtype == torch.float32 else OUT_BF16, _ptr(workspace), workspace.numel(),
+        OUT_FP32 if dx.dtype == torch.float32 else OUT_BF16, _space(workspace), workspace.numel(),
         _stream())
     _check(st, "nvfp4_w4a16_lora_gemm_dgrad")
 
@@ -419,7 +440,7 @@ def nvfp4_lora_grads(x: torch.Tensor, noise, dy: torch.Tensor, lora_a: torch.Ten
     if noise is not None:
         _need(noise, torch.float32, (K,), "noise")
     st = load().nvfp4_lora_grads(_ptr(x), _ptr(noise), _ptr(dy), M, N, K, _ptr(lora_a), _ptr(lora_b), r,
-                                 float(lora_scale), _ptr(grad_a), _ptr(grad_b), _ptr(workspace),
+                                 float(lora_scale), _ptr(grad_a), _ptr(grad_b), _space(workspace),
                                  workspace.numel(), _stream())
     _check(st, "nvfp4_lora_grads")
 
@@ -479,7 +500,7 @@ def _out_code(dtype, name):
 
 def _raw_stream():
     # torch.cuda.current_stream() without building the Stream object
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch._C._cuda_getCurrentRawStream(_current())
 
 
 def _call(name, *args):
@@ -489,12 +510,13 @@ def _call(name, *args):
 
 
 def _matrix(t, name):
-    """Checks a 2-D CUDA matrix whose rows are contiguous; returns (rows, cols, row stride in elements, type code)."""
+    """Checks a 2-D matrix on the current device whose rows are contiguous; returns (rows, cols, row stride in
+    elements, type code)."""
+    if t.get_device() != _current():
+        _device_of(t, name)
     code = _DTYPE_CODE.get(t.dtype)
     shape = t.shape
-    if code is None or not t.is_cuda or len(shape) != 2:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+    if code is None or len(shape) != 2:
         _out_code(t.dtype, name)
         raise ValueError(f"{name} must have 2 dimensions, got {len(shape)}")
     rows, cols = shape
@@ -506,6 +528,15 @@ def _matrix(t, name):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace):
+    """Checks a workspace that the caller keeps."""
+    if workspace.dtype is not _U8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous torch.uint8 tensor")
+    if workspace.get_device() != _current():
+        _device_of(workspace, "workspace")
+    return workspace
 
 
 def nvfp4_tiled_scale_bytes(rows: int, cols: int, fmt: int) -> int:
@@ -520,6 +551,8 @@ class _Fp4Operand:
     def __init__(self, codes, scales, tensor_scale=None):
         if not (codes.is_cuda and scales.is_cuda):
             raise ValueError("codes and scales must be CUDA tensors")
+        if scales.get_device() != codes.get_device():
+            raise ValueError("codes and scales must be on one device")
         if codes.dtype != _U8 or scales.dtype != _U8:
             raise ValueError("codes and scales must be torch.uint8")
         if codes.dim() != 2 or not codes.is_contiguous() or not scales.is_contiguous():
@@ -533,6 +566,8 @@ class _Fp4Operand:
                              f"{self.block}")
         if tensor_scale is not None:
             _need(tensor_scale, _F32, (1,), "tensor_scale")
+            if tensor_scale.get_device() != codes.get_device():
+                raise ValueError("codes and tensor_scale must be on one device")
         self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
         self.rows, self.cols = rows, cols
 
@@ -546,6 +581,8 @@ class _Fp4Operand:
 
     def addresses(self):
         """Of the codes and of the scales."""
+        if self.codes.get_device() != _current():
+            _device_of(self.codes, "operand")
         return self.codes.data_ptr(), self.scales.data_ptr()
 
     @classmethod
@@ -568,8 +605,9 @@ class MxOperand(_Fp4Operand):
         super().__init__(codes, scales)
 
     def dequantize(self, dtype=torch.float32):
+        at = self.addresses()
         out = torch.empty(self.shape, dtype=dtype, device=self.device)
-        _call("nvfp4_mx_dequantize", *self.addresses(), self.rows, self.cols, _addr(out), _out_code(dtype, "dtype"),
+        _call("nvfp4_mx_dequantize", *at, self.rows, self.cols, _addr(out), _out_code(dtype, "dtype"),
               _raw_stream())
         return out
 
@@ -587,6 +625,11 @@ class _MxMade(MxOperand):
         self._buffer = torch.empty(self._at + self._nscales, dtype=_U8, device=device)
 
     def addresses(self):
+        if self._buffer.get_device() != _current():
+            _device_of(self._buffer, "operand")
+        return self._addresses()
+
+    def _addresses(self):
         base = self._buffer.data_ptr()
         return base, base + self._at
 
@@ -636,10 +679,10 @@ def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values
         # a buffer each: what is kept for a backward pass does not hold the other direction
         if rowwise:
             row = _MxMade(rows, cols, dev)
-            q, qs = row.addresses()
+            q, qs = row._addresses()
         if colwise:
             col = _MxMade(cols, rows32, dev)
-            qt, qts = col.addresses()
+            qt, qts = col._addresses()
     if values:
         if rowwise:
             v = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
@@ -669,10 +712,11 @@ def w4a4_gemm(a, w, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
     if K != w.cols:
         raise ValueError(f"a and w must have the same number of columns, got {K} and {w.cols}")
     ydt = _out_code(out_dtype, "out_dtype")
+    ap, wp = a.addresses(), w.addresses()
+    ws = _scratch(workspace) if workspace is not None else \
+        new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), a.device)
     y = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    ws = workspace if workspace is not None else new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), y.device)
-    _call("nvfp4_w4a4_gemm", a.format, *a.addresses(), _addr(a.tensor_scale), *w.addresses(), _addr(w.tensor_scale),
-          M, N, K, y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw_stream())
+    _call("nvfp4_w4a4_gemm", a.format, *ap, _addr(a.tensor_scale), *wp, _addr(w.tensor_scale), M, N, K, y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw_stream())
     return y
 
 
@@ -683,9 +727,11 @@ def mx_linear(x: torch.Tensor, w: MxOperand, out_dtype=torch.float32, workspace=
     if not isinstance(w, MxOperand) or K != w.cols:
         raise ValueError("w must be an MxOperand with x's number of columns")
     N = w.rows
+    wp = w.addresses()
+    ws = _scratch(workspace) if workspace is not None else \
+        new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    ws = workspace if workspace is not None else new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
-    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, *w.addresses(), y.data_ptr(), ydt,
+    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, *wp, y.data_ptr(), ydt,
           ws.data_ptr(), ws.numel(), _raw_stream())
     return y
 
@@ -704,12 +750,12 @@ def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, d
         raise ValueError(f"x_col must be an MxOperand of shape {(K, M32)}")
     if w_col is not None and (not isinstance(w_col, MxOperand) or w_col.shape != (K, N)):
         raise ValueError(f"w_col must be an MxOperand of shape {(K, N)}")
-    dx = torch.empty((M, K), dtype=dx_dtype, device=dy.device) if w_col is not None else None
-    dw = torch.empty((N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
-    ws = workspace if workspace is not None else \
-        new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
     xp = (None, None) if x_col is None else x_col.addresses()
     wp = (None, None) if w_col is None else w_col.addresses()
+    ws = _scratch(workspace) if workspace is not None else \
+        new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
+    dx = torch.empty((M, K), dtype=dx_dtype, device=dy.device) if w_col is not None else None
+    dw = torch.empty((N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
     _call("nvfp4_mx_linear_backward", dy.data_ptr(), dt, ld, M, N, K, *xp, *wp, _addr(dx), xdt, _addr(dw), wdt,
           ws.data_ptr(), ws.numel(), _raw_stream())
     return dx, dw
@@ -728,8 +774,10 @@ def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_lo
     if ib is None or len(shape) != 2:
         raise ValueError("index must be a 2-dimensional int32 or int64 tensor")
     k = shape[1]
-    if shape[0] != T or teacher.shape != shape or not (index.is_cuda and teacher.is_cuda) or \
-            not (index.is_contiguous() and teacher.is_contiguous()):
+    if index.get_device() != _current() or teacher.get_device() != _current():
+        _device_of(index, "index")
+        _device_of(teacher, "teacher")
+    if shape[0] != T or teacher.shape != shape or not (index.is_contiguous() and teacher.is_contiguous()):
         raise ValueError(f"index and teacher must be contiguous CUDA tensors of one shape ({T}, k), got "
                          f"{tuple(shape)} and {tuple(teacher.shape)}")
     if row_weight is not None:
@@ -745,6 +793,8 @@ def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_lo
         rows, cols, lddz, ddt = _matrix(dz, "dz")
         if ddt != zdt or rows != T or cols != V:
             raise ValueError("dz must have z's type and shape")
+    if workspace is not None:
+        _scratch(workspace)
     _call("nvfp4_distill_topk", z.data_ptr(), zdt, T, V, ldz, index.data_ptr(), ib, teacher.data_ptr(), tdt, k,
           temperature, 1 if tail else 0, _addr(row_weight), _addr(grad_loss), ng, _addr(loss), _addr(dz), lddz,
           _addr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream())
@@ -790,6 +840,8 @@ def nvfp4_distill_wait_selftest(z, index, teacher, tail=False, row_weight=None, 
         _need(loss, _F32, (T,), "loss")
     if dz is not None:
         _need(dz, z.dtype, (T, V), "dz")
+    if workspace is not None:
+        _scratch(workspace)
     _call("nvfp4_distill_wait_selftest", z.data_ptr(), zdt, T, V, index.data_ptr(), teacher.data_ptr(), k,
           1 if tail else 0, _addr(row_weight), _addr(loss), _addr(dz), _addr(workspace),
           0 if workspace is None else workspace.numel(), _raw_stream())
