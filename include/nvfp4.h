@@ -471,8 +471,8 @@ nvfp4_status nvfp4_mx_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int6
  *     (and of the rows behind it in the same block) NaN, and is recorded as
  *     NVFP4_ERR_TIMEOUT when there is a workspace.
  * T >= 1; 1 <= V, a row of at most 1638272 bytes; 1 <= k <= 1024; index_bytes
- * 4 or 8; temperature finite and positive.  z, dz 16-byte aligned as every
- * pointer; ldz, lddz >= V arbitrary. */
+ * 4 or 8; temperature positive, it and log2(e) / temperature finite (FP32).
+ * z, dz 16-byte aligned as every pointer; ldz, lddz >= V arbitrary. */
 nvfp4_status nvfp4_distill_topk(const void *z, nvfp4_dtype z_dtype, int64_t T, int64_t V, int64_t ldz,
                                 const void *index, int index_bytes, const void *teacher,
                                 nvfp4_dtype teacher_dtype, int64_t k, float temperature, int rest_class,

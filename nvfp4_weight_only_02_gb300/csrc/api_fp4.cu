@@ -66,7 +66,7 @@ nvfp4_status distill_args(DistillArgs &a, const void *z, nvfp4_dtype z_dtype, in
     const float inv_tau = 1.0f / temperature;
     if (!z || !index || !teacher || (!loss && !dz) || !dtype_ok(z_dtype) || !dtype_ok(teacher_dtype) ||
         (index_bytes != 4 && index_bytes != 8) || !(temperature > 0.0f) || !std::isfinite(temperature) ||
-        !std::isfinite(inv_tau) || inv_tau == 0.0f || (grad_loss && !dz))
+        !std::isfinite(inv_tau * kLog2e) || inv_tau == 0.0f || (grad_loss && !dz))
         return NVFP4_ERR_INVALID_ARG;
     const int64_t size = z_dtype == NVFP4_OUT_FP32 ? 4 : 2;
     // 8 CTAs hold a row, each slice rounded up to 16 bytes

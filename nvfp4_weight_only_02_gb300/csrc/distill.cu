@@ -38,7 +38,6 @@ using namespace sm100;
 namespace {
 
 constexpr int kDsThreads = 256, kDsWarps = kDsThreads / 32;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // 2^x; results below 2^-126 are flushed to 0, which a sum of values in (0, 1]
 // whose largest is 1 cannot notice.

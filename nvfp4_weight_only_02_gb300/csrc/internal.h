@@ -168,6 +168,7 @@ cudaError_t encode_scale_map(CUtensorMap *map, const uint8_t *scales, uint64_t k
 // Distillation loss and gradient (csrc/distill.cu).
 constexpr int kDistillMaxK = 1024;             // teacher entries per row
 constexpr int64_t kDistillMaxSlice = 200 * 1024;  // bytes of a row one CTA (of up to 8) holds
+constexpr float kLog2e = 1.4426950408889634f;  // exponents are base 2 and scaled by kLog2e * inv_tau, which is finite
 struct DistillArgs {
     const void *z;
     bool z_fp32;

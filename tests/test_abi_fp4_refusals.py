@@ -26,3 +26,13 @@ def test_distill_wait_selftest(lib):
     for kw in (dict(z=bad), dict(i=bad), dict(t=bad), dict(w=bad), dict(loss=bad), dict(dz=bad)):
         assert f(**kw) == binding.ERR_ALIGNMENT, kw
     assert f(ws=good, n=255) == binding.ERR_WORKSPACE
+
+
+def test_distill_temperature_whose_reciprocal_leaves_fp32(lib):
+    """The kernels scale by log2(e) / temperature: below 4.24e-39 that is beyond FP32 although 1 / temperature is not."""
+    f = lambda tau: lib.nvfp4_distill_topk(good, 0, 2, 100, 100, good, 4, good, 0, 4, tau, 0, None, None, 0, good, good,  # noqa: E731
+                                           100, good, 255, None)
+    for tau in (3e-39, 4.2e-39):
+        assert f(tau) == binding.ERR_INVALID_ARG, tau
+    for tau in (4.3e-39, 1.0, 3e38):
+        assert f(tau) == binding.ERR_WORKSPACE, tau    # the argument passes
