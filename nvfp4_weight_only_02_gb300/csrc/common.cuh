@@ -192,6 +192,19 @@ __device__ __forceinline__ void pdl_wait()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// 16 bytes that are used once.  Not through the read-only path, which may not
+// be used for what another kernel writes while this one runs: a dependent
+// launch starts before the kernel that produces its input has ended.
+__device__ __forceinline__ uint4 ld_once_u4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint4 ld_stream_u4(const void *p)
 {
     uint4 v;
