@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kWsThreads, 2)
         constexpr uint32_t id2 = idesc_fp4(kWsRows, NT, kNv ? 0 : 1, 2);
         if (elect_one()) {
             bool ok = !S::kOwn || mbar_wait(x_full, 0);
+            int done = 0;   // stages multiplied, if a wait gives up
             int st = 0, st2 = kStages - S::kSfBufs, sf = 0;  // st2: the stage kSfBufs steps ago
             uint32_t ph = 0, ph2 = 1;
             for (int i = 0; i < nk && ok; i++) {
@@ -165,8 +166,10 @@ __global__ void __launch_bounds__(kWsThreads, 2)
                 // stages implies, and this stage's operands have landed
                 ok = (kStages <= S::kSfBufs || i < S::kSfBufs || mbar_wait(&empty[st2], ph2)) &&
                      mbar_wait(&full[st], ph);
-                if (!ok)
+                if (!ok) {
+                    done = i;
                     break;
+                }
                 tc_fence_after();
                 const int sx = S::kOwn ? i : st;
                 const uint64_t wd = smem_desc_sw128(smem_addr(sW + st * kWsRows * 128));
@@ -203,8 +206,13 @@ __global__ void __launch_bounds__(kWsThreads, 2)
                     ph2 ^= 1;
                 }
             }
-            if (!ok)
+            if (!ok) {
+                // the copies that the stages multiplied so far let go land before the CTA leaves, and the epilogue
+                // hears of the MMAs issued: it waits for them before TMEM is given back
                 record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                ring_drain(full, kStages, done, min(nk, done + kStages));
+                mma_commit(acc_full);
+            }
         }
     } else {
         pdl_wait();
@@ -244,8 +252,13 @@ __global__ void __launch_bounds__(kWsThreads, 2)
             fence_proxy_async_smem();
             mbar_arrive(x_full);
         }
-        if (!mbar_wait_warp(acc_full, 0) && threadIdx.x == 0)
-            record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+        if (!mbar_wait_warp(acc_full, 0)) {
+            if (threadIdx.x == 0)
+                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+            // longer than the issuing thread can take over its own waits
+            for (int i = 0; i < 2 * nk + kStages + 4 && !mbar_wait_warp(acc_full, 0); i++) {
+            }
+        }
         tc_fence_after();
     }
     __syncwarp();

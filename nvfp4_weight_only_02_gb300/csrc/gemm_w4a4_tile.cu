@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
     uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    volatile uint32_t *s_loaded = s_tmem + 2, *s_issued = s_tmem + 3;   // stages copied and multiplied
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = (int)cluster_ctarank();
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_init(&acc_empty[0], 2 * kTlEpiWarps);
         mbar_init(&acc_empty[1], 2 * kTlEpiWarps);
         *s_abort = 0;
+        *s_issued = 0;
         mbar_fence_init();
     }
     if (warp == kTlEpiWarps + 1)
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                 if (i2 >= (uint32_t)kStages && !mbar_wait(&empty[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
                     fail();
             }
+            *s_loaded = it;
         }
     } else if (warp == kTlEpiWarps + 1) {
         // ---------------- MMA, by one thread of the pair's leader.  What this loop takes per stage bounds
@@ -325,6 +328,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                     break;
                 }
             }
+            *s_issued = it;
         }
     } else {
         // ---------------- epilogue: warp w has lanes 32 (w % 4) .. + 31 and every other 32 columns, the columns
@@ -431,6 +435,15 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (crank == 0 && warp == kTlEpiWarps + 1 && *s_abort) {
+        // after a wait that gave up: copies on their way land, and MMAs issued are done, before either CTA leaves (the
+        // leader's barriers count both CTAs' copies; what the other one issued beyond them is as old as its own wait)
+        const uint32_t loaded = *s_loaded, issued = *s_issued;
+        ring_drain(full, kStages, loaded > (uint32_t)kStages ? loaded - kStages : 0u, loaded);
+        if (issued > 0)
+            ring_drain(empty, kStages, issued - 1, issued);
+        __syncwarp();
+    }
     cluster_sync();  // neither CTA leaves while the other may still signal or read it
     if (warp == kTlEpiWarps + 1) {
         tc_fence_after();

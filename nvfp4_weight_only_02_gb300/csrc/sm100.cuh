@@ -74,6 +74,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     }
 }
 
+// After a wait that gave up: wait for uses [from, to) of a ring of barriers,
+// one after the other, until one of them gives up too.  A call, so that kernels
+// which run for a few microseconds fetch no more code.
+static __device__ __noinline__ void ring_drain(uint64_t *bar, uint32_t stages, uint32_t from, uint32_t to)
+{
+    for (uint32_t i = from; i < to && mbar_wait(&bar[i % stages], (i / stages) & 1); i++) {
+    }
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y)
 {
