@@ -238,7 +238,7 @@ nvfp4_status nvfp4_mx_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, in
         return NVFP4_ERR_WORKSPACE;
     NVFP4_TRY_DEVICE(dev);
     W4A4Args a = {};
-    if (w4a4_takes_tokens(M, N, K, *dev)) {
+    if (w4a4_takes_tokens(M, N, K, x_dtype == NVFP4_OUT_FP32, *dev)) {
         a.x = x;
         a.x_fp32 = x_dtype == NVFP4_OUT_FP32;
         a.ldx = ldx;

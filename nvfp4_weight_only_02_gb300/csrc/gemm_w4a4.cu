@@ -333,13 +333,6 @@ __global__ void __launch_bounds__(kWsThreads, 2)
     }
 }
 
-// K is split while the tiles leave CTA places free: two per SM, at most 8 CTAs to a cluster.
-int split_for(int64_t tiles, int64_t K, const DeviceInfo &dev)
-{
-    const int64_t ksteps = (K + kWsK - 1) / kWsK;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({8, ksteps, 2 * dev.num_sms / tiles}));
-}
-
 template <bool kNv, int NT, Tokens kTok>
 cudaError_t run_stream(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 {
@@ -368,7 +361,7 @@ cudaError_t run_stream(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
     p.ktiles = (int)((a.K + per_tile - 1) / per_tile);
     p.mtiles = (int)((a.M + NT - 1) / NT);
     const int64_t tiles = (int64_t)p.mtiles * ((a.N + kWsRows - 1) / kWsRows);
-    p.split = split_for(tiles, a.K, dev);
+    p.split = ws_split(tiles, a.K, dev.num_sms);
     const int nk = (p.ksteps + p.split - 1) / p.split;
     p.stages = S::stages(nk);
     p.early = a.after_quantise ? 1 : 0;
@@ -418,21 +411,9 @@ cudaError_t run_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)
 
 }  // namespace
 
-bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev)
+bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, bool fp32, const DeviceInfo &dev)
 {
-    // Every CTA quantises its part of K for all tokens again, so what it takes and how many turns of CTAs do that
-    // decide (bf16, one kernel / with a quantiser of its own, us): N = 18944, K = 3584, split 2: 4 tokens (7168
-    // elements a CTA) 10.4 / 11.2, 8 (14336) 12.0 / 11.2; N = K = 3584, split 8: 12 (6144) 6.2 / 6.5, 16 (8192)
-    // 7.3 / 6.5; N = 27648, K = 5120, one CTA a tile: 1 (5120) 15.4 / 16.6, 4 (20480) 19.8 / 16.8; N = 76032,
-    // K = 3584, two turns: 1 (3584) 26.4 / 27.8, 2 (7168) 29.3 / 28.0.
-    if (M > 16)
-        return false;
-    const int64_t tiles = (N + kWsRows - 1) / kWsRows, ksteps = (K + kWsK - 1) / kWsK, split = split_for(tiles, K, dev);
-    const int64_t nk = (ksteps + split - 1) / split, turns = (tiles * split + 2 * dev.num_sms - 1) / (2 * dev.num_sms);
-    if (M * nk * kWsK * turns > 7680)
-        return false;
-    // at least three stages of weights beside the tokens
-    return nk <= 64 && WsShape<false, 16, kBf16>::stages((int)nk) >= std::min<int64_t>(3, std::max<int64_t>(nk, 2));
+    return ws_takes_tokens(M, N, K, fp32, dev.num_sms);
 }
 
 cudaError_t launch_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev)

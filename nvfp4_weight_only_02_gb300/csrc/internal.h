@@ -156,8 +156,8 @@ struct W4A4Args {
     bool after_quantise;           // launched right behind the quantiser of A on the same stream
 };
 cudaError_t launch_w4a4(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
-// Whether launch_w4a4 takes unquantised tokens (MXFP4) of these sizes.
-bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev);
+// Whether launch_w4a4 takes unquantised tokens (MXFP4) of these sizes and type.
+bool w4a4_takes_tokens(int64_t M, int64_t N, int64_t K, bool fp32, const DeviceInfo &dev);
 // The variant for many tokens (csrc/gemm_w4a4_tile.cu).
 cudaError_t launch_w4a4_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo &dev);
 // Tiled scales (row_tiles x ktiles tiles of 512 bytes) as a tensor map whose
