@@ -164,11 +164,13 @@ def _space(workspace):
     return ctypes.c_void_p(workspace.data_ptr())
 
 
-def _need(t, dtype, shape, name):
-    _device_of(t, name)
+def _need(t, dtype, shape, name, dev=None):
+    """dev: the current device, where the caller has it at hand."""
+    if t.get_device() != (_current() if dev is None else dev):
+        _device_of(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -256,21 +258,22 @@ def _projection_array(entries):
     if ydt not in (torch.float32, torch.bfloat16):
         raise ValueError("y must be float32 or bfloat16")
     arr = (Projection * len(entries))()
+    dev = _current()
     for i, (x, codes, scales, ts, a, b, s, z, y) in enumerate(entries):
         K = x.shape[1]
         N = codes.shape[0]
-        _need(x, torch.bfloat16, (M, K), f"x[{i}]")
-        _need(codes, torch.uint8, (N, K // 2), f"codes[{i}]")
-        _need(scales, torch.uint8, (N, K // 16), f"scales[{i}]")
-        _need(ts, torch.float32, (1,), f"tensor_scale[{i}]")
+        _need(x, torch.bfloat16, (M, K), f"x[{i}]", dev)
+        _need(codes, torch.uint8, (N, K // 2), f"codes[{i}]", dev)
+        _need(scales, torch.uint8, (N, K // 16), f"scales[{i}]", dev)
+        _need(ts, torch.float32, (1,), f"tensor_scale[{i}]", dev)
         if (a is None) != (r == 0):
             raise ValueError("every entry of a list has the same LoRA rank")
         if a is not None:
-            _need(a, torch.bfloat16, (r, K), f"lora_a[{i}]")
-            _need(b, torch.bfloat16, (N, r), f"lora_b[{i}]")
+            _need(a, torch.bfloat16, (r, K), f"lora_a[{i}]", dev)
+            _need(b, torch.bfloat16, (N, r), f"lora_b[{i}]", dev)
         if z is not None:
-            _need(z, torch.float32, (K,), f"noise[{i}]")
-        _need(y, ydt, (M, N), f"y[{i}]")
+            _need(z, torch.float32, (K,), f"noise[{i}]", dev)
+        _need(y, ydt, (M, N), f"y[{i}]", dev)
         arr[i] = Projection(_ptr(x), _ptr(codes), _ptr(scales), _ptr(ts), _ptr(a), _ptr(b), _ptr(z), _ptr(y),
                             N, K, float(s))
     return arr, M, r, OUT_FP32 if ydt == torch.float32 else OUT_BF16
