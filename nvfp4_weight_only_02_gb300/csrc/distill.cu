@@ -693,15 +693,18 @@ __global__ void __launch_bounds__(kDsThreads)
 // Two CTAs per SM, persistent over the rows, a row each.  A cluster per row
 // spends more on starting clusters and waiting for the slowest CTA than on the
 // logits (4096 rows of 131072 bf16 logits: 500 us, 63 % of the copy bandwidth);
-// here a row's chunks pass through a ring in shared memory twice (389 us,
-// 81 %).  The chunks that the ring still holds after the first pass are used
-// from there, the ones before them come again from L2, which holds the rest of
-// 304 rows of 256 KB; the gradient is stored to be evicted first, so that it
-// does not push them out (with plain stores 417 us).  One warp copies, the others are consumers.  One CTA of
-// 1024 threads per SM was slower (475 us against 424 at the time): its
-// reductions and the turn from one pass to the other leave the SM without work,
-// which the other CTA fills here.
-// What bounds it now is issue: about 50 instructions per 8 logits and pass.
+// here a row's chunks pass through a ring in shared memory twice (382 us,
+// 83 %).  The chunks that the ring still holds after the first pass are used
+// from there, the ones before them come again, most of them from L2; the
+// gradient of aligned rows is stored to be evicted first, so that it does not
+// push them out (with plain stores 407 us).  One warp copies, the others are
+// consumers.  One CTA of 1024 threads per SM was slower (475 us against 424 at
+// the time): its reductions and the turn from one pass to the other leave the
+// SM without work, which the other CTA fills here.
+// What bounds it is DRAM: of 1024 rows a quarter of what is read again (16 % of
+// the logits; 43 % with plain stores) misses L2, and with that it moves 6.1 TB/s
+// at 4096 rows, 89 % of the copy rate.  Issue (about 50 instructions per 8
+// logits and pass) takes 64 % of the slots.
 constexpr int kDtThreads = 512, kDtPerSm = 2, kDtWarps = kDtThreads / 32 - 1, kDtConsumers = 32 * kDtWarps;
 constexpr int kDtEach = 4;                       // 16-byte vectors of a chunk that a consumer takes
 constexpr int kDtVecs = kDtEach * kDtConsumers;
@@ -1059,7 +1062,7 @@ __global__ void __launch_bounds__(kDtThreads, kDtPerSm)
                     } else if (kFast && c * kDtVecs >= j0 && (c + 1) * kDtVecs <= j1) {
                         uint4 *dst = reinterpret_cast<uint4 *>(dzr + (int64_t)j * NE - sh);
                         // by two: all four need more than the 64 registers of two CTAs, and their spills
-                        // cost 475 us instead of 402 at 4096 x 131072
+                        // cost 475 us instead of 402 at 4096 x 131072 (by two, 4 bytes are spilt in bf16)
 #pragma unroll 2
                         for (int u = 0; u < kDtEach; u++) {
                             float v[NE];
@@ -1163,9 +1166,13 @@ cudaError_t run_distill(const DistillArgs &a, cudaStream_t s, const DeviceInfo &
 // of 131072 logits: 96 rows 16.0 / 19.4, 152 rows 27.0 / 21.7, 304 rows 44.3 /
 // 35.6, 2432 rows 283 / 256 (all with plain stores); 2432 rows of 64 KB 54.3 /
 // 79.5, of 96 KB 103.4 / 105.7.  The loss alone, 304 rows: 8 KB 4.0 / 5.0, 64 KB
-// 5.7 / 7.2, 128 KB 16.3 / 10.4.  So the stream takes rows above 96 KB when
-// there is one for every SM, as far as its threads hold the teacher's entries
-// and its ring has two chunks.
+// 5.7 / 7.2, 128 KB 16.3 / 10.4.  FP32 rows of 512 KB, with a gradient: 160 rows
+// 49.5 / 45.4, 608 rows 146 / 138, 2432 rows 529 / 541; of 594 KB: 54.1 / 51.3,
+// 159 / 161, 581 / 631; the loss alone, 608 rows of 512 KB 96.2 / 51.4, 2432 of
+// 594 KB 368 / 208.  So the stream takes rows above 96 KB when there is one for
+// every SM, as far as its threads hold the teacher's entries and its ring has
+// two chunks; where thousands of rows above 512 KB want a gradient it loses 2 to
+// 8 %, since L2 then holds little of what is read again.
 //
 // Within clusters, one entry a thread for up to 256 of them, else four: most
 // teachers keep fewer than 256, and the other three's registers and branches

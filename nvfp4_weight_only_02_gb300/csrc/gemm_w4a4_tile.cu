@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                         stage_and_store(w, n0);
                     }
                 } else if (m0 + lane < p.M) {
-                    // rows of Y that do not start on 16-byte boundaries
+                    // rows of Y that do not start on 16-byte boundaries: a lane writes its row element by element,
+                    // and the stores bound the kernel (4096 x 18945 x 3584: bf16 695 us, FP32 563; 18944: 85 and 104)
                     const size_t at = (size_t)(m0 + lane) * p.N + n0;
 #pragma unroll
                     for (int c = 0; c < 32; c++) {

@@ -71,8 +71,11 @@ struct MqParams {
 // What bounds it: 2 (4) bytes read and 17/32 written an element and direction.
 // 16384 x 3584 bf16: rows alone 23.2 us (6.4 TB/s, 94 % of the copy rate), with
 // values 41.9 us (94 %); columns alone 30.1 us (73 %); both 37.8 us (70 %), with
-// values 65.9 us (93 %).  8192 x 3584 FP32, both: 32.0 us (68 %).  The column
-// direction is bound by issue: about 15 instructions an element over both.
+// values 65.9 us (93 %).  8192 x 3584 FP32, both: 32.0 us (68 %).  Both directions
+// are bound by issue, 17 instructions an element: 71 % of the slots over the
+// whole kernel, and a warp waits for its slot longer than for anything else; the
+// rest goes to the first loads and to shared memory (40 % of its wavefronts are
+// bank conflicts).
 // Measured against it, both directions: codes straight from the column pass's
 // registers, 16 bytes a column, 40.9 us; a persistent CTA with tiles brought by
 // TMA 41.5 us (rows 26.2); registers capped for five CTAs an SM 44.5 us.
