@@ -143,7 +143,9 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-_current = torch._C._cuda_getDevice   # index of the current device
+# index of the current device, and the raw handle of a device's current stream (no Stream object is built)
+_current = getattr(torch._C, "_cuda_getDevice", None)
+_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _device_of(t, name):
@@ -502,8 +504,7 @@ def _out_code(dtype, name):
 
 
 def _raw_stream():
-    # torch.cuda.current_stream() without building the Stream object
-    return torch._C._cuda_getCurrentRawStream(_current())
+    return _raw(_current())
 
 
 def _call(name, *args):
@@ -512,10 +513,10 @@ def _call(name, *args):
         raise NVFP4Error(st, name)
 
 
-def _matrix(t, name):
-    """Checks a 2-D matrix on the current device whose rows are contiguous; returns (rows, cols, row stride in
+def _matrix(t, name, dev):
+    """Checks a 2-D matrix on the current device, dev, whose rows are contiguous; returns (rows, cols, row stride in
     elements, type code)."""
-    if t.get_device() != _current():
+    if t.get_device() != dev:
         _device_of(t, name)
     code = _DTYPE_CODE.get(t.dtype)
     shape = t.shape
@@ -533,13 +534,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(workspace):
-    """Checks a workspace that the caller keeps."""
-    if workspace.dtype is not _U8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous torch.uint8 tensor")
-    if workspace.get_device() != _current():
-        _device_of(workspace, "workspace")
-    return workspace
+def _bad_scratch(workspace):
+    _device_of(workspace, "workspace")
+    raise ValueError("workspace must be a contiguous torch.uint8 tensor")
+
+
+def _operand_elsewhere(index, dev):
+    raise ValueError(f"operands must be on the current device, cuda:{dev}, got cuda:{index}")
 
 
 def nvfp4_tiled_scale_bytes(rows: int, cols: int, fmt: int) -> int:
@@ -572,7 +573,7 @@ class _Fp4Operand:
             if tensor_scale.get_device() != codes.get_device():
                 raise ValueError("codes and tensor_scale must be on one device")
         self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
-        self.rows, self.cols = rows, cols
+        self.rows, self.cols, self.index = rows, cols, codes.get_device()
 
     @property
     def shape(self):
@@ -584,8 +585,6 @@ class _Fp4Operand:
 
     def addresses(self):
         """Of the codes and of the scales."""
-        if self.codes.get_device() != _current():
-            _device_of(self.codes, "operand")
         return self.codes.data_ptr(), self.scales.data_ptr()
 
     @classmethod
@@ -608,9 +607,10 @@ class MxOperand(_Fp4Operand):
         super().__init__(codes, scales)
 
     def dequantize(self, dtype=torch.float32):
-        at = self.addresses()
+        if self.index != _current():
+            _operand_elsewhere(self.index, _current())
         out = torch.empty(self.shape, dtype=dtype, device=self.device)
-        _call("nvfp4_mx_dequantize", *at, self.rows, self.cols, _addr(out), _out_code(dtype, "dtype"),
+        _call("nvfp4_mx_dequantize", *self.addresses(), self.rows, self.cols, _addr(out), _out_code(dtype, "dtype"),
               _raw_stream())
         return out
 
@@ -621,18 +621,13 @@ class _MxMade(MxOperand):
 
     tensor_scale = None
 
-    def __init__(self, rows, cols, device):
-        self.rows, self.cols = rows, cols
+    def __init__(self, rows, cols, device, index):
+        self.rows, self.cols, self.index = rows, cols, index
         self._at = (rows * cols // 2 + 15) & ~15
         self._nscales = (rows + 127) // 128 * ((cols + 127) // 128) * 512
         self._buffer = torch.empty(self._at + self._nscales, dtype=_U8, device=device)
 
     def addresses(self):
-        if self._buffer.get_device() != _current():
-            _device_of(self._buffer, "operand")
-        return self._addresses()
-
-    def _addresses(self):
         base = self._buffer.data_ptr()
         return base, base + self._at
 
@@ -674,24 +669,25 @@ def mx_quantize(x: torch.Tensor, rowwise=True, colwise=False, codes=True, values
     """MXFP4 quantisation of x (rows, cols), bf16 or float32, along its columns (rowwise) and/or its rows (colwise).
     codes: return operands for products; values: return x as the codes stand for it (bf16), e.g. for a
     straight-through forward."""
-    rows, cols, ld, dt = _matrix(x, "x")
+    index = _current()
+    rows, cols, ld, dt = _matrix(x, "x", index)
     dev = x.device
     rows32 = (rows + 31) // 32 * 32
     row = col = v = vt = q = qs = qt = qts = None
     if codes:
         # a buffer each: what is kept for a backward pass does not hold the other direction
         if rowwise:
-            row = _MxMade(rows, cols, dev)
-            q, qs = row._addresses()
+            row = _MxMade(rows, cols, dev, index)
+            q, qs = row.addresses()
         if colwise:
-            col = _MxMade(cols, rows32, dev)
-            qt, qts = col._addresses()
+            col = _MxMade(cols, rows32, dev, index)
+            qt, qts = col.addresses()
     if values:
         if rowwise:
             v = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
         if colwise:
             vt = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    _call("nvfp4_mx_quantize", x.data_ptr(), dt, rows, cols, ld, q, qs, _addr(v), qt, qts, _addr(vt), _raw_stream())
+    _call("nvfp4_mx_quantize", x.data_ptr(), dt, rows, cols, ld, q, qs, _addr(v), qt, qts, _addr(vt), _raw(index))
     return MxQuantized(row, col, v, vt)
 
 
@@ -714,28 +710,43 @@ def w4a4_gemm(a, w, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
     M, N, K = a.rows, w.rows, a.cols
     if K != w.cols:
         raise ValueError(f"a and w must have the same number of columns, got {K} and {w.cols}")
-    ydt = _out_code(out_dtype, "out_dtype")
-    ap, wp = a.addresses(), w.addresses()
-    ws = _scratch(workspace) if workspace is not None else \
-        new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), a.device)
+    ydt = _DTYPE_CODE.get(out_dtype)
+    if ydt is None:
+        _out_code(out_dtype, "out_dtype")
+    dev = _current()
+    if a.index != dev or w.index != dev:
+        _operand_elsewhere(a.index if a.index != dev else w.index, dev)
+    ws = workspace
+    if ws is None:
+        ws = new_workspace(nvfp4_w4a4_workspace_bytes(M, N, K), a.device)
+    elif ws.get_device() != dev or ws.dtype is not _U8 or not ws.is_contiguous():
+        _bad_scratch(ws)
     y = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    _call("nvfp4_w4a4_gemm", a.format, *ap, _addr(a.tensor_scale), *wp, _addr(w.tensor_scale), M, N, K, y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw_stream())
+    _call("nvfp4_w4a4_gemm", a.format, *a.addresses(), _addr(a.tensor_scale), *w.addresses(), _addr(w.tensor_scale),
+          M, N, K, y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw(dev))
     return y
 
 
 def mx_linear(x: torch.Tensor, w: MxOperand, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
     """Y (M, N) = Q(X) W^T: x (M, K) bf16 or float32, quantised to MXFP4 on the way."""
-    M, K, ld, dt = _matrix(x, "x")
-    ydt = _out_code(out_dtype, "out_dtype")
+    dev = _current()
+    M, K, ld, dt = _matrix(x, "x", dev)
+    ydt = _DTYPE_CODE.get(out_dtype)
+    if ydt is None:
+        _out_code(out_dtype, "out_dtype")
     if not isinstance(w, MxOperand) or K != w.cols:
         raise ValueError("w must be an MxOperand with x's number of columns")
+    if w.index != dev:
+        _operand_elsewhere(w.index, dev)
     N = w.rows
-    wp = w.addresses()
-    ws = _scratch(workspace) if workspace is not None else \
-        new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
+    ws = workspace
+    if ws is None:
+        ws = new_workspace(nvfp4_mx_linear_workspace_bytes(M, N, K), x.device)
+    elif ws.get_device() != dev or ws.dtype is not _U8 or not ws.is_contiguous():
+        _bad_scratch(ws)
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, *wp, y.data_ptr(), ydt,
-          ws.data_ptr(), ws.numel(), _raw_stream())
+    _call("nvfp4_mx_linear", x.data_ptr(), dt, ld, M, N, K, *w.addresses(), y.data_ptr(), ydt,
+          ws.data_ptr(), ws.numel(), _raw(dev))
     return y
 
 
@@ -743,7 +754,8 @@ def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, d
                        workspace=None):
     """(dX (M, K), dW (N, K)) of Y = X W^T with straight-through MXFP4 quantisers.  dy (M, N) bf16 or float32;
     x_col, w_col: mx_quantize(..., colwise=True).col of X and W.  w_col None: no dX; x_col None: no dW."""
-    M, N, ld, dt = _matrix(dy, "dy")
+    dev = _current()
+    M, N, ld, dt = _matrix(dy, "dy", dev)
     xdt, wdt = _out_code(dx_dtype, "dx_dtype"), _out_code(dw_dtype, "dw_dtype")
     if x_col is None and w_col is None:
         raise ValueError("one of x_col and w_col is needed")
@@ -753,14 +765,20 @@ def mx_linear_backward(dy: torch.Tensor, x_col, w_col, dx_dtype=torch.float32, d
         raise ValueError(f"x_col must be an MxOperand of shape {(K, M32)}")
     if w_col is not None and (not isinstance(w_col, MxOperand) or w_col.shape != (K, N)):
         raise ValueError(f"w_col must be an MxOperand of shape {(K, N)}")
+    for operand in (x_col, w_col):
+        if operand is not None and operand.index != dev:
+            _operand_elsewhere(operand.index, dev)
     xp = (None, None) if x_col is None else x_col.addresses()
     wp = (None, None) if w_col is None else w_col.addresses()
-    ws = _scratch(workspace) if workspace is not None else \
-        new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
+    ws = workspace
+    if ws is None:
+        ws = new_workspace(nvfp4_mx_linear_backward_workspace_bytes(M, N, K), dy.device)
+    elif ws.get_device() != dev or ws.dtype is not _U8 or not ws.is_contiguous():
+        _bad_scratch(ws)
     dx = torch.empty((M, K), dtype=dx_dtype, device=dy.device) if w_col is not None else None
     dw = torch.empty((N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
     _call("nvfp4_mx_linear_backward", dy.data_ptr(), dt, ld, M, N, K, *xp, *wp, _addr(dx), xdt, _addr(dw), wdt,
-          ws.data_ptr(), ws.numel(), _raw_stream())
+          ws.data_ptr(), ws.numel(), _raw(dev))
     return dx, dw
 
 
@@ -770,37 +788,39 @@ _INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
 
 def nvfp4_distill_topk(z, index, teacher, temperature, tail, row_weight, grad_loss, loss, dz, workspace):
     """The C entry point on tensors; loss or dz may be None (see include/nvfp4.h)."""
-    T, V, ldz, zdt = _matrix(z, "z")
+    dev = _current()
+    T, V, ldz, zdt = _matrix(z, "z", dev)
     tdt = _out_code(teacher.dtype, "teacher")
     ib = _INDEX_BYTES.get(index.dtype)
     shape = index.shape
     if ib is None or len(shape) != 2:
         raise ValueError("index must be a 2-dimensional int32 or int64 tensor")
     k = shape[1]
-    if index.get_device() != _current() or teacher.get_device() != _current():
+    if index.get_device() != dev or teacher.get_device() != dev:
         _device_of(index, "index")
         _device_of(teacher, "teacher")
     if shape[0] != T or teacher.shape != shape or not (index.is_contiguous() and teacher.is_contiguous()):
         raise ValueError(f"index and teacher must be contiguous CUDA tensors of one shape ({T}, k), got "
                          f"{tuple(shape)} and {tuple(teacher.shape)}")
     if row_weight is not None:
-        _need(row_weight, _F32, (T,), "row_weight")
+        _need(row_weight, _F32, (T,), "row_weight", dev)
     ng = 0
     if grad_loss is not None:
         ng = grad_loss.numel()
-        _need(grad_loss, _F32, (T,) if ng != 1 else grad_loss.shape, "grad_loss")
+        _need(grad_loss, _F32, (T,) if ng != 1 else grad_loss.shape, "grad_loss", dev)
     if loss is not None:
-        _need(loss, _F32, (T,), "loss")
+        _need(loss, _F32, (T,), "loss", dev)
     lddz = V
     if dz is not None:
-        rows, cols, lddz, ddt = _matrix(dz, "dz")
+        rows, cols, lddz, ddt = _matrix(dz, "dz", dev)
         if ddt != zdt or rows != T or cols != V:
             raise ValueError("dz must have z's type and shape")
-    if workspace is not None:
-        _scratch(workspace)
+    if workspace is not None and not (workspace.get_device() == dev and workspace.dtype is _U8 and
+                                      workspace.is_contiguous()):
+        _bad_scratch(workspace)
     _call("nvfp4_distill_topk", z.data_ptr(), zdt, T, V, ldz, index.data_ptr(), ib, teacher.data_ptr(), tdt, k,
           temperature, 1 if tail else 0, _addr(row_weight), _addr(grad_loss), ng, _addr(loss), _addr(dz), lddz,
-          _addr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream())
+          _addr(workspace), 0 if workspace is None else workspace.numel(), _raw(dev))
 
 
 def distill_topk_loss(z, index, teacher, temperature=1.0, tail=False, row_weight=None, workspace=None):
@@ -832,7 +852,8 @@ def distill_topk_grad(z, index, teacher, grad_loss=None, temperature=1.0, tail=F
 
 def nvfp4_distill_wait_selftest(z, index, teacher, tail=False, row_weight=None, loss=None, dz=None, workspace=None):
     """The distillation kernels with waits that give up at once (see include/nvfp4.h): z (T, V) contiguous."""
-    T, V, ldz, zdt = _matrix(z, "z")
+    dev = _current()
+    T, V, ldz, zdt = _matrix(z, "z", dev)
     k = index.shape[1]
     _need(z, z.dtype, (T, V), "z")
     _need(index, torch.int32, (T, k), "index")
@@ -843,8 +864,9 @@ def nvfp4_distill_wait_selftest(z, index, teacher, tail=False, row_weight=None, 
         _need(loss, _F32, (T,), "loss")
     if dz is not None:
         _need(dz, z.dtype, (T, V), "dz")
-    if workspace is not None:
-        _scratch(workspace)
+    if workspace is not None and not (workspace.get_device() == dev and workspace.dtype is _U8 and
+                                      workspace.is_contiguous()):
+        _bad_scratch(workspace)
     _call("nvfp4_distill_wait_selftest", z.data_ptr(), zdt, T, V, index.data_ptr(), teacher.data_ptr(), k,
           1 if tail else 0, _addr(row_weight), _addr(loss), _addr(dz), _addr(workspace),
-          0 if workspace is None else workspace.numel(), _raw_stream())
+          0 if workspace is None else workspace.numel(), _raw(dev))

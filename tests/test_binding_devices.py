@@ -46,7 +46,7 @@ def device_zero(monkeypatch):
 
     monkeypatch.setattr(nv, "_current", lambda: 0)
     monkeypatch.setattr(nv, "_call", reached)
-    monkeypatch.setattr(nv, "_raw_stream", lambda: 0)
+    monkeypatch.setattr(nv, "_raw", lambda device: 0)
     monkeypatch.setattr(nv, "_stream", lambda: 0)
     monkeypatch.setattr(nv, "load", reached)
     monkeypatch.setattr(nv, "_lib", None)
