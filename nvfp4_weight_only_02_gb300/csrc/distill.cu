@@ -386,6 +386,16 @@ __device__ __forceinline__ float entry_value(const DistillArgs &a, int64_t at)
                       : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.val)[at]);
 }
 
+// After a wait for a copy that gave up: reported where there is a status word,
+// and waited for once more, so that the CTA does not leave with it on its way.
+// (A call: few rows take microseconds, in which more code shows.)
+__device__ __noinline__ void copy_gave_up(uint32_t *ctl, uint64_t *bar)
+{
+    if (ctl)
+        record_status(ctl, NVFP4_ERR_TIMEOUT);
+    mbar_wait(bar, 0);
+}
+
 // One row per cluster of C CTAs; CTA `rank` takes logits [rank L, rank L + L).
 // kEntries: teacher entries a thread holds.
 template <typename T, bool kGrad, int kEntries>
@@ -489,11 +499,8 @@ __global__ void __launch_bounds__(kDsThreads)
     if (C > 1)
         cluster_arrive();  // matched below: every CTA of the cluster runs before anyone writes to it
     const bool landed = len <= 0 || (!a.give_up && mbar_wait(&s_bar, 0));
-    if (!landed) {
-        if (a.ctl)
-            record_status(a.ctl, NVFP4_ERR_TIMEOUT);
-        mbar_wait(&s_bar, 0);   // once more: the CTA does not leave with copies on their way
-    }
+    if (!landed)
+        copy_gave_up(a.ctl, &s_bar);
 
     // elements of the first and last 16 bytes outside the slice: -inf
     if (tid < NE && len > 0) {
