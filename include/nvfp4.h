@@ -489,6 +489,141 @@ nvfp4_status nvfp4_distill_wait_selftest(const void *z, nvfp4_dtype z_dtype, int
                                          const float *row_weight, float *loss, void *dz, void *workspace,
                                          size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Mixtures of experts on MXFP4 operands: routing, the layer with one weight
+ * matrix an expert and ragged numbers of rows, and the weighted sum back to
+ * the tokens, forward and backward.
+ *
+ * A token t has k choices; slot t k + j is choice j of token t.  The slots
+ * that have an expert are grouped: sorted by expert, in the order of their
+ * numbers within one.  Rows of the experts' inputs and outputs are compact in
+ * that order: row r belongs to slot order[r].  Rows behind the last one (slots
+ * without an expert leave some) are neither read nor written.  The grouping is
+ * held in a PLAN, a device buffer of nvfp4_moe_plan_bytes(T, k, E) bytes that
+ * the calls below read (int32 arrays, at the byte offsets that
+ * nvfp4_moe_plan_part gives):
+ *   NVFP4_MOE_OFFSETS:  E + 1: rows offsets[e] .. offsets[e + 1] - 1 are expert e's;
+ *   NVFP4_MOE_ORDER:    T k: slot of each row, -1 behind the last one;
+ *   NVFP4_MOE_POSITION: T k: row of each slot, -1 without an expert.
+ * 1 <= T, T k <= 2^24, 1 <= k <= 32, 1 <= E <= 1024.
+ */
+typedef enum nvfp4_moe_part {
+    NVFP4_MOE_OFFSETS = 0,
+    NVFP4_MOE_ORDER = 1,
+    NVFP4_MOE_POSITION = 2
+} nvfp4_moe_part;
+typedef enum nvfp4_moe_scoring {
+    NVFP4_MOE_SOFTMAX = 0,
+    NVFP4_MOE_SIGMOID = 1
+} nvfp4_moe_scoring;
+
+size_t nvfp4_moe_plan_bytes(int64_t T, int64_t k, int64_t E);   /* 0 for sizes it does not take */
+size_t nvfp4_moe_plan_part(int64_t T, int64_t k, int64_t E, nvfp4_moe_part part);
+
+/* The k experts of every token from its logits z (T x E, bf16 or FP32, ldz
+ * elements between rows), their weights, and the plan.
+ *   score s = softmax(z) or sigmoid(z) (elementwise);
+ *   experts: the k largest of s + bias (E floats; NULL: of z), in descending
+ *     order, equal ones by index; k <= E;
+ *   weights: scale * s_j, or with renormalise != 0 scale * s_j / (sum of the
+ *     k scores taken).  The bias chooses and is not part of the weight.
+ * An expert whose logit is -inf (or whose s + bias is -inf or NaN) is not taken: a slot that finds none
+ * has expert -1 and weight 0, and a row of nothing but -inf has no expert.  A
+ * NaN among a token's logits (softmax: or +inf) makes its weights NaN.
+ * weights: T x k floats, experts: T x k int32, both written. */
+nvfp4_status nvfp4_moe_route(const void *z, nvfp4_dtype z_dtype, int64_t T, int64_t E, int64_t ldz, int64_t k,
+                             nvfp4_moe_scoring scoring, int renormalise, const float *bias, float scale,
+                             float *weights, int32_t *experts, void *plan, size_t plan_bytes, void *stream);
+
+/* dz (T x E, z's type, lddz elements between rows) from the gradient of the
+ * weights (T x k floats), with z, weights and experts as nvfp4_moe_route took
+ * and gave them.  The choice itself has no gradient; slots without an expert
+ * add nothing.  dz must not overlap z. */
+nvfp4_status nvfp4_moe_route_backward(const float *dweights, const void *z, nvfp4_dtype z_dtype, int64_t T,
+                                      int64_t E, int64_t ldz, int64_t k, nvfp4_moe_scoring scoring,
+                                      int renormalise, float scale, const float *weights, const int32_t *experts,
+                                      void *dz, int64_t lddz, void *stream);
+
+/* The plan of given experts (T x k int32; negative: the slot has none).  A
+ * token may have an expert twice.  An index >= E is taken as none and recorded
+ * as NVFP4_ERR_INDEX when there is a workspace (zero-filled, >= 256 bytes;
+ * NULL: not recorded).  Rows that are sorted by expert already are tokens with
+ * k = 1: order is then the identity. */
+nvfp4_status nvfp4_moe_plan(const int32_t *experts, int64_t T, int64_t k, int64_t E, void *plan, size_t plan_bytes,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/* out[t] = base[t] + sum over j of weights[t][j] y[position[t][j]], FP32
+ * sums in the order of j.  y: rows x N; weights: T x k floats or NULL for 1
+ * (a slot without an expert adds nothing, unless its weight is a NaN); base: T
+ * x N of out's type or NULL; out: T x N, may be base.  bf16 or FP32. */
+nvfp4_status nvfp4_moe_combine(const void *y, nvfp4_dtype y_dtype, const float *weights, const void *plan,
+                               size_t plan_bytes, int64_t T, int64_t k, int64_t E, int64_t N, const void *base,
+                               void *out, nvfp4_dtype out_dtype, void *stream);
+
+/* Its backward pass: dy[position[t][j]] = weights[t][j] dout[t] (rows x N) and
+ * dweights[t][j] = <dout[t], y[position[t][j]]> (0 without an expert).  dout,
+ * y, dy of one type; either output may be NULL, and y with dweights.  dy may
+ * be y.  The gradient of base is dout. */
+nvfp4_status nvfp4_moe_combine_backward(const void *dout, const void *y, nvfp4_dtype dtype, const float *weights,
+                                        const void *plan, size_t plan_bytes, int64_t T, int64_t k, int64_t E,
+                                        int64_t N, void *dy, float *dweights, void *stream);
+
+/* MXFP4 operands of the experts' products.  Every expert's rows begin on a
+ * multiple of 128 in them: P = nvfp4_moe_padded_rows(T, k, E) rows.
+ *   codes, scales: P x K, blocks along K (what a row's padding holds is
+ *     unspecified: it is not part of any product);
+ *   codes_t, scales_t: K x P, blocks of 32 along an expert's own rows, zeros
+ *     behind its last.
+ * x: T x K tokens (sorted_rows == 0), a token's row going to each of its
+ * experts, or T k rows in the experts' order, of which the last ones may be
+ * unused; bf16 or FP32, ldx elements between rows (16-byte aligned). */
+int64_t nvfp4_moe_padded_rows(int64_t T, int64_t k, int64_t E);   /* 0 for sizes it does not take */
+nvfp4_status nvfp4_moe_quantize(const void *x, nvfp4_dtype x_dtype, int64_t ldx, int sorted_rows, const void *plan,
+                                size_t plan_bytes, int64_t T, int64_t k, int64_t E, int64_t K, uint8_t *codes,
+                                uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, void *stream);
+
+/* The experts' weights (E x N x K, contiguous, bf16 or FP32) as E operands
+ * behind one another, each as nvfp4_mx_quantize writes it: codes (E x N x
+ * K/2) and tiled scales; codes_t (E x K x N32/2) and scales_t. */
+nvfp4_status nvfp4_mx_quantize_experts(const void *w, nvfp4_dtype w_dtype, int64_t E, int64_t N, int64_t K,
+                                       uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                                       void *stream);
+
+/* y (rows x N, FP32 or bf16) = x W_e^T for the rows of each expert e, FP32
+ * accumulation; x as nvfp4_moe_quantize writes it, W: E operands N x K.
+ * Results do not depend on scheduling.  1 <= N <= 2^24, K a multiple of 32 up
+ * to 2^24.  workspace: nvfp4_moe_gemm_workspace_bytes(...) bytes (0 for sizes it
+ * does not take). */
+size_t nvfp4_moe_gemm_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+nvfp4_status nvfp4_moe_gemm(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes,
+                            const uint8_t *w_scales, const void *plan, size_t plan_bytes, int64_t T, int64_t k,
+                            int64_t E, int64_t N, int64_t K, void *y, nvfp4_dtype y_dtype, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/* The layer: y (rows x N) = Q(x) W_e^T, x as nvfp4_moe_quantize takes it. */
+size_t nvfp4_moe_linear_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+nvfp4_status nvfp4_moe_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, int sorted_rows,
+                              const uint8_t *w_codes, const uint8_t *w_scales, const void *plan, size_t plan_bytes,
+                              int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, void *y, nvfp4_dtype y_dtype,
+                              void *workspace, size_t ws_bytes, void *stream);
+
+/* The layer's backward pass with straight-through quantisers:
+ *     dX_r = Q(dY_r) Q_c(W_e)           (rows x K, over N; sum it over a token's
+ *                                        slots with nvfp4_moe_combine),
+ *     dW_e = Q_c(dY_e)^T Q_c(X_e)       (E x N x K, over the expert's rows; zeros
+ *                                        for an expert without any),
+ * dY: T k rows x N in the experts' order, bf16 or FP32; Q_c(X), Q_c(W): the
+ * codes_t, scales_t of nvfp4_moe_quantize and nvfp4_mx_quantize_experts.  dx,
+ * dw: FP32 or bf16, overwritten; either may be NULL (then its operand may be
+ * NULL too).  N and K multiples of 32. */
+size_t nvfp4_moe_linear_backward_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+nvfp4_status nvfp4_moe_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int64_t lddy, const uint8_t *x_codes_t,
+                                       const uint8_t *x_scales_t, const uint8_t *w_codes_t,
+                                       const uint8_t *w_scales_t, const void *plan, size_t plan_bytes, int64_t T,
+                                       int64_t k, int64_t E, int64_t N, int64_t K, void *dx, nvfp4_dtype dx_dtype,
+                                       void *dw, nvfp4_dtype dw_dtype, void *workspace, size_t ws_bytes,
+                                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

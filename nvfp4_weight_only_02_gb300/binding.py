@@ -9,6 +9,7 @@ if the library is missing, loading fails loudly: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -23,6 +24,8 @@ OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_UNSUPPORTED_DE
     ERR_NONFINITE, ERR_TIMEOUT, ERR_INDEX = range(10)
 OUT_BF16, OUT_FP32 = 0, 1
 FORMAT_MXFP4, FORMAT_NVFP4 = 0, 1
+MOE_OFFSETS, MOE_ORDER, MOE_POSITION = 0, 1, 2
+MOE_SCORING = {"softmax": 0, "sigmoid": 1}
 
 EXPORTS = [
     "nvfp4_workspace_bytes", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_w4a16_lora_gemm",
@@ -33,7 +36,11 @@ EXPORTS = [
     "nvfp4_w4a16_lora_gemm_list", "nvfp4_tiled_scale_bytes", "nvfp4_tile_scales", "nvfp4_mx_quantize",
     "nvfp4_mx_dequantize", "nvfp4_w4a4_workspace_bytes", "nvfp4_w4a4_gemm", "nvfp4_mx_linear_workspace_bytes",
     "nvfp4_mx_linear", "nvfp4_mx_linear_backward_workspace_bytes", "nvfp4_mx_linear_backward", "nvfp4_distill_topk",
-    "nvfp4_distill_wait_selftest",
+    "nvfp4_distill_wait_selftest", "nvfp4_moe_plan_bytes", "nvfp4_moe_plan_part", "nvfp4_moe_route",
+    "nvfp4_moe_route_backward", "nvfp4_moe_plan", "nvfp4_moe_combine", "nvfp4_moe_combine_backward",
+    "nvfp4_moe_padded_rows", "nvfp4_moe_quantize", "nvfp4_mx_quantize_experts", "nvfp4_moe_gemm_workspace_bytes",
+    "nvfp4_moe_gemm", "nvfp4_moe_linear_workspace_bytes", "nvfp4_moe_linear",
+    "nvfp4_moe_linear_backward_workspace_bytes", "nvfp4_moe_linear_backward",
 ]
 
 
@@ -112,6 +119,26 @@ def load(build_if_missing: bool = True):
             "nvfp4_distill_wait_selftest": (st, [P, ctypes.c_int, i64, i64, P, P, i64, ctypes.c_int, P, P, P, P,
                                                  ctypes.c_size_t, P]),
         }
+        z, c = ctypes.c_size_t, ctypes.c_int
+        shape4, shape5 = [i64] * 4, [i64] * 5          # T, k, E, N;  T, k, E, N, K
+        sig.update({
+            "nvfp4_moe_plan_bytes": (z, [i64] * 3),
+            "nvfp4_moe_plan_part": (z, [i64] * 3 + [c]),
+            "nvfp4_moe_route": (st, [P, c, i64, i64, i64, i64, c, c, P, ctypes.c_float, P, P, P, z, P]),
+            "nvfp4_moe_route_backward": (st, [P, P, c, i64, i64, i64, i64, c, c, ctypes.c_float, P, P, P, i64, P]),
+            "nvfp4_moe_plan": (st, [P, i64, i64, i64, P, z, P, z, P]),
+            "nvfp4_moe_combine": (st, [P, c, P, P, z] + shape4 + [P, P, c, P]),
+            "nvfp4_moe_combine_backward": (st, [P, P, c, P, P, z] + shape4 + [P, P, P]),
+            "nvfp4_moe_padded_rows": (i64, [i64] * 3),
+            "nvfp4_moe_quantize": (st, [P, c, i64, c, P, z] + shape4 + [P, P, P, P, P]),
+            "nvfp4_mx_quantize_experts": (st, [P, c, i64, i64, i64, P, P, P, P, P]),
+            "nvfp4_moe_gemm_workspace_bytes": (z, shape5),
+            "nvfp4_moe_gemm": (st, [P, P, P, P, P, z] + shape5 + [P, c, P, z, P]),
+            "nvfp4_moe_linear_workspace_bytes": (z, shape5),
+            "nvfp4_moe_linear": (st, [P, c, i64, c, P, P, P, z] + shape5 + [P, c, P, z, P]),
+            "nvfp4_moe_linear_backward_workspace_bytes": (z, shape5),
+            "nvfp4_moe_linear_backward": (st, [P, c, i64, P, P, P, P, P, z] + shape5 + [P, c, P, c, P, z, P]),
+        })
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
             f.restype = res
@@ -870,3 +897,333 @@ def nvfp4_distill_wait_selftest(z, index, teacher, tail=False, row_weight=None, 
     _call("nvfp4_distill_wait_selftest", z.data_ptr(), zdt, T, V, index.data_ptr(), teacher.data_ptr(), k,
           1 if tail else 0, _addr(row_weight), _addr(loss), _addr(dz), _addr(workspace),
           0 if workspace is None else workspace.numel(), _raw(dev))
+
+
+# ------------------------------------------------------------------ mixtures of experts
+def nvfp4_moe_gemm_workspace_bytes(T: int, k: int, E: int, N: int, K: int) -> int:
+    return (_lib or load()).nvfp4_moe_gemm_workspace_bytes(T, k, E, N, K)
+
+
+def nvfp4_moe_linear_workspace_bytes(T: int, k: int, E: int, N: int, K: int) -> int:
+    return (_lib or load()).nvfp4_moe_linear_workspace_bytes(T, k, E, N, K)
+
+
+def nvfp4_moe_linear_backward_workspace_bytes(T: int, k: int, E: int, N: int, K: int) -> int:
+    return (_lib or load()).nvfp4_moe_linear_backward_workspace_bytes(T, k, E, N, K)
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_sizes(T, k, E):
+    """Bytes of a plan, 32-bit words before its offsets, order and positions, padded rows."""
+    lib = _lib or load()
+    nbytes = lib.nvfp4_moe_plan_bytes(T, k, E)
+    if nbytes == 0:
+        raise ValueError(f"no plan for {T} tokens with {k} of {E} experts")
+    return (nbytes, *(lib.nvfp4_moe_plan_part(T, k, E, p) // 4 for p in (MOE_OFFSETS, MOE_ORDER, MOE_POSITION)),
+            lib.nvfp4_moe_padded_rows(T, k, E))
+
+
+class MoePlan:
+    """Rows grouped by expert: T tokens with k of E experts each.  A row stands for one slot (token, choice); rows are
+    sorted by expert.  Views into one device buffer, made when they are asked for:
+    offsets (E + 1): rows offsets[e] .. offsets[e + 1] - 1 are expert e's; order (T k): slot of each row, -1 behind the
+    last one; position (T, k): row of each slot, -1 without an expert."""
+
+    __slots__ = ("T", "k", "E", "rows", "padded_rows", "nbytes", "buffer", "index", "_at")
+
+    def __init__(self, T, k, E, device, index):
+        self.nbytes, *self._at, self.padded_rows = _moe_sizes(T, k, E)
+        self.T, self.k, self.E, self.rows, self.index = T, k, E, T * k, index
+        self.buffer = torch.empty(self.nbytes // 4, dtype=torch.int32, device=device)
+
+    @property
+    def offsets(self):
+        return self.buffer.as_strided((self.E + 1,), (1,), self._at[0])
+
+    @property
+    def order(self):
+        return self.buffer.as_strided((self.rows,), (1,), self._at[1])
+
+    @property
+    def position(self):
+        return self.buffer.as_strided((self.T, self.k), (self.k, 1), self._at[2])
+
+
+class MoeRouting:
+    """What moe_route returns: weights (T, k) float32, experts (T, k) int32 (-1: none), plan."""
+
+    __slots__ = ("weights", "experts", "plan", "scoring", "renormalise", "scale")
+
+    def __init__(self, weights, experts, plan, scoring, renormalise, scale):
+        self.weights, self.experts, self.plan = weights, experts, plan
+        self.scoring, self.renormalise, self.scale = scoring, renormalise, scale
+
+
+class MxExperts:
+    """MXFP4 weights of E experts: codes (E, N, K/2) uint8, tiled scales (E, bytes of one expert) uint8."""
+
+    def __init__(self, codes, scales):
+        if codes.dtype != _U8 or scales.dtype != _U8 or len(codes.shape) != 3 or len(scales.shape) != 2:
+            raise ValueError("codes must be a 3-dimensional and scales a 2-dimensional torch.uint8 tensor")
+        if not (codes.is_cuda and scales.is_cuda) or scales.get_device() != codes.get_device():
+            raise ValueError("codes and scales must be CUDA tensors of one device")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        E, N, half = codes.shape
+        nbytes = (N + 127) // 128 * ((2 * half + 127) // 128) * 512
+        if E == 0 or N == 0 or half == 0 or half % 16 or scales.shape != (E, nbytes):
+            raise ValueError(f"codes must hold whole blocks of 32 and scales {nbytes} bytes an expert")
+        self.codes, self.scales, self.index = codes, scales, codes.get_device()
+        self.E, self.N, self.K = E, N, 2 * half
+
+    @property
+    def shape(self):
+        return self.E, self.N, self.K
+
+    def addresses(self):
+        return self.codes.data_ptr(), self.scales.data_ptr()
+
+    def expert(self, e) -> MxOperand:
+        """The weights of one expert, sharing memory."""
+        return MxOperand(self.codes[e], self.scales[e])
+
+
+def _plan_here(plan, dev):
+    if not isinstance(plan, MoePlan):
+        raise ValueError("plan must be a MoePlan")
+    if plan.index != dev:
+        _operand_elsewhere(plan.index, dev)
+
+
+def _scratch(workspace, need, dev, device):
+    if workspace is None:
+        return new_workspace(need, device)
+    if workspace.get_device() != dev or workspace.dtype is not _U8 or not workspace.is_contiguous():
+        _bad_scratch(workspace)
+    return workspace
+
+
+def moe_route(logits: torch.Tensor, k: int, scoring="softmax", renormalise=True, bias=None, scale=1.0) -> MoeRouting:
+    """The k best experts of every token, their weights and the plan.  logits (T, E) bf16 or float32; scoring "softmax" or
+    "sigmoid"; renormalise: weights are scores divided by the sum of those taken; bias (E) float32 is added to the scores
+    for the choice only; scale multiplies the weights."""
+    dev = _current()
+    T, E, ld, dt = _matrix(logits, "logits", dev)
+    how = MOE_SCORING.get(scoring)
+    if how is None:
+        raise ValueError('scoring must be "softmax" or "sigmoid"')
+    if bias is not None:
+        _need(bias, _F32, (E,), "bias", dev)
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be between 1 and the number of experts, {E}")
+    plan = MoePlan(T, k, E, logits.device, dev)
+    weights = torch.empty((T, k), dtype=_F32, device=logits.device)
+    experts = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    _call("nvfp4_moe_route", logits.data_ptr(), dt, T, E, ld, k, how, 1 if renormalise else 0, _addr(bias), scale,
+          weights.data_ptr(), experts.data_ptr(), plan.buffer.data_ptr(), plan.nbytes, _raw(dev))
+    return MoeRouting(weights, experts, plan, scoring, renormalise, scale)
+
+
+def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, routing: MoeRouting) -> torch.Tensor:
+    """Gradient of the logits (their type) from the gradient of routing.weights, (T, k) float32."""
+    dev = _current()
+    T, E, ld, dt = _matrix(logits, "logits", dev)
+    plan = routing.plan
+    if (T, E) != (plan.T, plan.E):
+        raise ValueError(f"logits must have shape {(plan.T, plan.E)}")
+    k = plan.k
+    _need(dweights, _F32, (T, k), "dweights", dev)
+    _need(routing.weights, _F32, (T, k), "routing.weights", dev)
+    _need(routing.experts, torch.int32, (T, k), "routing.experts", dev)
+    dz = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _call("nvfp4_moe_route_backward", dweights.data_ptr(), logits.data_ptr(), dt, T, E, ld, k,
+          MOE_SCORING[routing.scoring], 1 if routing.renormalise else 0, routing.scale, routing.weights.data_ptr(),
+          routing.experts.data_ptr(), dz.data_ptr(), E, _raw(dev))
+    return dz
+
+
+def moe_plan(experts: torch.Tensor, num_experts: int, workspace=None) -> MoePlan:
+    """The plan of given experts (T, k) int32 (negative: the slot has none; beyond the last one: the same, and recorded
+    in the workspace when there is one)."""
+    dev = _current()
+    if len(experts.shape) != 2:
+        raise ValueError("experts must have 2 dimensions")
+    T, k = experts.shape
+    _need(experts, torch.int32, (T, k), "experts", dev)
+    if workspace is not None and not (workspace.get_device() == dev and workspace.dtype is _U8 and
+                                      workspace.is_contiguous()):
+        _bad_scratch(workspace)
+    plan = MoePlan(T, k, num_experts, experts.device, dev)
+    _call("nvfp4_moe_plan", experts.data_ptr(), T, k, num_experts, plan.buffer.data_ptr(), plan.nbytes, _addr(workspace),
+          0 if workspace is None else workspace.numel(), _raw(dev))
+    return plan
+
+
+def moe_combine(y: torch.Tensor, weights, plan: MoePlan, base=None, out_dtype=None) -> torch.Tensor:
+    """out (T, N) = base + the sum over a token's slots of weights (T, k) float32 times rows of y (T k, N).  weights None:
+    1; base (T, N) of out's type; out_dtype: float32 or bfloat16 (y's where None)."""
+    dev = _current()
+    _plan_here(plan, dev)
+    if len(y.shape) != 2 or y.dtype not in _DTYPE_CODE:
+        raise ValueError("y must be a 2-dimensional float32 or bfloat16 tensor")
+    N = y.shape[1]
+    _need(y, y.dtype, (plan.rows, N), "y", dev)
+    odt = y.dtype if out_dtype is None else out_dtype
+    code = _out_code(odt, "out_dtype")
+    if weights is not None:
+        _need(weights, _F32, (plan.T, plan.k), "weights", dev)
+    if base is not None:
+        _need(base, odt, (plan.T, N), "base", dev)
+    out = torch.empty((plan.T, N), dtype=odt, device=y.device)
+    _call("nvfp4_moe_combine", y.data_ptr(), _DTYPE_CODE[y.dtype], _addr(weights), plan.buffer.data_ptr(), plan.nbytes,
+          plan.T, plan.k, plan.E, N, _addr(base), out.data_ptr(), code, _raw(dev))
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y, weights: torch.Tensor, plan: MoePlan, need_dy=True, need_dweights=True):
+    """(dy (T k, N), dweights (T, k) float32) of moe_combine; y may be None without dweights.  Rows of dy behind the last
+    one of the plan are not written.  The gradient of base is dout."""
+    dev = _current()
+    _plan_here(plan, dev)
+    if len(dout.shape) != 2 or dout.dtype not in _DTYPE_CODE:
+        raise ValueError("dout must be a 2-dimensional float32 or bfloat16 tensor")
+    if not (need_dy or need_dweights):
+        raise ValueError("one of dy and dweights is needed")
+    N = dout.shape[1]
+    _need(dout, dout.dtype, (plan.T, N), "dout", dev)
+    if need_dweights and y is None:
+        raise ValueError("dweights needs y")
+    if y is not None:
+        _need(y, dout.dtype, (plan.rows, N), "y", dev)
+    _need(weights, _F32, (plan.T, plan.k), "weights", dev)
+    dy = torch.empty((plan.rows, N), dtype=dout.dtype, device=dout.device) if need_dy else None
+    dw = torch.empty((plan.T, plan.k), dtype=_F32, device=dout.device) if need_dweights else None
+    _call("nvfp4_moe_combine_backward", dout.data_ptr(), _addr(y), _DTYPE_CODE[dout.dtype], weights.data_ptr(),
+          plan.buffer.data_ptr(), plan.nbytes, plan.T, plan.k, plan.E, N, _addr(dy), _addr(dw), _raw(dev))
+    return dy, dw
+
+
+def _moe_rows(x, plan, sorted_rows, dev, name):
+    """(columns, row stride, type code) of tokens (T rows) or sorted rows (T k)."""
+    rows, K, ld, dt = _matrix(x, name, dev)
+    want = plan.rows if sorted_rows else plan.T
+    if rows != want:
+        raise ValueError(f"{name} must have {want} rows, got {rows}")
+    return K, ld, dt
+
+
+def moe_quantize(x: torch.Tensor, plan: MoePlan, rowwise=True, colwise=False, sorted_rows=False) -> MxQuantized:
+    """MXFP4 operands of the experts' products from tokens x (T, K), bf16 or float32, or from rows (T k, K) in the
+    experts' order (sorted_rows).  .row (padded rows, K) for moe_gemm; .col (K, padded rows) for the weight gradient, with
+    blocks along each expert's own rows."""
+    dev = _current()
+    _plan_here(plan, dev)
+    K, ld, dt = _moe_rows(x, plan, sorted_rows, dev, "x")
+    row = col = q = qs = qt = qts = None
+    if rowwise:
+        row = _MxMade(plan.padded_rows, K, x.device, dev)
+        q, qs = row.addresses()
+    if colwise:
+        col = _MxMade(K, plan.padded_rows, x.device, dev)
+        qt, qts = col.addresses()
+    _call("nvfp4_moe_quantize", x.data_ptr(), dt, ld, 1 if sorted_rows else 0, plan.buffer.data_ptr(), plan.nbytes, plan.T,
+          plan.k, plan.E, K, q, qs, qt, qts, _raw(dev))
+    return MxQuantized(row, col, None, None)
+
+
+def moe_quantize_weights(w: torch.Tensor, rowwise=True, colwise=False) -> MxQuantized:
+    """The experts' weights w (E, N, K), bf16 or float32, as MXFP4: .row an MxExperts (E, N, K) with blocks along K, .col
+    an MxExperts (E, K, N rounded up to 32) with blocks along N."""
+    dev = _current()
+    dt = _DTYPE_CODE.get(w.dtype)
+    if dt is None or len(w.shape) != 3:
+        raise ValueError("w must be a 3-dimensional float32 or bfloat16 tensor")
+    E, N, K = w.shape
+    _need(w, w.dtype, (E, N, K), "w", dev)
+    N32 = (N + 31) // 32 * 32
+    tiles = (N + 127) // 128 * ((K + 127) // 128) * 512
+    row = col = q = qs = qt = qts = None
+    if rowwise:
+        q, qs = (torch.empty(s, dtype=_U8, device=w.device) for s in ((E, N, K // 2), (E, tiles)))
+    if colwise:
+        qt, qts = (torch.empty(s, dtype=_U8, device=w.device) for s in ((E, K, N32 // 2), (E, tiles)))
+    _call("nvfp4_mx_quantize_experts", w.data_ptr(), dt, E, N, K, _addr(q), _addr(qs), _addr(qt), _addr(qts), _raw(dev))
+    if rowwise:
+        row = MxExperts(q, qs)
+    if colwise:
+        col = MxExperts(qt, qts)
+    return MxQuantized(row, col, None, None)
+
+
+def moe_gemm(x: MxOperand, w: MxExperts, plan: MoePlan, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
+    """Y (T k, N) = x W_e^T for the rows of each expert: x = moe_quantize(...).row.  Rows behind the last one of the plan
+    are not written."""
+    dev = _current()
+    _plan_here(plan, dev)
+    ydt = _out_code(out_dtype, "out_dtype")
+    if not isinstance(x, MxOperand) or not isinstance(w, MxExperts) or w.E != plan.E or \
+            x.shape != (plan.padded_rows, w.K):
+        raise ValueError(f"x must be an MxOperand of {plan.padded_rows} rows and w an MxExperts of {plan.E} experts with "
+                         "x's number of columns")
+    if x.index != dev or w.index != dev:
+        _operand_elsewhere(x.index if x.index != dev else w.index, dev)
+    T, k, E, N, K = plan.T, plan.k, plan.E, w.N, w.K
+    ws = _scratch(workspace, nvfp4_moe_gemm_workspace_bytes(T, k, E, N, K), dev, plan.buffer.device)
+    y = torch.empty((plan.rows, N), dtype=out_dtype, device=plan.buffer.device)
+    _call("nvfp4_moe_gemm", *x.addresses(), *w.addresses(), plan.buffer.data_ptr(), plan.nbytes, T, k, E, N, K,
+          y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw(dev))
+    return y
+
+
+def moe_linear(x: torch.Tensor, w: MxExperts, plan: MoePlan, out_dtype=torch.float32, sorted_rows=False,
+               workspace=None) -> torch.Tensor:
+    """Y (T k, N) = Q(x) W_e^T for the rows of each expert: tokens x (T, K) bf16 or float32, or rows (T k, K) in the
+    experts' order (sorted_rows), quantised to MXFP4 on the way.  Rows behind the last one of the plan are not written."""
+    dev = _current()
+    _plan_here(plan, dev)
+    K, ld, dt = _moe_rows(x, plan, sorted_rows, dev, "x")
+    ydt = _out_code(out_dtype, "out_dtype")
+    if not isinstance(w, MxExperts) or w.E != plan.E or w.K != K:
+        raise ValueError(f"w must be an MxExperts of {plan.E} experts with x's number of columns")
+    if w.index != dev:
+        _operand_elsewhere(w.index, dev)
+    T, k, E, N = plan.T, plan.k, plan.E, w.N
+    ws = workspace
+    if ws is None:
+        ws = new_workspace(nvfp4_moe_linear_workspace_bytes(T, k, E, N, K), x.device)
+    elif ws.get_device() != dev or ws.dtype is not _U8 or not ws.is_contiguous():
+        _bad_scratch(ws)
+    y = torch.empty((plan.rows, N), dtype=out_dtype, device=x.device)
+    _call("nvfp4_moe_linear", x.data_ptr(), dt, ld, 1 if sorted_rows else 0, *w.addresses(), plan.buffer.data_ptr(),
+          plan.nbytes, T, k, E, N, K, y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw(dev))
+    return y
+
+
+def moe_linear_backward(dy: torch.Tensor, x_col, w_col, plan: MoePlan, dx_dtype=torch.float32, dw_dtype=torch.float32,
+                        workspace=None):
+    """(dX (T k, K), dW (E, N, K)) of the layer with straight-through MXFP4 quantisers.  dy (T k, N) bf16 or float32 in the
+    experts' order; x_col: moe_quantize(..., colwise=True).col; w_col: moe_quantize_weights(..., colwise=True).col.
+    w_col None: no dX; x_col None: no dW.  dX has a row a slot: moe_combine(dX, None, plan) sums a token's."""
+    dev = _current()
+    _plan_here(plan, dev)
+    N, ld, dt = _moe_rows(dy, plan, True, dev, "dy")
+    xdt, wdt = _out_code(dx_dtype, "dx_dtype"), _out_code(dw_dtype, "dw_dtype")
+    if x_col is None and w_col is None:
+        raise ValueError("one of x_col and w_col is needed")
+    T, k, E = plan.T, plan.k, plan.E
+    K = x_col.rows if x_col is not None else w_col.N
+    if x_col is not None and (not isinstance(x_col, MxOperand) or x_col.shape != (K, plan.padded_rows)):
+        raise ValueError(f"x_col must be an MxOperand of shape {(K, plan.padded_rows)}")
+    if w_col is not None and (not isinstance(w_col, MxExperts) or w_col.shape != (E, K, N)):
+        raise ValueError(f"w_col must be an MxExperts of shape {(E, K, N)}")
+    for operand in (x_col, w_col):
+        if operand is not None and operand.index != dev:
+            _operand_elsewhere(operand.index, dev)
+    xp = (None, None) if x_col is None else x_col.addresses()
+    wp = (None, None) if w_col is None else w_col.addresses()
+    ws = _scratch(workspace, nvfp4_moe_linear_backward_workspace_bytes(T, k, E, N, K), dev, dy.device)
+    dx = torch.empty((plan.rows, K), dtype=dx_dtype, device=dy.device) if w_col is not None else None
+    dw = torch.empty((E, N, K), dtype=dw_dtype, device=dy.device) if x_col is not None else None
+    _call("nvfp4_moe_linear_backward", dy.data_ptr(), dt, ld, *xp, *wp, plan.buffer.data_ptr(), plan.nbytes, T, k, E, N, K,
+          _addr(dx), xdt, _addr(dw), wdt, ws.data_ptr(), ws.numel(), _raw(dev))
+    return dx, dw

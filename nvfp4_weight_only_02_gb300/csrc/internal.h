@@ -165,6 +165,111 @@ cudaError_t launch_w4a4_tile(const W4A4Args &a, cudaStream_t s, const DeviceInfo
 cudaError_t encode_scale_map(CUtensorMap *map, const uint8_t *scales, uint64_t ktiles, uint64_t row_tiles,
                              uint32_t box_k, uint32_t box_rows);
 
+// Launch that may start while the kernel before it on the stream ends; the
+// kernel waits (pdl_wait) before it touches memory.
+template <typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int block, size_t smem, cudaStream_t s,
+                                    const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Routing of tokens to experts and back (csrc/moe_route.cu); the plan's layout
+// is in moe_plan.h.
+struct MoeRouteArgs {
+    const void *z;            // T x E logits (leading dimension ldz), or null: the experts are given
+    bool z_fp32;
+    int64_t T, ldz;
+    int E, k;
+    bool sigmoid, renorm;
+    const float *bias;        // E or null
+    float scale;
+    float *weights;           // T x k
+    int32_t *experts;         // T x k
+    int32_t *plan;
+    uint32_t *ctl;            // status words or null
+};
+cudaError_t launch_moe_route(const MoeRouteArgs &a, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_moe_route_backward(const MoeRouteArgs &a, const float *dw, void *dz, int64_t lddz, cudaStream_t s);
+struct MoeCombineArgs {
+    const void *y;            // rows x N
+    bool y_fp32;
+    const float *weights;     // T x k or null (1)
+    const int32_t *position;  // T x k
+    int64_t T, N;
+    int k;
+    const void *base;         // T x N or null, of out's type
+    void *out;                // T x N
+    bool out_fp32;
+    const void *dout;         // backward: T x N of y's type
+    void *dy;                 // rows x N or null
+    float *dw;                // T x k or null
+};
+cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t s);
+cudaError_t launch_moe_combine_backward(const MoeCombineArgs &a, cudaStream_t s);
+
+// Where the rows of a quantised operand come from when they are grouped by
+// expert: device arrays of the plan (csrc/moe_plan.h).
+struct MoeRows {
+    const int32_t *header;    // rows, blocks, tiles
+    const int32_t *order;     // slot of each row
+    const int32_t *padded;    // padded row of each slot
+    const int4 *blocks;       // expert, first padded row, first row, rows
+    int64_t max_blocks;
+    int64_t slots;
+    int k;                    // rows of x are tokens, k slots each; 0: they are the grouped rows
+};
+// Rows of x to their places (csrc/mx_quant.cu): codes padded rows x cols/2.
+cudaError_t launch_mx_quantize_rows(const MxQuantArgs &a, const MoeRows &m, cudaStream_t s);
+// The same with the column direction: blocks of 32 along an expert's own rows,
+// codes_t cols x padded rows / 2 (zeros behind an expert's last row).
+cudaError_t launch_mx_quantize_groups(const MxQuantArgs &a, const MoeRows &m, cudaStream_t s);
+// a.rows x a.cols matrices one behind the other, each an operand of its own.
+cudaError_t launch_mx_quantize_batch(const MxQuantArgs &a, int batch, cudaStream_t s);
+
+// Products grouped by expert (csrc/gemm_moe.cu).
+struct MoeGemmArgs {
+    const uint8_t *x_codes, *x_scales;   // padded rows x K
+    const uint8_t *w_codes, *w_scales;   // E x N x K
+    int64_t padded_rows, N, K;
+    int E;
+    const int32_t *header;
+    const int4 *tiles;
+    int64_t max_tiles;
+    int tile_rows;
+    void *y;                             // rows x N
+    bool y_fp32;
+    uint32_t *ctl;
+};
+cudaError_t launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t s, const DeviceInfo &dev);
+// dW[e] = A_e^T X_e over the expert's rows: operands N x padded rows and K x
+// padded rows, contracted from the expert's first block on.
+struct MoeWgradArgs {
+    const uint8_t *a_codes, *a_scales;   // N x padded rows
+    const uint8_t *x_codes, *x_scales;   // K x padded rows
+    int64_t padded_rows, N, K;
+    int E;
+    const int32_t *first_block;          // E + 1
+    void *dw;                            // E x N x K
+    bool dw_fp32;
+    uint32_t *ctl;
+};
+cudaError_t launch_moe_wgrad(const MoeWgradArgs &a, cudaStream_t s, const DeviceInfo &dev);
+
+// Tiled tensor map of three dimensions (element strides 1), zero fill outside.
+cudaError_t encode_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[3],
+                                 const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
+
 // Distillation loss and gradient (csrc/distill.cu).
 constexpr int kDistillMaxK = 1024;             // teacher entries per row
 constexpr int64_t kDistillMaxSlice = 200 * 1024;  // bytes of a row one CTA (of up to 8) holds

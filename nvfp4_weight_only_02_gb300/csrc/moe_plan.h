@@ -1,0 +1,76 @@
+// moe_plan.h -- layout of a grouping of rows by expert (the plan that
+// nvfp4_moe_route and nvfp4_moe_plan write, include/nvfp4.h).
+// Host and device arithmetic only: plain C++.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace nvfp4 {
+
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxK = 32;
+constexpr int64_t kMoeMaxSlots = 1LL << 24;
+constexpr int kMoeBlock = 128;      // every expert's rows begin on a multiple of this in the quantised operands
+constexpr int kMoeChunk = 32768;    // slots of a CTA at most (16-bit counters)
+constexpr int kMoeHeader = 16;      // 32-bit words
+
+// Words of the header.
+enum MoeHeaderWord : int { kMoeRows = 0, kMoeBlocks = 1, kMoeTiles = 2, kMoeTileRows = 3 };
+
+// Rows of a product's tile.  The weights are read once for each tile of an
+// expert, and up to 64 rows a product streams them at the cost of reading, so
+// a tile holds more rows than an expert has on average.  64 at least: the
+// tensor cores take a tile's scales from an even column (32 rows a column).
+inline int moe_tile_rows(int64_t slots, int experts)
+{
+    const int64_t mean = slots / std::min<int64_t>(slots, experts);
+    return mean <= 40 ? 64 : mean <= 96 ? 128 : 256;
+}
+
+// Where things are in the plan's buffer, in 32-bit words; every part begins on
+// a multiple of four.
+struct MoeLayout {
+    int64_t slots;      // T k
+    int experts;
+    int tile_rows;
+    int64_t max_blocks, max_tiles;
+    int ctas;           // of the counting kernels; 1: everything in one
+    int64_t offsets, first_block, position, order, padded, blocks, tiles, counts, total;
+
+    MoeLayout(int64_t T, int64_t k, int E)
+    {
+        slots = T * k;
+        experts = E;
+        tile_rows = moe_tile_rows(slots, E);
+        const int64_t some = std::min<int64_t>(slots, E);   // experts with rows, at most
+        max_blocks = slots / kMoeBlock + some;
+        max_tiles = slots / tile_rows + some;
+        ctas = (int)std::max<int64_t>(std::min<int64_t>(128, (slots + 2047) / 2048), (slots + kMoeChunk - 1) / kMoeChunk);
+        int64_t at = kMoeHeader;
+        auto take = [&](int64_t words) {
+            const int64_t p = at;
+            at += (words + 3) / 4 * 4;
+            return p;
+        };
+        offsets = take(E + 1);
+        first_block = take(E + 1);
+        position = take(slots);
+        order = take(slots);
+        padded = take(slots);
+        blocks = take(4 * max_blocks);
+        tiles = take(4 * max_tiles);
+        counts = take(ctas > 1 ? (int64_t)ctas * E : 0);
+        total = at;
+    }
+    int64_t padded_rows() const { return max_blocks * kMoeBlock; }
+};
+
+inline bool moe_sizes_ok(int64_t T, int64_t k, int64_t E)
+{
+    return T >= 1 && T <= kMoeMaxSlots && k >= 1 && k <= kMoeMaxK && E >= 1 && E <= kMoeMaxExperts && T * k <= kMoeMaxSlots;
+}
+
+}  // namespace nvfp4

@@ -57,7 +57,13 @@ struct MqParams {
     int64_t ctiles;   // tiles along a row
     uint8_t *codes, *scales, *codes_t, *scales_t;
     uint16_t *values, *values_t;
+    MoeRows moe;      // grouped rows: where they come from
 };
+
+// Where a tile's rows come from and go to: a matrix; one of several behind one
+// another (blockIdx.y); rows grouped by expert, gathered into blocks of 128
+// that belong to one expert each.
+enum MqSource { kMatrix, kBatch, kExpertRows };
 
 // One read of x for both directions, a tile a CTA: 16 bytes a thread and row
 // at a time, all of them on their way before the first is used.  Row direction,
@@ -81,10 +87,11 @@ struct MqParams {
 // TMA 41.5 us (rows 26.2); registers capped for five CTAs an SM 44.5 us.
 constexpr int kMqThreads = 256;
 
-template <typename T, bool kRow, bool kCol>
+template <typename T, bool kRow, bool kCol, MqSource kSource>
 __global__ void __launch_bounds__(kMqThreads)
-    mx_quantize_kernel(const T *__restrict__ x, const int64_t ld, const MqParams p)
+    mx_quantize_kernel(const T *__restrict__ x, const int64_t ld, const MqParams params)
 {
+    MqParams p = params;
     using S = MqShape<T>;
     constexpr int kCols = S::kCols, kPer = S::kPer, kGroups = kCols / 32;   // 32-column groups of a tile
     constexpr int kLanes = kCols / 8, kStep = kMqThreads / kLanes;          // lanes to a row, rows at a time
@@ -96,11 +103,29 @@ __global__ void __launch_bounds__(kMqThreads)
     const int64_t rows = p.rows, cols = p.cols, rows32 = (rows + 31) / 32 * 32;
     const int64_t rtiles = (rows + kMqRows - 1) / kMqRows, ktiles = (cols + 127) / 128;
     const int64_t rt = blockIdx.x / p.ctiles, ct = blockIdx.x % p.ctiles, r0 = rt * kMqRows, c0 = ct * kCols;
-    const int left = (int)min(rows - r0, (int64_t)kMqRows);                 // rows of the tile that exist
+    int left = (int)min(rows - r0, (int64_t)kMqRows);                       // rows of the tile that exist
     // A product launched behind this kernel starts its weight copies as soon as
     // every block is here; by then all kernels before this one are complete.
     pdl_wait();
     pdl_launch_dependents();
+    if constexpr (kSource == kBatch) {
+        const int64_t b = blockIdx.y;
+        x += b * rows * ld;
+        p.codes += p.codes ? b * rows * (cols / 2) : 0;
+        p.scales += p.scales ? b * rtiles * ktiles * 512 : 0;
+        p.codes_t += p.codes_t ? b * cols * (rows32 / 2) : 0;
+        p.scales_t += p.scales_t ? b * ktiles * rtiles * 512 : 0;
+    }
+    int64_t row0 = 0;        // grouped: the block's first row
+    if constexpr (kSource == kExpertRows) {
+        if (rt >= p.moe.header[1])
+            return;
+        const int4 block = p.moe.blocks[rt];
+        row0 = block.z;
+        left = block.w;
+    }
+    // rows of the tile in the column direction: a group's last block is padded with zeros
+    const int cleft = kSource == kExpertRows ? kMqRows : left;
 
     const int lr = tid / kLanes, c8 = tid % kLanes * 8;
     const bool cok = c0 + c8 < cols;
@@ -109,8 +134,14 @@ __global__ void __launch_bounds__(kMqThreads)
 #pragma unroll
     for (int i = 0; i < kIter; i++) {
         raw[i].zero();
-        if (cok && i * kStep + lr < left)
-            raw[i].load(src + (int64_t)(i * kStep) * ld);
+        if (cok && i * kStep + lr < left) {
+            if constexpr (kSource == kExpertRows) {
+                const int64_t r = row0 + i * kStep + lr;
+                raw[i].load(x + (p.moe.k ? p.moe.order[r] / p.moe.k : r) * ld + c0 + c8);
+            } else {
+                raw[i].load(src + (int64_t)(i * kStep) * ld);
+            }
+        }
     }
     if (kCol) {
 #pragma unroll
@@ -169,7 +200,7 @@ __global__ void __launch_bounds__(kMqThreads)
 #pragma unroll
         for (int j = 0; j < kPer; j++)
             s_q[(c + j) * 5 + rb] = make_uint4(q[j][0], q[j][1], q[j][2], q[j][3]);
-        if (rb * 32 < left && c0 + c < cols) {
+        if (rb * 32 < cleft && c0 + c < cols) {
             if (p.values_t) {
 #pragma unroll
                 for (int g = 0; g < 4; g++) {
@@ -202,7 +233,7 @@ __global__ void __launch_bounds__(kMqThreads)
 #pragma unroll
         for (int i = tid; i < kCols * 4; i += kMqThreads) {
             const int c = i >> 2, rb = i & 3;
-            if (rb * 32 < left && c0 + c < cols)
+            if (rb * 32 < cleft && c0 + c < cols)
                 *reinterpret_cast<uint4 *>(dst + c * (rows32 / 2) + rb * 16) = s_q[c * 5 + rb];
         }
     }
@@ -227,6 +258,61 @@ __global__ void __launch_bounds__(kMqThreads)
         dst[half * kGroups] = s_sct[w / kGroups + 32 * (w % kGroups)];
         if (alone)
             dst[kGroups] = 0u;
+    }
+}
+
+// Rows of x to their places in the experts' order, each read once: a warp takes
+// 256 elements of a row, quantises them and writes codes and scale words to
+// every place that the row has (a token has one for each of its experts).  The
+// rows behind an expert's last one are left as they are: a product's output
+// rows depend on their own row only.
+constexpr int kMrChunk = 256, kMrUnroll = 2;
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    mx_quantize_rows_kernel(const T *__restrict__ x, const int64_t ld, const int64_t rows, const int64_t cols,
+                            uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, const MoeRows m)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t chunks = (cols + kMrChunk - 1) / kMrChunk, ktiles = (cols + 127) / 128;
+    const int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kMrUnroll;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t some = m.k ? rows : min(rows, (int64_t)m.header[0]);   // grouped rows that there are
+    Raw8<T> raw[kMrUnroll];
+#pragma unroll
+    for (int u = 0; u < kMrUnroll; u++) {
+        const int64_t r = (i0 + u) / chunks, c = (i0 + u) % chunks * kMrChunk + lane * 8;
+        raw[u].zero();
+        if (r < some && c < cols)
+            raw[u].load(x + r * ld + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kMrUnroll; u++) {
+        const int64_t r = (i0 + u) / chunks, c = (i0 + u) % chunks * kMrChunk + lane * 8;
+        uint32_t a = raw[u].amax_bits();
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        uint32_t byte;
+        const uint32_t q = raw[u].encode(a, byte);
+        // the four blocks of 128 elements in one word
+        uint32_t word = 0;
+#pragma unroll
+        for (int b = 0; b < 4; b++)
+            word |= __shfl_sync(0xffffffffu, byte, (lane & 16) + 4 * b) << (8 * b);
+        if (r >= some)
+            break;
+        const int n = m.k ? m.k : 1;
+        for (int j = 0; j < n; j++) {
+            const int32_t at = m.k ? m.padded[r * n + j] : m.padded[m.order[r]];
+            if (at < 0)
+                continue;
+            if (c < cols)
+                *reinterpret_cast<uint32_t *>(codes + ((int64_t)at * cols + c) / 2) = q;
+            if ((lane & 15) == 0 && c < cols)
+                *reinterpret_cast<uint32_t *>(scales + (((int64_t)at >> 7) * ktiles + (c >> 7)) * 512 + (at & 31) * 16 +
+                                              (at & 127) / 32 * 4) = word;
+        }
     }
 }
 
@@ -278,11 +364,12 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t *__restr
     }
 }
 
-template <typename T, bool kRow, bool kCol>
-cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s)
+template <typename T, bool kRow, bool kCol, MqSource kSource = kMatrix>
+cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s, const MoeRows &moe = {}, int batch = 1)
 {
     constexpr int kCols = MqShape<T>::kCols;
     MqParams p;
+    p.moe = moe;
     p.rows = a.rows;
     p.cols = a.cols;
     p.ctiles = (a.cols + kCols - 1) / kCols;
@@ -293,7 +380,7 @@ cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s)
     p.values = a.values;
     p.values_t = a.values_t;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.rows + kMqRows - 1) / kMqRows * p.ctiles));
+    cfg.gridDim = dim3((unsigned)((a.rows + kMqRows - 1) / kMqRows * p.ctiles), (unsigned)batch);
     cfg.blockDim = dim3(kMqThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -301,16 +388,24 @@ cudaError_t run_quantize(const MxQuantArgs &a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx_quantize_kernel<T, kRow, kCol>, (const T *)a.x, a.ld, p);
+    return cudaLaunchKernelEx(&cfg, mx_quantize_kernel<T, kRow, kCol, kSource>, (const T *)a.x, a.ld, p);
+}
+
+template <typename T, MqSource kSource = kMatrix>
+cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s, const MoeRows &moe = {}, int batch = 1)
+{
+    const bool row = a.codes || a.values, col = a.codes_t || a.values_t;
+    return row && col ? run_quantize<T, true, true, kSource>(a, s, moe, batch)
+           : row      ? run_quantize<T, true, false, kSource>(a, s, moe, batch)
+                      : run_quantize<T, false, true, kSource>(a, s, moe, batch);
 }
 
 template <typename T>
-cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s)
+cudaError_t run_quantize_rows(const MxQuantArgs &a, const MoeRows &m, cudaStream_t s)
 {
-    const bool row = a.codes || a.values, col = a.codes_t || a.values_t;
-    return row && col ? run_quantize<T, true, true>(a, s)
-           : row      ? run_quantize<T, true, false>(a, s)
-                      : run_quantize<T, false, true>(a, s);
+    const int64_t tasks = a.rows * ((a.cols + kMrChunk - 1) / kMrChunk), per = 8 * kMrUnroll;
+    return launch_dependent(mx_quantize_rows_kernel<T>, dim3((unsigned)((tasks + per - 1) / per)), 256, 0, s,
+                            (const T *)a.x, a.ld, a.rows, a.cols, a.codes, a.scales, m);
 }
 
 unsigned grid_for(int64_t n, const DeviceInfo &dev)
@@ -324,6 +419,24 @@ unsigned grid_for(int64_t n, const DeviceInfo &dev)
 cudaError_t launch_mx_quantize(const MxQuantArgs &a, cudaStream_t s)
 {
     return a.x_fp32 ? run_quantize_dirs<float>(a, s) : run_quantize_dirs<__nv_bfloat16>(a, s);
+}
+
+cudaError_t launch_mx_quantize_rows(const MxQuantArgs &a, const MoeRows &m, cudaStream_t s)
+{
+    return a.x_fp32 ? run_quantize_rows<float>(a, m, s) : run_quantize_rows<__nv_bfloat16>(a, m, s);
+}
+
+cudaError_t launch_mx_quantize_groups(const MxQuantArgs &a, const MoeRows &m, cudaStream_t s)
+{
+    MxQuantArgs g = a;
+    g.rows = m.max_blocks * kMqRows;
+    return a.x_fp32 ? run_quantize_dirs<float, kExpertRows>(g, s, m) : run_quantize_dirs<__nv_bfloat16, kExpertRows>(g, s, m);
+}
+
+cudaError_t launch_mx_quantize_batch(const MxQuantArgs &a, int batch, cudaStream_t s)
+{
+    return a.x_fp32 ? run_quantize_dirs<float, kBatch>(a, s, {}, batch)
+                    : run_quantize_dirs<__nv_bfloat16, kBatch>(a, s, {}, batch);
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
