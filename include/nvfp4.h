@@ -624,6 +624,36 @@ nvfp4_status nvfp4_moe_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int
                                        void *dw, nvfp4_dtype dw_dtype, void *workspace, size_t ws_bytes,
                                        void *stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit integers with one FP32 scale for each token and output channel, for
+ * layers that 4 bits do not suit: quantiser of rows, product, layer.
+ *
+ * Quantisation of the rows of x (rows x cols, bf16 or FP32, ld elements between
+ * rows): scale = amax / 127, code = the integer next to 127 x / amax, ties to
+ * even (amax: the row's largest magnitude).  A row of zeros has scale 0 and
+ * codes 0; a row with an infinity or a NaN scale NaN and codes 0.
+ * 1 <= rows <= 2^30, cols a multiple of 16 up to 131072; x and its rows on
+ * 16-byte boundaries. */
+nvfp4_status nvfp4_int8_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                                 int8_t *codes, float *scales, void *stream);
+
+/* Y[m][n] = a_scales[m] w_scales[n] sum over k of a[m][k] w[n][k] (A: M x K,
+ * W: N x K codes), FP32 or bf16 (RNE of the FP32 result).  The integers are
+ * summed in FP32: exactly while the sums of a row's products stay below 2^24
+ * in magnitude.  Results do not depend on scheduling.  Codes are -127 .. 127
+ * (-128 is taken as it is).  K a multiple of 16 up to 131072.  workspace:
+ * nvfp4_int8_linear_workspace_bytes(M, N, K) bytes (0 for sizes it does not take). */
+size_t nvfp4_int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nvfp4_status nvfp4_int8_gemm(const int8_t *a_codes, const float *a_scales, const int8_t *w_codes,
+                             const float *w_scales, int64_t M, int64_t N, int64_t K, void *y, nvfp4_dtype y_dtype,
+                             void *workspace, size_t ws_bytes, void *stream);
+
+/* The layer: nvfp4_int8_quantize of the tokens x (M x K, bf16 or FP32, ldx
+ * elements between rows), then nvfp4_int8_gemm, the same Y; any M >= 1. */
+nvfp4_status nvfp4_int8_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, int64_t M, int64_t N, int64_t K,
+                               const int8_t *w_codes, const float *w_scales, void *y, nvfp4_dtype y_dtype,
+                               void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,7 +40,8 @@ EXPORTS = [
     "nvfp4_moe_route_backward", "nvfp4_moe_plan", "nvfp4_moe_combine", "nvfp4_moe_combine_backward",
     "nvfp4_moe_padded_rows", "nvfp4_moe_quantize", "nvfp4_mx_quantize_experts", "nvfp4_moe_gemm_workspace_bytes",
     "nvfp4_moe_gemm", "nvfp4_moe_linear_workspace_bytes", "nvfp4_moe_linear",
-    "nvfp4_moe_linear_backward_workspace_bytes", "nvfp4_moe_linear_backward",
+    "nvfp4_moe_linear_backward_workspace_bytes", "nvfp4_moe_linear_backward", "nvfp4_int8_quantize",
+    "nvfp4_int8_linear_workspace_bytes", "nvfp4_int8_gemm", "nvfp4_int8_linear",
 ]
 
 
@@ -138,6 +139,10 @@ def load(build_if_missing: bool = True):
             "nvfp4_moe_linear": (st, [P, c, i64, c, P, P, P, z] + shape5 + [P, c, P, z, P]),
             "nvfp4_moe_linear_backward_workspace_bytes": (z, shape5),
             "nvfp4_moe_linear_backward": (st, [P, c, i64, P, P, P, P, P, z] + shape5 + [P, c, P, c, P, z, P]),
+            "nvfp4_int8_quantize": (st, [P, c, i64, i64, i64, P, P, P]),
+            "nvfp4_int8_linear_workspace_bytes": (z, [i64] * 3),
+            "nvfp4_int8_gemm": (st, [P, P, P, P, i64, i64, i64, P, c, P, z, P]),
+            "nvfp4_int8_linear": (st, [P, c, i64, i64, i64, i64, P, P, P, c, P, z, P]),
         })
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -1227,3 +1232,85 @@ def moe_linear_backward(dy: torch.Tensor, x_col, w_col, plan: MoePlan, dx_dtype=
     _call("nvfp4_moe_linear_backward", dy.data_ptr(), dt, ld, *xp, *wp, plan.buffer.data_ptr(), plan.nbytes, T, k, E, N, K,
           _addr(dx), xdt, _addr(dw), wdt, ws.data_ptr(), ws.numel(), _raw(dev))
     return dx, dw
+
+
+# ------------------------------------------------------------------ 8-bit integers
+class Int8Matrix:
+    """8-bit integers with one scale a row: codes (rows, cols) int8, scales (rows) float32."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "index")
+
+    def __init__(self, codes, scales):
+        if codes.dtype != torch.int8 or len(codes.shape) != 2 or scales.dtype != _F32:
+            raise ValueError("codes must be a 2-dimensional torch.int8 tensor, scales torch.float32")
+        if not (codes.is_cuda and scales.is_cuda) or scales.get_device() != codes.get_device():
+            raise ValueError("codes and scales must be CUDA tensors of one device")
+        self.rows, self.cols = codes.shape
+        if scales.shape != (self.rows,) or not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous, with one scale a row")
+        self.codes, self.scales, self.index = codes, scales, codes.get_device()
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def nvfp4_int8_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return (_lib or load()).nvfp4_int8_linear_workspace_bytes(M, N, K)
+
+
+def int8_quantize(x: torch.Tensor) -> Int8Matrix:
+    """The rows of x (rows, cols), bf16 or float32, as 8-bit integers: tokens, or the output channels of a weight."""
+    dev = _current()
+    rows, cols, ld, dt = _matrix(x, "x", dev)
+    codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scales = torch.empty(rows, dtype=_F32, device=x.device)
+    _call("nvfp4_int8_quantize", x.data_ptr(), dt, rows, cols, ld, codes.data_ptr(), scales.data_ptr(), _raw(dev))
+    return Int8Matrix(codes, scales)
+
+
+def _int8_weight(w, K, dev):
+    if not isinstance(w, Int8Matrix) or w.cols != K:
+        raise ValueError(f"w must be an Int8Matrix with {K} columns")
+    if w.index != dev:
+        _operand_elsewhere(w.index, dev)
+
+
+def int8_gemm(a: Int8Matrix, w: Int8Matrix, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
+    """Y (M, N) = A W^T of two matrices of 8-bit integers."""
+    dev = _current()
+    M, K = a.shape
+    if a.index != dev:
+        _operand_elsewhere(a.index, dev)
+    _int8_weight(w, K, dev)
+    ydt = _out_code(out_dtype, "out_dtype")
+    N = w.rows
+    ws = _scratch(workspace, nvfp4_int8_linear_workspace_bytes(M, N, K), dev, a.device)
+    y = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _call("nvfp4_int8_gemm", a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), M, N, K,
+          y.data_ptr(), ydt, ws.data_ptr(), ws.numel(), _raw(dev))
+    return y
+
+
+def int8_linear(x: torch.Tensor, w: Int8Matrix, out_dtype=torch.float32, workspace=None) -> torch.Tensor:
+    """Y (M, N) = Q(X) W^T: x (M, K) bf16 or float32, each token quantised to 8-bit integers on the way."""
+    dev = _current()
+    M, K, ld, dt = _matrix(x, "x", dev)
+    _int8_weight(w, K, dev)
+    ydt = _DTYPE_CODE.get(out_dtype)
+    if ydt is None:
+        _out_code(out_dtype, "out_dtype")
+    N = w.rows
+    ws = workspace
+    if ws is None:
+        ws = new_workspace(nvfp4_int8_linear_workspace_bytes(M, N, K), x.device)
+    elif ws.get_device() != dev or ws.dtype is not _U8 or not ws.is_contiguous():
+        _bad_scratch(ws)
+    y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    _call("nvfp4_int8_linear", x.data_ptr(), dt, ld, M, N, K, w.codes.data_ptr(), w.scales.data_ptr(), y.data_ptr(), ydt,
+          ws.data_ptr(), ws.numel(), _raw(dev))
+    return y

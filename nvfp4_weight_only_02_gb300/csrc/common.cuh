@@ -106,6 +106,16 @@ __device__ __forceinline__ void e2m1x8_to_h2x4(uint32_t w, uint32_t out[4])
         : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3]) : "r"(w));
 }
 
+// Four 8-bit integers -> two f16x2, exact: the byte plus 128 becomes the low
+// bits of 1024 + u, and 1152 is taken off again.
+__device__ __forceinline__ void int8x4_to_h2x2(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = w ^ 0x80808080u, k = 0x64806480u;   // 1152 twice
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(k));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(k));
+}
+
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
 {
     uint32_t d;

@@ -1,0 +1,628 @@
+// gemm_int8.cu -- Y[m][n] = s_m s_n sum_k q[m][k] w[n][k] with 8-bit integers q
+// and w and one FP32 scale for each token and output channel.
+//
+// This chip's 8-bit integer tensor rate is far below its 16-bit one, and the
+// integers -127..127 and their products are exact in fp16 and FP32, so the
+// codes are multiplied as fp16 (tcgen05, FP32 accumulators): sums are exact
+// while they stay below 2^24 and rounded as FP32 sums beyond.
+//
+// The weights stay 8 bits until they are next to the tensor core.  Their rows
+// are the MMA's M side, whose operand may come from TMEM: warps read a stage of
+// codes from shared memory, a row a thread, make fp16 of them (byte permute into
+// 1024 + u, u = w + 128, minus 1152: 5 instructions for 4 weights) and store
+// them to TMEM.  Shared memory then carries each weight twice as one byte, and
+// not again as two bytes written and read.  Tokens are quantised to fp16
+// integers by a kernel before this one and come by TMA.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "w4a4_pair.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kI8K = 128;         // elements of K a stage
+constexpr int kI8Rows = 128;      // weight rows a CTA
+constexpr int kI8WBytes = kI8Rows * kI8K, kI8ACols = kI8K / 2;   // a stage's codes, and its columns as fp16 in TMEM
+constexpr int kI8Conv = 8;        // warps that convert: two for each 32 rows, half a stage's columns each
+
+struct Int8Params {
+    const float *x_scale, *w_scale;
+    int M, N;
+    int ksteps;
+    int mtiles, ntiles;
+    int split;    // streaming: CTAs of a cluster that share a tile's K
+    int early;    // the weights were complete before the kernel before this one started
+    void *y;
+    int y_fp32;
+    uint32_t *ctl;
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[smem]^T over 16 elements of K, f16 operands.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_ts_pair(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// A converting warp's part of a stage: row 32 (warp % 4) + lane, columns 64 (warp / 4) .. + 63, from the swizzled
+// layout of a TMA copy.
+__device__ __forceinline__ void convert_part(const uint8_t *stage, uint32_t a_tmem, int warp, int lane)
+{
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    uint32_t v[32];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((4 * half + j) ^ (row & 7)) << 4));
+        int8x4_to_h2x2(q.x, v[8 * j], v[8 * j + 1]);
+        int8x4_to_h2x2(q.y, v[8 * j + 2], v[8 * j + 3]);
+        int8x4_to_h2x2(q.z, v[8 * j + 4], v[8 * j + 5]);
+        int8x4_to_h2x2(q.w, v[8 * j + 6], v[8 * j + 7]);
+    }
+    tmem_st32(a_tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32, v);
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(local), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------- few tokens
+// A CTA takes 128 weight rows and NT tokens; K is split over the CTAs of a
+// cluster when there are fewer tiles than CTA places, the shares added in rank
+// order through distributed shared memory.
+constexpr int kIsThreads = 32 * (kI8Conv + 2);  // + copies, MMA
+
+template <int NT>
+struct IsShape {
+    static constexpr int kCtas = NT <= 64 ? 2 : 1;        // on an SM
+    static constexpr int kStageBytes = kI8WBytes + NT * kI8K * 2;
+    static constexpr int kTmemCols = 512 / kCtas;
+    static constexpr int kAccCols = NT < 32 ? 32 : NT;
+    static constexpr int kStages = NT <= 64 ? 3 : 4;
+    static constexpr int kRing = kStages * kStageBytes;
+    // CTAs that fit an SM's shared memory never want more than its TMEM columns together (w4a4_shape.h)
+    static constexpr int kLeast = kTmemCols / 128 * 46 * 1024;
+    static constexpr size_t kSmem = 1024 + (kRing > kLeast ? kRing : kLeast);
+    static_assert(kAccCols + kStages * kI8ACols <= kTmemCols && NT * 512 <= kRing && kSmem * kCtas <= 226 * 1024, "fits");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kIsThreads, IsShape<NT>::kCtas)
+    int8_stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Int8Params p)
+{
+    using S = IsShape<NT>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sW = smem, *sX = sW + kStages * kI8WBytes;
+    float *red = reinterpret_cast<float *>(smem);   // [NT][128], once the ring is drained
+    __shared__ __align__(8) uint64_t full[kStages], a_full[kStages], done[kStages], acc_full[1];
+    __shared__ uint32_t s_tmem;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = blockIdx.x / p.split, nt = tile / p.mtiles, mt = tile % p.mtiles;
+    const int ks0 = (int)((int64_t)p.ksteps * rank / p.split), ks1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);
+    const int nk = ks1 - ks0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(&full[s], 1);
+            mbar_init(&a_full[s], kI8Conv);
+            mbar_init(&done[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_fence_init();
+    }
+    if (warp == kI8Conv + 1) {
+        tmem_alloc(&s_tmem, S::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem, a_ring = tmem + S::kAccCols;
+
+    if (warp == kI8Conv) {
+        // ---------------- copies
+        auto load_w = [&](int i, int st) {
+            mbar_arrive_expect_tx(&full[st], S::kStageBytes);
+            tma_load_2d(sW + st * kI8WBytes, &tm_w, &full[st], (ks0 + i) * kI8K, nt * kI8Rows);
+        };
+        auto load_x = [&](int i, int st) {
+            uint8_t *dst = sX + st * NT * kI8K * 2;
+            tma_load_2d(dst, &tm_x, &full[st], (ks0 + i) * kI8K, mt * NT);
+            tma_load_2d(dst + NT * 128, &tm_x, &full[st], (ks0 + i) * kI8K + 64, mt * NT);
+        };
+        const int head = min(nk, kStages);
+        if (elect_one()) {
+            // before the kernels ahead in the stream are complete, the weights may be brought on their way
+            for (int i = 0; i < head; i++) {
+                if (p.early)
+                    load_w(i, i);
+                else
+                    tma_prefetch_2d(&tm_w, (ks0 + i) * kI8K, nt * kI8Rows);
+            }
+            pdl_wait();
+            pdl_launch_dependents();
+            for (int i = 0; i < head; i++) {
+                if (!p.early)
+                    load_w(i, i);
+                load_x(i, i);
+            }
+            for (int i = head; i < nk; i++) {
+                const int st = i % kStages;
+                if (!mbar_wait(&done[st], (i / kStages - 1) & 1)) {
+                    record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                    break;
+                }
+                load_w(i, st);
+                load_x(i, st);
+            }
+        }
+    } else if (warp == kI8Conv + 1) {
+        // ---------------- MMA
+        if (elect_one()) {
+            constexpr uint32_t id = idesc_f16(kI8Rows, NT, 0);
+            bool ok = true;
+            int i = 0;
+            for (; i < nk; i++) {
+                const int st = i % kStages;
+                ok = mbar_wait(&full[st], (i / kStages) & 1) && mbar_wait(&a_full[st], (i / kStages) & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * NT * kI8K * 2));
+#pragma unroll
+                for (int j = 0; j < kI8K / 16; j++)
+                    mma_f16_ts(tmem, a_ring + st * kI8ACols + j * 8, xd + (j / 4) * (NT * 128 / 16) + (j % 4) * 2, id,
+                               (i | j) != 0);
+                mma_commit(&done[st]);
+                if (i + 1 == nk)
+                    mma_commit(acc_full);
+            }
+            if (!ok) {
+                // copies on their way land before the CTA leaves, and the epilogue hears of the MMAs issued
+                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                ring_drain(full, kStages, i, min(nk, i + kStages));
+                mma_commit(acc_full);
+            }
+        }
+    } else {
+        // ---------------- weights to fp16
+        for (int i = 0; i < nk; i++) {
+            const int st = i % kStages;
+            // a stage that has landed was copied when the MMAs on its TMEM columns were done
+            if (!mbar_wait_warp(&full[st], (i / kStages) & 1))
+                break;
+            tc_fence_after();
+            convert_part(sW + st * kI8WBytes, a_ring + st * kI8ACols, warp, lane);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&a_full[st]);
+        }
+        pdl_wait();
+        if (!mbar_wait_warp(acc_full, 0)) {
+            if (threadIdx.x == 0)
+                record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+            // longer than the issuing thread can take over its own waits
+            for (int i = 0; i < 2 * nk + kStages + 4 && !mbar_wait_warp(acc_full, 0); i++) {
+            }
+        }
+        tc_fence_after();
+    }
+    __syncwarp();
+    auto store = [&](int m, int n, float v) {
+        v = __fmul_rn(__fmul_rn(v, p.x_scale[m]), p.w_scale[n]);
+        if (p.y_fp32)
+            reinterpret_cast<float *>(p.y)[(size_t)m * p.N + n] = v;
+        else
+            reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)m * p.N + n] = __float2bfloat16_rn(v);
+    };
+    const int cols = min(NT, p.M - mt * NT);   // tokens of this tile
+    if (warp < kI8Conv) {
+        // every other 32 tokens
+        const int quad = warp & 3, r = quad * 32 + lane, n = nt * kI8Rows + r;
+        for (int c = (warp >> 2) * 32; c < cols; c += 64) {
+            uint32_t v[32];
+            __syncwarp();   // the stores before may have parted the warp
+            tmem_ld32_start(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
+            tmem_ld32_finish(v);
+#pragma unroll
+            for (int i = 0; i < 32; i++) {
+                if (c + i < cols) {
+                    if (p.split > 1)
+                        red[(c + i) * 128 + r] = __uint_as_float(v[i]);
+                    else if (n < p.N)
+                        store(mt * NT + c + i, n, __uint_as_float(v[i]));
+                }
+            }
+        }
+    }
+    if (p.split > 1) {
+        // ---------------- the tokens are shared out
+        __syncwarp();
+        __syncthreads();
+        cluster_sync();
+        const int c0 = cols * rank / p.split, c1 = cols * (rank + 1) / p.split;
+        for (int i = threadIdx.x; i < (c1 - c0) * 128; i += kIsThreads) {
+            const int c = c0 + i / 128, r = i % 128, n = nt * kI8Rows + r;
+            const uint32_t at = smem_addr(&red[c * 128 + r]);
+            float part[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                if (q < p.split)
+                    part[q] = ld_cluster_f32(at, (uint32_t)q);
+            float v = part[0];
+#pragma unroll
+            for (int q = 1; q < 8; q++)
+                if (q < p.split)
+                    v += part[q];
+            if (n < p.N)
+                store(mt * NT + c, n, v);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kI8Conv + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- many tokens
+// CTA pairs, 256 weight rows x 256 tokens at a time, persistent.  Both CTAs
+// convert their 128 weight rows into their own TMEM; the leader's MMAs read
+// both, and half of the tokens from each CTA's shared memory.
+constexpr int kItTokens = 256;
+constexpr int kItEpi = 4;
+constexpr int kItThreads = 32 * (kI8Conv + kItEpi + 2);   // converting, epilogue, copies, MMA
+constexpr int kItStages = 4;
+constexpr int kItXBytes = kItTokens / 2 * kI8K * 2, kItStageBytes = kI8WBytes + kItXBytes;
+constexpr size_t kItSmem = 512 + (size_t)kItStages * kItStageBytes;
+constexpr int kItGroup = 8;   // raster: token tiles per group
+
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
+    int8_tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Int8Params p)
+{
+    constexpr int kStages = kItStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sW = smem, *sX = sW + kStages * kI8WBytes;
+    uint64_t *full_w = reinterpret_cast<uint64_t *>(sX + kStages * kItXBytes), *full_x = full_w + kStages;
+    uint64_t *a_full = full_x + kStages, *done = a_full + kStages, *acc_full = done + kStages, *acc_empty = acc_full + 1;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 1);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    volatile uint32_t *s_loaded = s_tmem + 2, *s_issued = s_tmem + 3;   // stages copied and multiplied
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = (int)cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(&full_w[s], 1);
+            mbar_init(&full_x[s], 1);
+            mbar_init(&a_full[s], 2 * kI8Conv);
+            mbar_init(&done[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * kItEpi);
+        *s_abort = 0;
+        *s_loaded = 0;
+        *s_issued = 0;
+        mbar_fence_init();
+    }
+    if (warp == kI8Conv + kItEpi + 1)
+        tmem_alloc_pair(s_tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers and TMEM before anything of the pair touches them
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem, a_ring = tmem + kItTokens;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int cid = (int)cluster_id_x(), ncl = (int)cluster_count_x();
+    const int ntot = p.mtiles * p.ntiles;
+    auto fail = [&]() {
+        record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+        *s_abort = 1;
+    };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *s_abort); };
+    // groups of kItGroup token tiles, the token tile fastest: the pairs that run together share weights and tokens in L2
+    auto tile_at = [&](int t, int &mt, int &nt) {
+        const int per = kItGroup * p.ntiles, g = t / per, i = t % per, gm = min(kItGroup, p.mtiles - g * kItGroup);
+        mt = g * kItGroup + i % gm;
+        nt = i / gm;
+    };
+    // columns of a tile's MMAs
+    auto width = [&](int mt) { return (min(kItTokens, p.M - mt * kItTokens) + 31) & ~31; };
+
+    if (warp == kI8Conv + kItEpi) {
+        // ---------------- copies: this CTA's weight rows, and half of the tokens for the leader's barrier
+        if (elect_one()) {
+            uint32_t it = 0;
+            for (int t = cid; t < ntot && !*s_abort; t += ncl) {
+                int mt, nt;
+                tile_at(t, mt, nt);
+                const int m0 = mt * kItTokens + crank * (width(mt) / 2), n0 = nt * 256 + crank * 128;
+                for (int ks = 0; ks < p.ksteps; ks++, it++) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(&done[st], ((it / kStages) & 1) ^ 1)) {
+                        fail();
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full_w[st], kI8WBytes);
+                    tma_load_2d(sW + st * kI8WBytes, &tm_w, &full_w[st], ks * kI8K, n0);
+                    const uint32_t bar = cluster_addr(&full_x[st], 0);
+                    if (crank == 0)
+                        mbar_arrive_expect_tx(&full_x[st], 2 * kItXBytes);
+                    tma_load_2d_pair(sX + st * kItXBytes, &tm_x, bar, ks * kI8K, m0);
+                    tma_load_2d_pair(sX + st * kItXBytes + kItXBytes / 2, &tm_x, bar, ks * kI8K + 64, m0);
+                }
+            }
+            // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
+            for (int k = 0; k < kStages && !*s_abort; k++) {
+                const uint32_t i2 = it + k;
+                if (i2 >= (uint32_t)kStages && !mbar_wait(&done[i2 % kStages], ((i2 / kStages) & 1) ^ 1))
+                    fail();
+            }
+            *s_loaded = it;
+        }
+    } else if (warp == kI8Conv + kItEpi + 1) {
+        // ---------------- MMA, by one thread of the pair's leader
+        if (crank == 0 && elect_one()) {
+            uint32_t it = 0, lt = 0;
+            for (int t = cid; t < ntot && !*s_abort; t += ncl, lt++) {
+                int mt, nt;
+                tile_at(t, mt, nt);
+                const uint32_t id = idesc_f16(256, width(mt), 0);
+                if (lt >= 1 && !mbar_wait(acc_empty, (lt - 1) & 1)) {
+                    fail();
+                    break;
+                }
+                tc_fence_after();
+                bool ok = true;
+                for (int ks = 0; ks < p.ksteps; ks++, it++) {
+                    const int st = it % kStages;
+                    if (!mbar_wait(&full_x[st], (it / kStages) & 1) || !mbar_wait(&a_full[st], (it / kStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * kItXBytes));
+#pragma unroll
+                    for (int j = 0; j < kI8K / 16; j++)
+                        mma_f16_ts_pair(tmem, a_ring + st * kI8ACols + j * 8, xd + (j / 4) * (kItXBytes / 2 / 16) + (j % 4) * 2,
+                                        id, (ks | j) != 0);
+                    mma_commit_pair(&done[st]);
+                    if (ks + 1 == p.ksteps)
+                        mma_commit_pair(acc_full);
+                }
+                if (!ok) {
+                    fail();
+                    break;
+                }
+            }
+            *s_issued = it;
+        }
+    } else if (warp < kI8Conv) {
+        // ---------------- weights to fp16, stage by stage, also while a tile's accumulator is being read
+        uint32_t it = 0;
+        const uint32_t total = (uint32_t)((ntot - cid + ncl - 1) / ncl) * (uint32_t)p.ksteps;
+        for (; it < total; it++) {
+            const int st = it % kStages;
+            // a stage that has landed was copied when the MMAs on its TMEM columns were done
+            if (!mbar_wait_warp(&full_w[st], (it / kStages) & 1)) {
+                fail();
+                break;
+            }
+            if (aborted())
+                break;
+            tc_fence_after();
+            convert_part(sW + st * kI8WBytes, a_ring + st * kI8ACols, warp, lane);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_release(cluster_addr(&a_full[st], 0));
+        }
+    } else {
+        // ---------------- epilogue: a warp has 32 weight rows, one a lane
+        const int quad = warp & 3;
+        const uint32_t bar = cluster_addr(acc_empty, 0);
+        uint32_t lt = 0;
+        for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
+            int mt, nt;
+            tile_at(t, mt, nt);
+            const int n = nt * 256 + crank * 128 + quad * 32 + lane, rows = min(kItTokens, p.M - mt * kItTokens);
+            const float sw = n < p.N ? p.w_scale[n] : 0.0f;
+            if (!mbar_wait_warp(acc_full, lt & 1)) {
+                fail();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
+            uint32_t buf[2][32];
+            tmem_ld32_start(acc, buf[0]);
+#pragma unroll
+            for (int c = 0; c < kItTokens / 32; c++) {
+                uint32_t(&v)[32] = buf[c & 1];
+                __syncwarp();   // the stores before may have parted the warp
+                tmem_ld32_finish(v);
+                if (c + 1 < kItTokens / 32) {
+                    tmem_ld32_start(acc + (c + 1) * 32, buf[(c + 1) & 1]);
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(bar);
+                }
+                const int left = rows - c * 32, m = mt * kItTokens + c * 32;
+                if (left <= 0)
+                    continue;
+                const float sx = lane < left ? p.x_scale[m + lane] : 0.0f;
+                const size_t at = (size_t)m * p.N + n;
+#pragma unroll
+                for (int i = 0; i < 32; i++) {
+                    const float s = __shfl_sync(0xffffffffu, sx, i);
+                    const float y = __fmul_rn(__fmul_rn(__uint_as_float(v[i]), s), sw);
+                    if (i < left && n < p.N) {
+                        if (p.y_fp32)
+                            reinterpret_cast<float *>(p.y)[at + (size_t)i * p.N] = y;
+                        else
+                            reinterpret_cast<__nv_bfloat16 *>(p.y)[at + (size_t)i * p.N] = __float2bfloat16_rn(y);
+                    }
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kI8Conv + kItEpi + 1 && *s_abort) {
+        // after a wait that gave up: copies on their way land, and MMAs issued are done, before either CTA leaves
+        const uint32_t loaded = *s_loaded, issued = *s_issued, from = loaded > (uint32_t)kStages ? loaded - kStages : 0u;
+        ring_drain(full_w, kStages, from, loaded);
+        if (crank == 0) {
+            ring_drain(full_x, kStages, from, loaded);
+            if (issued > 0)
+                ring_drain(done, kStages, issued - 1, issued);
+        }
+        __syncwarp();
+    }
+    cluster_sync();  // neither CTA leaves while the other may still signal or read it
+    if (warp == kI8Conv + kItEpi + 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+cudaError_t maps(CUtensorMap *tw, CUtensorMap *tx, const Int8GemmArgs &a, uint32_t tokens)
+{
+    const cudaError_t e = encode_tensor_map_2d(tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K, (uint64_t)a.N,
+                                               (uint64_t)a.K, kI8K, kI8Rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    return e != cudaSuccess ? e
+                            : encode_tensor_map_2d(tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, (uint64_t)a.K, (uint64_t)a.M,
+                                                   (uint64_t)a.K * 2, 64, tokens, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+Int8Params params(const Int8GemmArgs &a)
+{
+    Int8Params p = {};
+    p.x_scale = a.x_scale;
+    p.w_scale = a.w_scale;
+    p.M = (int)a.M;
+    p.N = (int)a.N;
+    p.ksteps = (int)((a.K + kI8K - 1) / kI8K);
+    p.split = 1;
+    p.early = 1;
+    p.y = a.y;
+    p.y_fp32 = a.y_fp32 ? 1 : 0;
+    p.ctl = a.ctl;
+    return p;
+}
+
+template <int NT>
+cudaError_t run_int8_stream(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    using S = IsShape<NT>;
+    CUtensorMap tw, tx;
+    cudaError_t e = maps(&tw, &tx, a, NT);
+    if (e == cudaSuccess)
+        e = allow_smem<int8_stream_kernel<NT>>(S::kSmem, dev);
+    if (e != cudaSuccess)
+        return e;
+    Int8Params p = params(a);
+    p.mtiles = (int)((a.M + NT - 1) / NT);
+    const int64_t tiles = (int64_t)p.mtiles * ((a.N + kI8Rows - 1) / kI8Rows);
+    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, p.ksteps, (int64_t)S::kCtas * dev.num_sms / tiles}));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.split));
+    cfg.blockDim = dim3(kIsThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, int8_stream_kernel<NT>, tw, tx, p);
+}
+
+cudaError_t run_int8_tile(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    CUtensorMap tw, tx;
+    cudaError_t e = maps(&tw, &tx, a, kItTokens / 2);
+    if (e == cudaSuccess)
+        e = allow_smem<int8_tile_kernel>(kItSmem, dev);
+    if (e != cudaSuccess)
+        return e;
+    Int8Params p = params(a);
+    p.mtiles = (int)((a.M + kItTokens - 1) / kItTokens);
+    p.ntiles = (int)((a.N + 255) / 256);
+    const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+    return launch_dependent(int8_tile_kernel, dim3(2 * (unsigned)std::min<int64_t>(tiles, dev.num_sms / 2)), kItThreads,
+                            kItSmem, s, tw, tx, p);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    if (a.M <= 16)
+        return run_int8_stream<16>(a, s, dev);
+    if (a.M <= 32)
+        return run_int8_stream<32>(a, s, dev);
+    if (a.M <= 64)
+        return run_int8_stream<64>(a, s, dev);
+    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+    if (a.M <= 128 || (big * 5 <= dev.num_sms && a.M <= 512))
+        return run_int8_stream<128>(a, s, dev);
+    return run_int8_tile(a, s, dev);
+}
+
+}  // namespace nvfp4

@@ -270,6 +270,32 @@ cudaError_t launch_moe_wgrad(const MoeWgradArgs &a, cudaStream_t s, const Device
 cudaError_t encode_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, const uint64_t (&dims)[3],
                                  const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 
+// 8-bit integers with a scale a row (csrc/int8_quant.cu): codes, or the same
+// integers as fp16.
+struct Int8QuantArgs {
+    const void *x;
+    bool x_fp32;
+    int64_t rows, cols, ld;
+    void *out;
+    bool half;
+    float *scale;
+};
+cudaError_t launch_int8_quantize(const Int8QuantArgs &a, cudaStream_t s);
+cudaError_t launch_int8_widen(const int8_t *in, int64_t n, void *out, cudaStream_t s);
+// Their product (csrc/gemm_int8.cu), launched right behind the kernel that
+// wrote x on the same stream.
+struct Int8GemmArgs {
+    const void *x;           // M x K integers as fp16
+    const float *x_scale;    // M
+    const int8_t *w;         // N x K
+    const float *w_scale;    // N
+    int64_t M, N, K;
+    void *y;
+    bool y_fp32;
+    uint32_t *ctl;
+};
+cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev);
+
 // Distillation loss and gradient (csrc/distill.cu).
 constexpr int kDistillMaxK = 1024;             // teacher entries per row
 constexpr int64_t kDistillMaxSlice = 200 * 1024;  // bytes of a row one CTA (of up to 8) holds
