@@ -262,11 +262,18 @@ __global__ void __launch_bounds__(kMqThreads)
 }
 
 // Rows of x to their places in the experts' order, each read once: a warp takes
-// 256 elements of a row, quantises them and writes codes and scale words to
-// every place that the row has (a token has one for each of its experts).  The
-// rows behind an expert's last one are left as they are: a product's output
-// rows depend on their own row only.
-constexpr int kMrChunk = 256, kMrUnroll = 2;
+// 1024 elements of a row, quantises them and writes codes and scale words to
+// every place that the row has (a token has one for each of its experts).  Four
+// lanes hold a block of 32, eight elements each, in four passes over 256; the
+// codes change lanes so that each lane stores 16 bytes, and the scale words are
+// stored a place a lane.  The rows behind an expert's last one are left as they
+// are: a product's output rows depend on their own row only.
+//
+// What bounds it: bytes; with 4-byte stores and a scale word at a time it was
+// bound by issue (8192 tokens of 4096, 8 places each: 66 us).  Measured against
+// it: one copy of the codes, whose rows the product gathers by TMA (four rows an
+// instruction): 18 cycles a row, and the product takes three times as long.
+constexpr int kMrChunk = 1024;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -275,44 +282,70 @@ __global__ void __launch_bounds__(256)
 {
     const int lane = threadIdx.x & 31;
     const int64_t chunks = (cols + kMrChunk - 1) / kMrChunk, ktiles = (cols + 127) / 128;
-    const int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kMrUnroll;
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), r = i / chunks, c0 = i % chunks * kMrChunk;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t some = m.k ? rows : min(rows, (int64_t)m.header[0]);   // grouped rows that there are
-    Raw8<T> raw[kMrUnroll];
+    if (r >= (m.k ? rows : min(rows, (int64_t)m.header[0])))   // grouped rows that there are
+        return;
+    Raw8<T> raw[4];
 #pragma unroll
-    for (int u = 0; u < kMrUnroll; u++) {
-        const int64_t r = (i0 + u) / chunks, c = (i0 + u) % chunks * kMrChunk + lane * 8;
+    for (int u = 0; u < 4; u++) {
+        const int64_t c = c0 + u * 256 + lane * 8;
         raw[u].zero();
-        if (r < some && c < cols)
+        if (c < cols)
             raw[u].load(x + r * ld + c);
     }
+    const int n = m.k ? m.k : 1;
+    // lane j: place j of the row
+    int mine = -1;
+    if (lane < n)
+        mine = m.padded[m.k ? r * n + lane : m.order[r]];
+    uint32_t q[4], word[4];   // word: this lane's half of the 256 elements, four blocks
 #pragma unroll
-    for (int u = 0; u < kMrUnroll; u++) {
-        const int64_t r = (i0 + u) / chunks, c = (i0 + u) % chunks * kMrChunk + lane * 8;
+    for (int u = 0; u < 4; u++) {
         uint32_t a = raw[u].amax_bits();
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
         uint32_t byte;
-        const uint32_t q = raw[u].encode(a, byte);
-        // the four blocks of 128 elements in one word
-        uint32_t word = 0;
+        q[u] = raw[u].encode(a, byte);
+        // bytes of lanes 4 b + .. of the half
+        uint32_t w = byte << (lane & 12) * 2;
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        w |= __shfl_xor_sync(0xffffffffu, w, 8);
+        word[u] = w;
+    }
+    // four lanes exchange: lane l gets pass l % 4 of its group of four, 16 bytes
 #pragma unroll
-        for (int b = 0; b < 4; b++)
-            word |= __shfl_sync(0xffffffffu, byte, (lane & 16) + 4 * b) << (8 * b);
-        if (r >= some)
-            break;
-        const int n = m.k ? m.k : 1;
-        for (int j = 0; j < n; j++) {
-            const int32_t at = m.k ? m.padded[r * n + j] : m.padded[m.order[r]];
-            if (at < 0)
-                continue;
-            if (c < cols)
-                *reinterpret_cast<uint32_t *>(codes + ((int64_t)at * cols + c) / 2) = q;
-            if ((lane & 15) == 0 && c < cols)
-                *reinterpret_cast<uint32_t *>(scales + (((int64_t)at >> 7) * ktiles + (c >> 7)) * 512 + (at & 31) * 16 +
-                                              (at & 127) / 32 * 4) = word;
+    for (int d = 1; d <= 2; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            if (!(u & d)) {
+                const uint32_t give = up ? q[u] : q[u | d];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+                q[u] = up ? got : q[u];
+                q[u | d] = up ? q[u | d] : got;
+            }
         }
+    }
+    const int64_t c = c0 + (lane & 3) * 256 + (lane >> 2) * 32;
+    // scale words: place lane / 8 (four places at a time), pass and half lane % 8
+    const uint32_t s0 = __shfl_sync(0xffffffffu, word[0], (lane & 1) * 16), s1 = __shfl_sync(0xffffffffu, word[1], (lane & 1) * 16);
+    const uint32_t s2 = __shfl_sync(0xffffffffu, word[2], (lane & 1) * 16), s3 = __shfl_sync(0xffffffffu, word[3], (lane & 1) * 16);
+    const int pass = (lane & 7) >> 1;
+    const uint32_t sw = pass & 2 ? (pass & 1 ? s3 : s2) : (pass & 1 ? s1 : s0);
+    const int64_t kt = c0 / 128 + (lane & 7);
+    for (int j0 = 0; j0 < n; j0 += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int at = j0 + j < n ? __shfl_sync(0xffffffffu, mine, j0 + j) : -1;
+            if (at >= 0 && c < cols)
+                *reinterpret_cast<uint4 *>(codes + ((int64_t)at * cols + c) / 2) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        const int at = __shfl_sync(0xffffffffu, mine, (j0 + (lane >> 3)) & 31);
+        if (j0 + (lane >> 3) < n && at >= 0 && kt < ktiles)
+            *reinterpret_cast<uint32_t *>(scales + ((int64_t)(at >> 7) * ktiles + kt) * 512 + (at & 31) * 16 +
+                                          (at & 127) / 32 * 4) = sw;
     }
 }
 
@@ -403,7 +436,7 @@ cudaError_t run_quantize_dirs(const MxQuantArgs &a, cudaStream_t s, const MoeRow
 template <typename T>
 cudaError_t run_quantize_rows(const MxQuantArgs &a, const MoeRows &m, cudaStream_t s)
 {
-    const int64_t tasks = a.rows * ((a.cols + kMrChunk - 1) / kMrChunk), per = 8 * kMrUnroll;
+    const int64_t tasks = a.rows * ((a.cols + kMrChunk - 1) / kMrChunk), per = 8;
     return launch_dependent(mx_quantize_rows_kernel<T>, dim3((unsigned)((tasks + per - 1) / per)), 256, 0, s,
                             (const T *)a.x, a.ld, a.rows, a.cols, a.codes, a.scales, m);
 }
