@@ -106,6 +106,13 @@ nvfp4_status nvfp4_int8_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, 
     if (ws_bytes < need)
         return NVFP4_ERR_WORKSPACE;
     NVFP4_TRY_DEVICE(dev);
+    if (int8_takes_tokens(M, N, K, *dev)) {
+        Int8GemmArgs a = gemm_args(x, nullptr, w_codes, w_scales, M, N, K, y, y_dtype, workspace);
+        a.raw = true;
+        a.raw_fp32 = x_dtype == NVFP4_OUT_FP32;
+        a.ldx = ldx;
+        return from_cuda(launch_int8_gemm(a, (cudaStream_t)stream, *dev));
+    }
     uint8_t *q = (uint8_t *)workspace + align256(kWsHeaderBytes);
     float *scale = (float *)(q + align256((size_t)M * K * 2));
     const Int8QuantArgs qa = {x, x_dtype == NVFP4_OUT_FP32, M, K, ldx, q, true, scale};

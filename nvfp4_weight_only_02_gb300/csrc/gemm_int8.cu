@@ -14,9 +14,12 @@
 // not again as two bytes written and read.  Tokens are quantised to fp16
 // integers by a kernel before this one and come by TMA.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
+#include "int8_codec.cuh"
 #include "internal.h"
+#include "mx_codec.cuh"
 #include "w4a4_pair.cuh"
 
 namespace nvfp4 {
@@ -26,11 +29,16 @@ namespace {
 constexpr int kI8K = 128;         // elements of K a stage
 constexpr int kI8Rows = 128;      // weight rows a CTA
 constexpr int kI8WBytes = kI8Rows * kI8K, kI8ACols = kI8K / 2;   // a stage's codes, and its columns as fp16 in TMEM
-constexpr int kI8Conv = 8;        // warps that convert: two for each 32 rows, half a stage's columns each
+// Warps that convert, in groups of four (32 rows each) that take turns: a stage
+// takes a group longer than the MMAs of few tokens (waits, shared memory, the
+// stores' completion), so two are in work at once.
+constexpr int kI8Conv = 8, kI8Groups = kI8Conv / 4;
 
 struct Int8Params {
     const float *x_scale, *w_scale;
-    int M, N;
+    const void *x;   // unquantised tokens (M x K, ldx between rows)
+    int64_t ldx;
+    int M, N, K;
     int ksteps;
     int mtiles, ntiles;
     int split;    // streaming: CTAs of a cluster that share a tile's K
@@ -50,7 +58,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]^T over 16 elements of K, f16 operands.
@@ -72,21 +79,25 @@ __device__ __forceinline__ void mma_f16_ts_pair(uint32_t d, uint32_t a, uint64_t
         : "memory");
 }
 
-// A converting warp's part of a stage: row 32 (warp % 4) + lane, columns 64 (warp / 4) .. + 63, from the swizzled
-// layout of a TMA copy.
-__device__ __forceinline__ void convert_part(const uint8_t *stage, uint32_t a_tmem, int warp, int lane)
+// A converting warp's part of a stage: row 32 (warp % 4) + lane, from the swizzled layout of a TMA copy.
+__device__ __forceinline__ void convert_rows(const uint8_t *stage, uint32_t a_tmem, int warp, int lane)
 {
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    uint32_t v[32];
+    const int row = (warp & 3) * 32 + lane;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((4 * half + j) ^ (row & 7)) << 4));
-        int8x4_to_h2x2(q.x, v[8 * j], v[8 * j + 1]);
-        int8x4_to_h2x2(q.y, v[8 * j + 2], v[8 * j + 3]);
-        int8x4_to_h2x2(q.z, v[8 * j + 4], v[8 * j + 5]);
-        int8x4_to_h2x2(q.w, v[8 * j + 6], v[8 * j + 7]);
+    for (int h = 0; h < 2; h++) {
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((4 * h + j) ^ (row & 7)) << 4));
+            int8x4_to_h2x2(q.x, v[8 * j], v[8 * j + 1]);
+            int8x4_to_h2x2(q.y, v[8 * j + 2], v[8 * j + 3]);
+            int8x4_to_h2x2(q.z, v[8 * j + 4], v[8 * j + 5]);
+            int8x4_to_h2x2(q.w, v[8 * j + 6], v[8 * j + 7]);
+        }
+        tmem_st32(a_tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 32, v);
     }
-    tmem_st32(a_tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 32, v);
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank)
@@ -102,51 +113,70 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank)
 // ---------------------------------------------------------------- few tokens
 // A CTA takes 128 weight rows and NT tokens; K is split over the CTAs of a
 // cluster when there are fewer tiles than CTA places, the shares added in rank
-// order through distributed shared memory.
-constexpr int kIsThreads = 32 * (kI8Conv + 2);  // + copies, MMA
+// order through distributed shared memory.  Codes, tokens and converted weights
+// have rings of their own: codes are let go when they are converted, tokens and
+// TMEM columns when they are multiplied.  Very few tokens are quantised by the
+// CTAs themselves (each needs the whole rows for their maxima, and writes the
+// part of K that it multiplies) while the first weights are on their way: a
+// kernel of its own costs a launch and 1 to 2 us.
+constexpr int kIsThreads = 32 * (kI8Conv + 3);  // + copies of weights, of tokens, MMA
+enum Int8Tokens { kInts, kRawBf16, kRawFp32 };
 
-template <int NT>
+template <int NT, Int8Tokens kTok>
 struct IsShape {
+    static constexpr bool kOwn = kTok != kInts;
     static constexpr int kCtas = NT <= 64 ? 2 : 1;        // on an SM
-    static constexpr int kStageBytes = kI8WBytes + NT * kI8K * 2;
+    static constexpr int kXBytes = NT * kI8K * 2;
     static constexpr int kTmemCols = 512 / kCtas;
     static constexpr int kAccCols = NT < 32 ? 32 : NT;
-    static constexpr int kStages = NT <= 64 ? 3 : 4;
-    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kW = kOwn ? 3 : NT == 16 ? 5 : NT == 32 ? 4 : NT == 64 ? 3 : 5;   // stages of codes,
+    static constexpr int kX = kOwn ? 15 : NT == 16 ? 5 : NT == 32 ? 4 : NT == 64 ? 3 : 4;  // of tokens (own: all of a CTA's)
+    static constexpr int kA = NT <= 64 ? 3 : 5;                                            // of converted weights
+    static constexpr int kRing = kW * kI8WBytes + kX * kXBytes;
     // CTAs that fit an SM's shared memory never want more than its TMEM columns together (w4a4_shape.h)
     static constexpr int kLeast = kTmemCols / 128 * 46 * 1024;
     static constexpr size_t kSmem = 1024 + (kRing > kLeast ? kRing : kLeast);
-    static_assert(kAccCols + kStages * kI8ACols <= kTmemCols && NT * 512 <= kRing && kSmem * kCtas <= 226 * 1024, "fits");
+    static_assert(kW >= kA && kA >= kI8Groups, "see the converting warps' waits");
+    static_assert(kAccCols + kA * kI8ACols <= kTmemCols && NT * 512 <= kRing && (kSmem + 1536) * kCtas <= 228 * 1024, "fits");
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kIsThreads, IsShape<NT>::kCtas)
+template <int NT, Int8Tokens kTok>
+__global__ void __launch_bounds__(kIsThreads, IsShape<NT, kTok>::kCtas)
     int8_stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Int8Params p)
 {
-    using S = IsShape<NT>;
-    constexpr int kStages = S::kStages;
+    using S = IsShape<NT, kTok>;
+    constexpr int kW = S::kW, kX = S::kX, kA = S::kA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *sW = smem, *sX = sW + kStages * kI8WBytes;
-    float *red = reinterpret_cast<float *>(smem);   // [NT][128], once the ring is drained
-    __shared__ __align__(8) uint64_t full[kStages], a_full[kStages], done[kStages], acc_full[1];
+    uint8_t *sW = smem, *sX = sW + kW * kI8WBytes;
+    float *red = reinterpret_cast<float *>(smem);   // [NT][128], once the rings are drained
+    __shared__ __align__(8) uint64_t w_full[kW], w_empty[kW], x_full[kX], x_empty[kX], a_full[kA], a_empty[kA], acc_full[1];
     __shared__ uint32_t s_tmem;
+    __shared__ float s_scale[S::kOwn ? NT : 1];
+    __shared__ uint32_t s_max[S::kOwn ? kI8Conv : 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
     const int tile = blockIdx.x / p.split, nt = tile / p.mtiles, mt = tile % p.mtiles;
     const int ks0 = (int)((int64_t)p.ksteps * rank / p.split), ks1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);
-    const int nk = ks1 - ks0;
+    const int nk = ks1 - ks0, cols = min(NT, p.M - mt * NT);   // stages; tokens of this tile
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; s++) {
-            mbar_init(&full[s], 1);
-            mbar_init(&a_full[s], kI8Conv);
-            mbar_init(&done[s], 1);
+        for (int s = 0; s < kW; s++) {
+            mbar_init(&w_full[s], 1);
+            mbar_init(&w_empty[s], 4);
+        }
+        for (int s = 0; s < kX; s++) {
+            mbar_init(&x_full[s], S::kOwn ? 32 * kI8Conv : 1);
+            mbar_init(&x_empty[s], 1);
+        }
+        for (int s = 0; s < kA; s++) {
+            mbar_init(&a_full[s], 4);
+            mbar_init(&a_empty[s], 1);
         }
         mbar_init(acc_full, 1);
         mbar_fence_init();
     }
-    if (warp == kI8Conv + 1) {
+    if (warp == kI8Conv + 2) {
         tmem_alloc(&s_tmem, S::kTmemCols);
         tmem_relinquish();
     }
@@ -156,103 +186,153 @@ __global__ void __launch_bounds__(kIsThreads, IsShape<NT>::kCtas)
     const uint32_t tmem = s_tmem, a_ring = tmem + S::kAccCols;
 
     if (warp == kI8Conv) {
-        // ---------------- copies
-        auto load_w = [&](int i, int st) {
-            mbar_arrive_expect_tx(&full[st], S::kStageBytes);
-            tma_load_2d(sW + st * kI8WBytes, &tm_w, &full[st], (ks0 + i) * kI8K, nt * kI8Rows);
+        // ---------------- copies of the weights' codes
+        auto load = [&](int i) {
+            mbar_arrive_expect_tx(&w_full[i % kW], kI8WBytes);
+            tma_load_2d(sW + i % kW * kI8WBytes, &tm_w, &w_full[i % kW], (ks0 + i) * kI8K, nt * kI8Rows);
         };
-        auto load_x = [&](int i, int st) {
-            uint8_t *dst = sX + st * NT * kI8K * 2;
-            tma_load_2d(dst, &tm_x, &full[st], (ks0 + i) * kI8K, mt * NT);
-            tma_load_2d(dst + NT * 128, &tm_x, &full[st], (ks0 + i) * kI8K + 64, mt * NT);
-        };
-        const int head = min(nk, kStages);
         if (elect_one()) {
-            // before the kernels ahead in the stream are complete, the weights may be brought on their way
+            // Before the kernels ahead in the stream are complete, the weights may be brought on their way: into
+            // shared memory where nothing that can still run writes them (p.early), else into L2 only.
+            const int head = min(nk, kW);
             for (int i = 0; i < head; i++) {
                 if (p.early)
-                    load_w(i, i);
+                    load(i);
                 else
                     tma_prefetch_2d(&tm_w, (ks0 + i) * kI8K, nt * kI8Rows);
             }
             pdl_wait();
             pdl_launch_dependents();
-            for (int i = 0; i < head; i++) {
-                if (!p.early)
-                    load_w(i, i);
-                load_x(i, i);
-            }
-            for (int i = head; i < nk; i++) {
-                const int st = i % kStages;
-                if (!mbar_wait(&done[st], (i / kStages - 1) & 1)) {
+            for (int i = p.early ? head : 0; i < nk; i++) {
+                if (i >= kW && !mbar_wait(&w_empty[i % kW], (i / kW - 1) & 1)) {
                     record_status(p.ctl, NVFP4_ERR_TIMEOUT);
                     break;
                 }
-                load_w(i, st);
-                load_x(i, st);
+                load(i);
             }
         }
     } else if (warp == kI8Conv + 1) {
+        // ---------------- copies of the tokens
+        if (!S::kOwn && elect_one()) {
+            pdl_wait();
+            for (int i = 0; i < nk; i++) {
+                const int st = i % kX;
+                if (i >= kX && !mbar_wait(&x_empty[st], (i / kX - 1) & 1)) {
+                    record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                    break;
+                }
+                mbar_arrive_expect_tx(&x_full[st], S::kXBytes);
+                tma_load_2d(sX + st * S::kXBytes, &tm_x, &x_full[st], (ks0 + i) * kI8K, mt * NT);
+                tma_load_2d(sX + st * S::kXBytes + NT * 128, &tm_x, &x_full[st], (ks0 + i) * kI8K + 64, mt * NT);
+            }
+        }
+    } else if (warp == kI8Conv + 2) {
         // ---------------- MMA
         if (elect_one()) {
             constexpr uint32_t id = idesc_f16(kI8Rows, NT, 0);
-            bool ok = true;
+            bool ok = !S::kOwn || mbar_wait(&x_full[0], 0);
             int i = 0;
-            for (; i < nk; i++) {
-                const int st = i % kStages;
-                ok = mbar_wait(&full[st], (i / kStages) & 1) && mbar_wait(&a_full[st], (i / kStages) & 1);
+            for (; i < nk && ok; i++) {
+                const int st = i % kX, sa = i % kA;
+                ok = (S::kOwn || mbar_wait(&x_full[st], (i / kX) & 1)) && mbar_wait(&a_full[sa], (i / kA) & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
-                const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * NT * kI8K * 2));
+                const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * S::kXBytes));
 #pragma unroll
                 for (int j = 0; j < kI8K / 16; j++)
-                    mma_f16_ts(tmem, a_ring + st * kI8ACols + j * 8, xd + (j / 4) * (NT * 128 / 16) + (j % 4) * 2, id,
+                    mma_f16_ts(tmem, a_ring + sa * kI8ACols + j * 8, xd + (j / 4) * (NT * 128 / 16) + (j % 4) * 2, id,
                                (i | j) != 0);
-                mma_commit(&done[st]);
+                if (!S::kOwn)
+                    mma_commit(&x_empty[st]);
+                mma_commit(&a_empty[sa]);
                 if (i + 1 == nk)
                     mma_commit(acc_full);
             }
             if (!ok) {
                 // copies on their way land before the CTA leaves, and the epilogue hears of the MMAs issued
                 record_status(p.ctl, NVFP4_ERR_TIMEOUT);
-                ring_drain(full, kStages, i, min(nk, i + kStages));
+                if (!S::kOwn)
+                    ring_drain(x_full, kX, i, min(nk, i + kX));
+                ring_drain(w_full, kW, i, min(nk, i + kA + kW));
                 mma_commit(acc_full);
             }
         }
     } else {
+        if constexpr (S::kOwn) {
+            // ---------------- this CTA's part of the tokens, as integers in the swizzled layout of a TMA copy
+            pdl_wait();
+            using T = std::conditional_t<kTok == kRawFp32, float, __nv_bfloat16>;
+            const int k0 = ks0 * kI8K / 8, n8 = p.K / 8;
+            for (int m = 0; m < p.M; m++) {
+                const T *src = reinterpret_cast<const T *>(p.x) + (int64_t)m * p.ldx;
+                uint32_t a = 0;
+#pragma unroll 4
+                for (int i = threadIdx.x; i < n8; i += 32 * kI8Conv) {
+                    Raw8<T> r;
+                    r.load(src + i * 8);
+                    a = max(a, r.amax_bits());
+                }
+                a = __reduce_max_sync(0xffffffffu, a);
+                named_sync(1, 32 * kI8Conv);    // the token before has been read
+                if (lane == 0)
+                    s_max[warp] = a;
+                named_sync(1, 32 * kI8Conv);
+                a = __reduce_max_sync(0xffffffffu, s_max[lane & (kI8Conv - 1)]);
+                const Int8Row row(a);
+                if (threadIdx.x == 0)
+                    s_scale[m] = row.scale();
+                for (int i = threadIdx.x; i < nk * (kI8K / 8); i += 32 * kI8Conv) {
+                    uint4 h = make_uint4(0u, 0u, 0u, 0u);
+                    if (k0 + i < n8) {
+                        Raw8<T> r;
+                        r.load(src + (k0 + i) * 8);
+                        h = row.halves(r);
+                    }
+                    const int st = i / (kI8K / 8), g = i % (kI8K / 8);   // stage; eight elements of it
+                    *reinterpret_cast<uint4 *>(sX + st * S::kXBytes + (g >> 3) * (NT * 128) + m * 128 +
+                                               (((g & 7) ^ (m & 7)) << 4)) = h;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&x_full[0]);
+            // near ties part a warp; what follows needs all of its lanes together
+            __syncwarp();
+        }
         // ---------------- weights to fp16
-        for (int i = 0; i < nk; i++) {
-            const int st = i % kStages;
-            // a stage that has landed was copied when the MMAs on its TMEM columns were done
-            if (!mbar_wait_warp(&full[st], (i / kStages) & 1))
+        for (int i = warp / 4; i < nk; i += kI8Groups) {
+            const int sw = i % kW, sa = i % kA;
+            // In this order: the other group may have had this barrier's use before, and a wait for a use passes while
+            // the one before it has not even completed.  The MMAs kA stages ago are behind that one (kW >= kA).
+            if ((i >= kA && !mbar_wait_warp(&a_empty[sa], (i / kA - 1) & 1)) || !mbar_wait_warp(&w_full[sw], (i / kW) & 1))
                 break;
             tc_fence_after();
-            convert_part(sW + st * kI8WBytes, a_ring + st * kI8ACols, warp, lane);
+            convert_rows(sW + sw * kI8WBytes, a_ring + sa * kI8ACols, warp, lane);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&a_full[st]);
+            if (lane == 0) {
+                mbar_arrive(&w_empty[sw]);
+                mbar_arrive(&a_full[sa]);
+            }
         }
         pdl_wait();
         if (!mbar_wait_warp(acc_full, 0)) {
             if (threadIdx.x == 0)
                 record_status(p.ctl, NVFP4_ERR_TIMEOUT);
             // longer than the issuing thread can take over its own waits
-            for (int i = 0; i < 2 * nk + kStages + 4 && !mbar_wait_warp(acc_full, 0); i++) {
+            for (int i = 0; i < 3 * nk + kX + kW + kA + 4 && !mbar_wait_warp(acc_full, 0); i++) {
             }
         }
         tc_fence_after();
     }
     __syncwarp();
     auto store = [&](int m, int n, float v) {
-        v = __fmul_rn(__fmul_rn(v, p.x_scale[m]), p.w_scale[n]);
+        v = __fmul_rn(__fmul_rn(v, S::kOwn ? s_scale[m] : p.x_scale[m]), p.w_scale[n]);
         if (p.y_fp32)
             reinterpret_cast<float *>(p.y)[(size_t)m * p.N + n] = v;
         else
             reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)m * p.N + n] = __float2bfloat16_rn(v);
     };
-    const int cols = min(NT, p.M - mt * NT);   // tokens of this tile
     if (warp < kI8Conv) {
         // every other 32 tokens
         const int quad = warp & 3, r = quad * 32 + lane, n = nt * kI8Rows + r;
@@ -277,10 +357,10 @@ __global__ void __launch_bounds__(kIsThreads, IsShape<NT>::kCtas)
         __syncwarp();
         __syncthreads();
         cluster_sync();
-        const int c0 = cols * rank / p.split, c1 = cols * (rank + 1) / p.split;
-        for (int i = threadIdx.x; i < (c1 - c0) * 128; i += kIsThreads) {
-            const int c = c0 + i / 128, r = i % 128, n = nt * kI8Rows + r;
-            const uint32_t at = smem_addr(&red[c * 128 + r]);
+        const int c0 = cols * 128 * rank / p.split, c1 = cols * 128 * (rank + 1) / p.split;
+        for (int i = c0 + threadIdx.x; i < c1; i += kIsThreads) {
+            const int c = i / 128, n = nt * kI8Rows + i % 128;
+            const uint32_t at = smem_addr(&red[i]);
             float part[8];
 #pragma unroll
             for (int q = 0; q < 8; q++)
@@ -299,7 +379,7 @@ __global__ void __launch_bounds__(kIsThreads, IsShape<NT>::kCtas)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kI8Conv + 1) {
+    if (warp == kI8Conv + 2) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kTmemCols);
     }
@@ -313,14 +393,10 @@ constexpr int kItTokens = 256;
 constexpr int kItEpi = 4;
 constexpr int kItThreads = 32 * (kI8Conv + kItEpi + 2);   // converting, epilogue, copies, MMA
 constexpr int kItStages = 4;
+static_assert(kItStages % kI8Groups == 0, "see the converting warps' waits");
 constexpr int kItXBytes = kItTokens / 2 * kI8K * 2, kItStageBytes = kI8WBytes + kItXBytes;
 constexpr size_t kItSmem = 512 + (size_t)kItStages * kItStageBytes;
 constexpr int kItGroup = 8;   // raster: token tiles per group
-
-__device__ __forceinline__ void mbar_arrive_release(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 
 __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
     int8_tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Int8Params p)
@@ -340,7 +416,7 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
         for (int s = 0; s < kStages; s++) {
             mbar_init(&full_w[s], 1);
             mbar_init(&full_x[s], 1);
-            mbar_init(&a_full[s], 2 * kI8Conv);
+            mbar_init(&a_full[s], 2 * 4);
             mbar_init(&done[s], 1);
         }
         mbar_init(acc_full, 1);
@@ -446,11 +522,12 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp < kI8Conv) {
         // ---------------- weights to fp16, stage by stage, also while a tile's accumulator is being read
-        uint32_t it = 0;
+        uint32_t it = (uint32_t)warp / 4;
         const uint32_t total = (uint32_t)((ntot - cid + ncl - 1) / ncl) * (uint32_t)p.ksteps;
-        for (; it < total; it++) {
+        for (; it < total; it += kI8Groups) {
             const int st = it % kStages;
-            // a stage that has landed was copied when the MMAs on its TMEM columns were done
+            // a stage that has landed was copied when the MMAs on its TMEM columns were done (a group has every use of
+            // a barrier that it has one of: kStages is a multiple of the groups)
             if (!mbar_wait_warp(&full_w[st], (it / kStages) & 1)) {
                 fail();
                 break;
@@ -458,11 +535,11 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
             if (aborted())
                 break;
             tc_fence_after();
-            convert_part(sW + st * kI8WBytes, a_ring + st * kI8ACols, warp, lane);
+            convert_rows(sW + st * kI8WBytes, a_ring + st * kI8ACols, warp, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_release(cluster_addr(&a_full[st], 0));
+                mbar_arrive_cluster(cluster_addr(&a_full[st], 0));   // hands over TMEM that is written (wait::st)
         }
     } else {
         // ---------------- epilogue: a warp has 32 weight rows, one a lane
@@ -541,9 +618,9 @@ cudaError_t maps(CUtensorMap *tw, CUtensorMap *tx, const Int8GemmArgs &a, uint32
 {
     const cudaError_t e = encode_tensor_map_2d(tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K, (uint64_t)a.N,
                                                (uint64_t)a.K, kI8K, kI8Rows, CU_TENSOR_MAP_SWIZZLE_128B);
-    return e != cudaSuccess ? e
-                            : encode_tensor_map_2d(tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, (uint64_t)a.K, (uint64_t)a.M,
-                                                   (uint64_t)a.K * 2, 64, tokens, CU_TENSOR_MAP_SWIZZLE_128B);
+    return e != cudaSuccess || !tx ? e
+                                   : encode_tensor_map_2d(tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, (uint64_t)a.K,
+                                                          (uint64_t)a.M, (uint64_t)a.K * 2, 64, tokens, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 Int8Params params(const Int8GemmArgs &a)
@@ -553,29 +630,40 @@ Int8Params params(const Int8GemmArgs &a)
     p.w_scale = a.w_scale;
     p.M = (int)a.M;
     p.N = (int)a.N;
+    p.K = (int)a.K;
+    p.x = a.x;
+    p.ldx = a.ldx;
     p.ksteps = (int)((a.K + kI8K - 1) / kI8K);
     p.split = 1;
-    p.early = 1;
     p.y = a.y;
     p.y_fp32 = a.y_fp32 ? 1 : 0;
     p.ctl = a.ctl;
     return p;
 }
 
-template <int NT>
+// CTAs of a cluster that share a tile's K.
+int stream_split(int64_t tiles, int64_t K, int places)
+{
+    return (int)std::max<int64_t>(1, std::min<int64_t>({8, (K + kI8K - 1) / kI8K, places / tiles}));
+}
+
+template <int NT, Int8Tokens kTok = kInts>
 cudaError_t run_int8_stream(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
-    using S = IsShape<NT>;
+    using S = IsShape<NT, kTok>;
     CUtensorMap tw, tx;
-    cudaError_t e = maps(&tw, &tx, a, NT);
+    cudaError_t e = maps(&tw, S::kOwn ? nullptr : &tx, a, NT);
     if (e == cudaSuccess)
-        e = allow_smem<int8_stream_kernel<NT>>(S::kSmem, dev);
+        e = allow_smem<int8_stream_kernel<NT, kTok>>(S::kSmem, dev);
     if (e != cudaSuccess)
         return e;
+    if (S::kOwn)
+        tx = tw;
     Int8Params p = params(a);
+    p.early = S::kOwn ? 0 : 1;
     p.mtiles = (int)((a.M + NT - 1) / NT);
     const int64_t tiles = (int64_t)p.mtiles * ((a.N + kI8Rows - 1) / kI8Rows);
-    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, p.ksteps, (int64_t)S::kCtas * dev.num_sms / tiles}));
+    p.split = stream_split(tiles, a.K, S::kCtas * dev.num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * p.split));
     cfg.blockDim = dim3(kIsThreads);
@@ -590,7 +678,7 @@ cudaError_t run_int8_stream(const Int8GemmArgs &a, cudaStream_t s, const DeviceI
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, int8_stream_kernel<NT>, tw, tx, p);
+    return cudaLaunchKernelEx(&cfg, int8_stream_kernel<NT, kTok>, tw, tx, p);
 }
 
 cudaError_t run_int8_tile(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
@@ -611,8 +699,19 @@ cudaError_t run_int8_tile(const Int8GemmArgs &a, cudaStream_t s, const DeviceInf
 
 }  // namespace
 
+// Whether the tokens are quantised in the product's kernel, not by a kernel of their own.  Every CTA reads the whole
+// rows for their maxima, so few elements only; what it multiplies has to fit beside three stages of weights.
+bool int8_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev)
+{
+    const int64_t tiles = (N + kI8Rows - 1) / kI8Rows, ksteps = (K + kI8K - 1) / kI8K;
+    const int split = stream_split(tiles, K, 2 * dev.num_sms);
+    return M <= 16 && M * K <= 16384 && (ksteps + split - 1) / split <= IsShape<16, kRawBf16>::kX && tiles * split <= 2 * dev.num_sms;
+}
+
 cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
+    if (a.raw)
+        return a.raw_fp32 ? run_int8_stream<16, kRawFp32>(a, s, dev) : run_int8_stream<16, kRawBf16>(a, s, dev);
     if (a.M <= 16)
         return run_int8_stream<16>(a, s, dev);
     if (a.M <= 32)

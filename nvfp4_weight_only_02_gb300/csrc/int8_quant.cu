@@ -1,15 +1,10 @@
-// int8_quant.cu -- rows of 8-bit integers with one scale a row.
+// int8_quant.cu -- rows of 8-bit integers with one scale a row (int8_codec.cuh has
+// the mathematics).
 //
-// Mathematics.  With a the largest magnitude of a row, s = a / 127 (FP32) and
-// q = the integer next to 127 x / a, ties to even.  127 x / a of bf16 or FP32
-// numbers is a tie, or at least 2^-33 of itself away from one, so the decision
-// in FP32 stands unless the quotient comes within 1e-4 of a tie; those few are
-// divided in 64 bits, where the division is exact at ties.  A row of zeros has
-// s = 0 and codes 0, a row with an infinity or a NaN s = NaN and codes 0.
-//
-// What bounds it: the bytes, read once: a CTA holds its row in registers (rows
-// above 32768 elements are read twice, the second time from L2).
+// What bounds it: the bytes, read once: a CTA holds its row in registers (what
+// lies beyond 20480 elements is read twice, the second time from L2).
 #include "common.cuh"
+#include "int8_codec.cuh"
 #include "internal.h"
 #include "mx_codec.cuh"
 
@@ -17,41 +12,33 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kIqThreads = 512, kIqHold = 8;   // groups of eight elements a thread holds
+constexpr int kIqMax = 512;   // threads of a CTA at most
 
-__device__ __forceinline__ float int8_round(float v, float inv, float amax)
-{
-    const float f = v * inv, r = rintf(f);
-    // also taken where the reciprocal leaves FP32's range
-    if (!(fabsf(f - r) < 0.4999f))
-        return (float)rint((double)v * 127.0 / (double)amax);
-    return r;
-}
-
-// kHalf: the integers as fp16 (exact), what the product's copies bring; else int8.
-template <typename T, bool kHalf>
-__global__ void __launch_bounds__(kIqThreads)
+// kHalf: the integers as fp16 (exact), what the product's copies bring; else int8.  kHold: groups of eight elements that
+// a thread holds.
+template <typename T, bool kHalf, int kHold>
+__global__ void __launch_bounds__(kIqMax)
     int8_quantize_kernel(const T *__restrict__ x, int64_t ld, int64_t cols, void *__restrict__ out, float *__restrict__ scale)
 {
-    __shared__ uint32_t s_max[kIqThreads / 32];
+    __shared__ uint32_t s_max[kIqMax / 32];
     const int64_t row = blockIdx.x, n8 = cols / 8;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, threads = blockDim.x;
     pdl_wait();
     pdl_launch_dependents();
     const T *src = x + row * ld;
-    Raw8<T> held[kIqHold];
+    Raw8<T> held[kHold];
     uint32_t m = 0;
 #pragma unroll
-    for (int u = 0; u < kIqHold; u++) {
-        const int64_t i = tid + (int64_t)u * kIqThreads;
+    for (int u = 0; u < kHold; u++) {
+        const int64_t i = tid + (int64_t)u * threads;
         held[u].zero();
         if (i < n8)
             held[u].load(src + i * 8);
     }
 #pragma unroll
-    for (int u = 0; u < kIqHold; u++)
+    for (int u = 0; u < kHold; u++)
         m = max(m, held[u].amax_bits());
-    for (int64_t i = tid + (int64_t)kIqHold * kIqThreads; i < n8; i += kIqThreads) {
+    for (int64_t i = tid + (int64_t)kHold * threads; i < n8; i += threads) {
         Raw8<T> r;
         r.load(src + i * 8);
         m = max(m, r.amax_bits());
@@ -60,27 +47,17 @@ __global__ void __launch_bounds__(kIqThreads)
     if ((tid & 31) == 0)
         s_max[tid >> 5] = m;
     __syncthreads();
-    m = s_max[tid & (kIqThreads / 32 - 1)];
+    m = (tid & 31) < threads / 32 ? s_max[tid & 31] : 0u;
     m = __reduce_max_sync(0xffffffffu, m);
-    const bool bad = m >= 0x7F800000u;
-    const float amax = __uint_as_float(m), inv = 127.0f / amax;
+    const Int8Row q(m);
     if (tid == 0)
-        scale[row] = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 127.0f);
+        scale[row] = q.scale();
     auto put = [&](const Raw8<T> &r, int64_t i) {
-        float v[8];
-        r.floats(v);
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            v[e] = bad || m == 0 ? 0.0f : int8_round(v[e], inv, amax);
         if (kHalf) {
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const __half2 p = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-                h[e] = *reinterpret_cast<const uint32_t *>(&p);
-            }
-            reinterpret_cast<uint4 *>(out)[row * n8 + i] = make_uint4(h[0], h[1], h[2], h[3]);
+            reinterpret_cast<uint4 *>(out)[row * n8 + i] = q.halves(r);
         } else {
+            float v[8];
+            q.integers(r, v);
             uint32_t w[2] = {0u, 0u};
 #pragma unroll
             for (int e = 0; e < 8; e++)
@@ -89,12 +66,12 @@ __global__ void __launch_bounds__(kIqThreads)
         }
     };
 #pragma unroll
-    for (int u = 0; u < kIqHold; u++) {
-        const int64_t i = tid + (int64_t)u * kIqThreads;
+    for (int u = 0; u < kHold; u++) {
+        const int64_t i = tid + (int64_t)u * threads;
         if (i < n8)
             put(held[u], i);
     }
-    for (int64_t i = tid + (int64_t)kIqHold * kIqThreads; i < n8; i += kIqThreads) {
+    for (int64_t i = tid + (int64_t)kHold * threads; i < n8; i += threads) {
         Raw8<T> r;
         r.load(src + i * 8);
         put(r, i);
@@ -119,21 +96,33 @@ __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restri
     out[2 * i + 1] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
+template <typename T, bool kHalf>
+cudaError_t run_rows(const Int8QuantArgs &a, cudaStream_t s)
+{
+    // four or five groups a thread: loads in flight, and few warps to meet for the maximum; one each in rows of up to 128
+    const int64_t n8 = a.cols / 8;
+    const dim3 grid((unsigned)a.rows);
+    if (n8 <= 128)
+        return launch_dependent(int8_quantize_kernel<T, kHalf, 1>, grid, (int)((n8 + 31) / 32 * 32), 0, s, (const T *)a.x,
+                                a.ld, a.cols, a.out, a.scale);
+    if (n8 <= 1024)
+        return launch_dependent(int8_quantize_kernel<T, kHalf, 4>, grid, n8 <= 512 ? 128 : 256, 0, s, (const T *)a.x, a.ld,
+                                a.cols, a.out, a.scale);
+    return launch_dependent(int8_quantize_kernel<T, kHalf, 5>, grid, kIqMax, 0, s, (const T *)a.x, a.ld, a.cols, a.out,
+                            a.scale);
+}
+
+template <typename T>
+cudaError_t run_quantize(const Int8QuantArgs &a, cudaStream_t s)
+{
+    return a.half ? run_rows<T, true>(a, s) : run_rows<T, false>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_int8_quantize(const Int8QuantArgs &a, cudaStream_t s)
 {
-    const dim3 grid((unsigned)a.rows);
-    if (a.x_fp32)
-        return a.half ? launch_dependent(int8_quantize_kernel<float, true>, grid, kIqThreads, 0, s, (const float *)a.x, a.ld,
-                                         a.cols, a.out, a.scale)
-                      : launch_dependent(int8_quantize_kernel<float, false>, grid, kIqThreads, 0, s, (const float *)a.x, a.ld,
-                                         a.cols, a.out, a.scale);
-    using B = __nv_bfloat16;
-    return a.half ? launch_dependent(int8_quantize_kernel<B, true>, grid, kIqThreads, 0, s, (const B *)a.x, a.ld, a.cols,
-                                     a.out, a.scale)
-                  : launch_dependent(int8_quantize_kernel<B, false>, grid, kIqThreads, 0, s, (const B *)a.x, a.ld, a.cols,
-                                     a.out, a.scale);
+    return a.x_fp32 ? run_quantize<float>(a, s) : run_quantize<__nv_bfloat16>(a, s);
 }
 
 cudaError_t launch_int8_widen(const int8_t *in, int64_t n, void *out, cudaStream_t s)

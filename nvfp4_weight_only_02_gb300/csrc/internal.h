@@ -285,7 +285,9 @@ cudaError_t launch_int8_widen(const int8_t *in, int64_t n, void *out, cudaStream
 // Their product (csrc/gemm_int8.cu), launched right behind the kernel that
 // wrote x on the same stream.
 struct Int8GemmArgs {
-    const void *x;           // M x K integers as fp16
+    const void *x;           // M x K integers as fp16, or raw tokens (leading dimension ldx)
+    bool raw, raw_fp32;
+    int64_t ldx;
     const float *x_scale;    // M
     const int8_t *w;         // N x K
     const float *w_scale;    // N
@@ -295,6 +297,8 @@ struct Int8GemmArgs {
     uint32_t *ctl;
 };
 cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev);
+// Whether it takes raw tokens of these sizes.
+bool int8_takes_tokens(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev);
 
 // Distillation loss and gradient (csrc/distill.cu).
 constexpr int kDistillMaxK = 1024;             // teacher entries per row

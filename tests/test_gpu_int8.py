@@ -88,3 +88,60 @@ def test_largest_sums(nv, M):
     tol = 127 * 128 * K * (K / 16 + 8) * 2.0 ** -23
     assert (y[:, 0] - 127 * 127 * K).abs().max() <= tol and (y[:, 1] + 127 * 128 * K).abs().max() <= tol
     assert (y[:, 2] == 0).all() and (y[:, 3:] == y[:, :1]).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 500, 3584), (1, 18944, 3584), (4, 300, 4096), (16, 300, 1024), (3, 200, 18944)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_ties(nv, M, N, K, dtype):
+    """A largest magnitude of 254 / 64 makes ties of all odd multiples of 1 / 64: also where the product's kernel
+    quantises the tokens itself (few of them), whose warps part at ties."""
+    g = _gen(M + K)
+    x = torch.randint(-200, 201, (M, K), device="cuda", generator=g).float() / 64
+    x[:, 5] = 254 / 64
+    x[:, ::3] = 0.3
+    w = nv.int8_quantize(torch.randn(N, K, device="cuda", generator=g))
+    x = x.to(dtype)
+    a = nv.int8_quantize(x)
+    assert torch.equal(a.codes.double(), _quant64(x)[0])
+    for _ in range(3):
+        assert torch.equal(nv.int8_linear(x, w), nv.int8_gemm(a, w))
+
+
+def test_layers_behind_one_another(nv):
+    """Launches overlap: each call's tokens are what the call before has just written."""
+    g = _gen(7)
+    for M, K in ((1, 1024), (8, 2048), (40, 512), (300, 512)):
+        ws_ = [nv.int8_quantize(torch.randn(K, K, device="cuda", generator=g) / K ** 0.5) for _ in range(3)]
+        x = torch.randn(M, K, device="cuda", generator=g)
+        space = nv.new_workspace(nv.nvfp4_int8_linear_workspace_bytes(M, K, K))
+        want, t = [], x
+        for i in range(12):
+            t = nv.int8_linear(t, ws_[i % 3])
+            torch.cuda.synchronize()
+            want.append(t)
+        buf = [x.clone(), torch.empty_like(x)]
+        torch.cuda.synchronize()
+        for i in range(12):
+            a, b = buf[i % 2], buf[1 - i % 2]
+            nv._call("nvfp4_int8_linear", a.data_ptr(), nv.OUT_FP32, K, M, K, K, ws_[i % 3].codes.data_ptr(),
+                     ws_[i % 3].scales.data_ptr(), b.data_ptr(), nv.OUT_FP32, space.data_ptr(), space.numel(),
+                     nv._raw_stream())
+        assert torch.equal(buf[0], want[11]) and torch.equal(buf[1], want[10])
+        assert nv.nvfp4_get_device_status(space) == nv.OK
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 18944, 3584), (10, 3584, 18944), (40, 18944, 3584), (100, 18944, 3584)])
+def test_weights_that_come_from_memory(nv, M, N, K):
+    """Weights beyond L2 in turn: stages land late and out of order."""
+    g = _gen(M)
+    w = [nv.int8_quantize(torch.randn(N, K, device="cuda", generator=g)) for _ in range(4)]
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    a = nv.int8_quantize(x)
+    codes = a.codes.double()
+    want = [(codes @ q.codes.double().t()) * a.scales.double()[:, None] * q.scales.double() for q in w]
+    ws = nv.new_workspace(nv.nvfp4_int8_linear_workspace_bytes(M, N, K))
+    for _ in range(5):
+        ys = [nv.int8_linear(x, q, workspace=ws) for q in w]
+        for y, r in zip(ys, want):
+            # sums are exact; two products are rounded
+            assert ((y.double() - r).abs() <= 3.1 * 2.0 ** -24 * r.abs()).all()
