@@ -20,6 +20,7 @@
 #include "int8_codec.cuh"
 #include "internal.h"
 #include "mx_codec.cuh"
+#include "tile_store.cuh"
 #include "w4a4_pair.cuh"
 
 namespace nvfp4 {
@@ -395,16 +396,18 @@ constexpr int kItThreads = 32 * (kI8Conv + kItEpi + 2);   // converting, epilogu
 constexpr int kItStages = 4;
 static_assert(kItStages % kI8Groups == 0, "see the converting warps' waits");
 constexpr int kItXBytes = kItTokens / 2 * kI8K * 2, kItStageBytes = kI8WBytes + kItXBytes;
-constexpr size_t kItSmem = 512 + (size_t)kItStages * kItStageBytes;
+constexpr size_t kItSmem = 512 + (size_t)kItStages * kItStageBytes + kStageOut;
 constexpr int kItGroup = 8;   // raster: token tiles per group
 
+template <bool kF32>
 __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
     int8_tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Int8Params p)
 {
     constexpr int kStages = kItStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sW = smem, *sX = sW + kStages * kI8WBytes;
-    uint64_t *full_w = reinterpret_cast<uint64_t *>(sX + kStages * kItXBytes), *full_x = full_w + kStages;
+    uint8_t *sOut = sX + kStages * kItXBytes;
+    uint64_t *full_w = reinterpret_cast<uint64_t *>(sOut + kStageOut), *full_x = full_w + kStages;
     uint64_t *a_full = full_x + kStages, *done = a_full + kStages, *acc_full = done + kStages, *acc_empty = acc_full + 1;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 1);
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
@@ -542,52 +545,55 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
                 mbar_arrive_cluster(cluster_addr(&a_full[st], 0));   // hands over TMEM that is written (wait::st)
         }
     } else {
-        // ---------------- epilogue: a warp has 32 weight rows, one a lane
+        // ---------------- epilogue: a warp has 32 weight rows
         const int quad = warp & 3;
         const uint32_t bar = cluster_addr(acc_empty, 0);
         uint32_t lt = 0;
-        for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
+        bool dead = false;   // after a wait that gave up: the four warps that store together stay together
+        for (int t = cid; t < ntot; t += ncl, lt++) {
             int mt, nt;
             tile_at(t, mt, nt);
-            const int n = nt * 256 + crank * 128 + quad * 32 + lane, rows = min(kItTokens, p.M - mt * kItTokens);
-            const float sw = n < p.N ? p.w_scale[n] : 0.0f;
-            if (!mbar_wait_warp(acc_full, lt & 1)) {
+            const int n0 = nt * 256 + crank * 128, rows = min(kItTokens, p.M - mt * kItTokens);
+            // scales of the outputs that the thread's registers hold: its lane's, or in the fragments' layout four
+            float sw[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int n = n0 + quad * 32 + (kF32 ? lane : 8 * i + lane / 4);
+                sw[i] = n < p.N ? p.w_scale[n] : 0.0f;
+            }
+            if (!dead && (aborted() || !mbar_wait_warp(acc_full, lt & 1))) {
                 fail();
-                break;
+                dead = true;
             }
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
             uint32_t buf[2][32];
-            tmem_ld32_start(acc, buf[0]);
+            tile_ld_start<kF32>(acc, buf[0]);
 #pragma unroll
             for (int c = 0; c < kItTokens / 32; c++) {
                 uint32_t(&v)[32] = buf[c & 1];
                 __syncwarp();   // the stores before may have parted the warp
                 tmem_ld32_finish(v);
                 if (c + 1 < kItTokens / 32) {
-                    tmem_ld32_start(acc + (c + 1) * 32, buf[(c + 1) & 1]);
+                    tile_ld_start<kF32>(acc + (c + 1) * 32, buf[(c + 1) & 1]);
                 } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_cluster(bar);
                 }
-                const int left = rows - c * 32, m = mt * kItTokens + c * 32;
-                if (left <= 0)
+                const int left = min(32, rows - c * 32), m = mt * kItTokens + c * 32;
+                if (left <= 0 || n0 >= p.N)
                     continue;
                 const float sx = lane < left ? p.x_scale[m + lane] : 0.0f;
-                const size_t at = (size_t)m * p.N + n;
 #pragma unroll
                 for (int i = 0; i < 32; i++) {
-                    const float s = __shfl_sync(0xffffffffu, sx, i);
-                    const float y = __fmul_rn(__fmul_rn(__uint_as_float(v[i]), s), sw);
-                    if (i < left && n < p.N) {
-                        if (p.y_fp32)
-                            reinterpret_cast<float *>(p.y)[at + (size_t)i * p.N] = y;
-                        else
-                            reinterpret_cast<__nv_bfloat16 *>(p.y)[at + (size_t)i * p.N] = __float2bfloat16_rn(y);
-                    }
+                    // register i: row i, or row 8 (i / 4 % 4) + 2 (lane % 4) + i % 2 of output 16 (i / 16) + 8 (i / 2 % 2)
+                    const float s = __shfl_sync(0xffffffffu, sx, kF32 ? i : 8 * (i / 4 % 4) + 2 * (lane & 3) + i % 2);
+                    v[i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[i]), s),
+                                                     sw[kF32 ? 0 : 2 * (i / 16) + i / 2 % 2]));
                 }
+                store_rows<kF32>(v, sOut, 1, p.y, m, left, p.N, n0, quad, lane, !dead);
             }
         }
     }
@@ -681,19 +687,20 @@ cudaError_t run_int8_stream(const Int8GemmArgs &a, cudaStream_t s, const DeviceI
     return cudaLaunchKernelEx(&cfg, int8_stream_kernel<NT, kTok>, tw, tx, p);
 }
 
+template <bool kF32>
 cudaError_t run_int8_tile(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
     CUtensorMap tw, tx;
     cudaError_t e = maps(&tw, &tx, a, kItTokens / 2);
     if (e == cudaSuccess)
-        e = allow_smem<int8_tile_kernel>(kItSmem, dev);
+        e = allow_smem<int8_tile_kernel<kF32>>(kItSmem, dev);
     if (e != cudaSuccess)
         return e;
     Int8Params p = params(a);
     p.mtiles = (int)((a.M + kItTokens - 1) / kItTokens);
     p.ntiles = (int)((a.N + 255) / 256);
     const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
-    return launch_dependent(int8_tile_kernel, dim3(2 * (unsigned)std::min<int64_t>(tiles, dev.num_sms / 2)), kItThreads,
+    return launch_dependent(int8_tile_kernel<kF32>, dim3(2 * (unsigned)std::min<int64_t>(tiles, dev.num_sms / 2)), kItThreads,
                             kItSmem, s, tw, tx, p);
 }
 
@@ -721,7 +728,7 @@ cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const Device
     const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
     if (a.M <= 128 || (big * 5 <= dev.num_sms && a.M <= 512))
         return run_int8_stream<128>(a, s, dev);
-    return run_int8_tile(a, s, dev);
+    return a.y_fp32 ? run_int8_tile<true>(a, s, dev) : run_int8_tile<false>(a, s, dev);
 }
 
 }  // namespace nvfp4

@@ -10,18 +10,21 @@
 // many columns as it has rows: experts with few rows waste nothing.  In the
 // quantised operands every expert's rows begin on a multiple of 128, where the
 // tiled scales and the copies can start; in Y the rows are compact, so stores
-// are by element and never touch a row of another expert or one behind the last.
+// are by row and never touch a row of another expert or one behind the last.
 #include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
 #include "moe_plan.h"
+#include "tile_store.cuh"
 #include "w4a4_pair.cuh"
 #include "w4a4_shape.h"
 
 namespace nvfp4 {
 
 namespace {
+
+static_assert(2 * kStageOut <= kTlEpiWarps * kTlStoreBytes, "the tiles' staging");
 
 struct MoeParams {
     const int32_t *header;
@@ -42,7 +45,7 @@ struct MoeParams {
 // ---------------------------------------------------------------- CTA pairs
 // Items (tile of rows, 256 weight rows), dealt out to the pairs in turn, the
 // weight tile fastest.
-template <int TR>
+template <int TR, bool kF32>
 __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
     moe_tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_sx,
@@ -51,8 +54,8 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
     using S = TlShape<false, TR>;
     constexpr int kStages = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sA = smem, *sB = sA + kStages * S::kABytes;
-    uint8_t *sSa = sB + kStages * S::kBBytes, *sSb = sSa + kStages * S::kSaBytes;
+    uint8_t *sA = smem, *sB = sA + kStages * S::kABytes, *sOut = sB + kStages * S::kBBytes;
+    uint8_t *sSa = sOut + 2 * kStageOut, *sSb = sSa + kStages * S::kSaBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(sSb + kStages * S::kSbBytes);
     uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 2;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 2);
@@ -188,27 +191,29 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
         constexpr int kChunks = TR / 32, kSharedChunks = S::kShared / 32;
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t bar0 = cluster_addr(&acc_empty[0], 0), bar1 = cluster_addr(&acc_empty[1], 0);
+        uint8_t *stage = sOut + half * kStageOut;
         uint32_t lt = 0;
-        for (int t = cid; t < ntot && !aborted(); t += ncl, lt++) {
+        bool dead = false;   // after a wait that gave up: the four warps that store together stay together
+        for (int t = cid; t < ntot; t += ncl, lt++) {
             const int4 tile = p.tiles[t / p.wtiles];
-            const int n = t % p.wtiles * 256 + crank * 128 + quad * 32 + lane;
-            if (!mbar_wait_warp(&acc_full[lt & 1], (lt >> 1) & 1)) {
+            const int n0 = t % p.wtiles * 256 + crank * 128;
+            if (!dead && (aborted() || !mbar_wait_warp(&acc_full[lt & 1], (lt >> 1) & 1))) {
                 fail();
-                break;
+                dead = true;
             }
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (lt & 1 ? S::kAcc1 : 0);
             // accumulator 0 ends with the shared columns, accumulator 1 begins with them
             const int first = lt & 1 ? 0 : kChunks - kSharedChunks;
             uint32_t buf[2][32];
-            tmem_ld32_start(acc + (first + half) % kChunks * 32, buf[0]);
+            tile_ld_start<kF32>(acc + (first + half) % kChunks * 32, buf[0]);
 #pragma unroll
             for (int i = 0; i < kChunks / 2; i++) {
                 uint32_t(&v)[32] = buf[i & 1];
                 __syncwarp();   // the stores before may have parted the warp
                 tmem_ld32_finish(v);
                 if (i + 1 < kChunks / 2)
-                    tmem_ld32_start(acc + (first + half + 2 * (i + 1)) % kChunks * 32, buf[(i + 1) & 1]);
+                    tile_ld_start<kF32>(acc + (first + half + 2 * (i + 1)) % kChunks * 32, buf[(i + 1) & 1]);
                 if (S::kShared ? half + 2 * i < kSharedChunks && half + 2 * i + 2 >= kSharedChunks
                                : i + 1 == kChunks / 2) {
                     // this warp's part of the shared columns (of all) is in registers
@@ -217,20 +222,9 @@ __global__ void __launch_bounds__(kTlThreads, 1) __cluster_dims__(2, 1, 1)
                     if (lane == 0)
                         mbar_arrive_cluster(S::kShared || !(lt & 1) ? bar0 : bar1);
                 }
-                const int c0 = (first + half + 2 * i) % kChunks * 32, left = tile.w - c0;
-                if (left <= 0 || n >= p.N)
-                    continue;
-                const size_t at = (size_t)(tile.z + c0) * p.N + n;
-#pragma unroll
-                for (int c = 0; c < 32; c++) {
-                    if (c < left) {
-                        if (p.y_fp32)
-                            reinterpret_cast<uint32_t *>(p.y)[at + (size_t)c * p.N] = v[c];
-                        else
-                            reinterpret_cast<__nv_bfloat16 *>(p.y)[at + (size_t)c * p.N] =
-                                __float2bfloat16_rn(__uint_as_float(v[c]));
-                    }
-                }
+                const int c0 = (first + half + 2 * i) % kChunks * 32, left = min(32, tile.w - c0);
+                if (left > 0 && n0 < p.N)
+                    store_rows<kF32>(v, stage, 1 + half, p.y, tile.z + c0, left, p.N, n0, quad, lane, !dead);
             }
         }
     }
@@ -783,7 +777,7 @@ MoeParams params(const MoeGemmArgs &a)
     return p;
 }
 
-template <int TR>
+template <int TR, bool kF32>
 cudaError_t run_moe_tile(const MoeGemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
     using S = TlShape<false, TR>;
@@ -800,12 +794,12 @@ cudaError_t run_moe_tile(const MoeGemmArgs &a, cudaStream_t s, const DeviceInfo 
         e = encode_scale_map(&tsx, a.x_scales, (uint64_t)p.ktiles, (uint64_t)a.padded_rows / 128, S::kTiles,
                              S::kBRowTiles);
     if (e == cudaSuccess)
-        e = allow_smem<moe_tile_kernel<TR>>(S::kSmem, dev);
+        e = allow_smem<moe_tile_kernel<TR, kF32>>(S::kSmem, dev);
     if (e != cudaSuccess)
         return e;
     p.wtiles = (int)((a.N + 255) / 256);
     const int64_t most = a.max_tiles * p.wtiles;
-    return launch_dependent(moe_tile_kernel<TR>, dim3(2 * (unsigned)std::min<int64_t>(most, dev.num_sms / 2)),
+    return launch_dependent(moe_tile_kernel<TR, kF32>, dim3(2 * (unsigned)std::min<int64_t>(most, dev.num_sms / 2)),
                             kTlThreads, S::kSmem, s, tw, tx, tsw, tsx, p);
 }
 
@@ -857,9 +851,9 @@ cudaError_t launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t s, const DeviceIn
     case 64:
         return run_moe_stream<64>(a, s, dev);
     case 128:
-        return run_moe_tile<128>(a, s, dev);
+        return a.y_fp32 ? run_moe_tile<128, true>(a, s, dev) : run_moe_tile<128, false>(a, s, dev);
     default:
-        return run_moe_tile<256>(a, s, dev);
+        return a.y_fp32 ? run_moe_tile<256, true>(a, s, dev) : run_moe_tile<256, false>(a, s, dev);
     }
 }
 

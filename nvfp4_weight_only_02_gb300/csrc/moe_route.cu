@@ -518,13 +518,20 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
 }
 
 // ---------------------------------------------------------------- combine
-// kVec elements of a row at a time: 16 bytes of the wider type's partner or,
-// where rows do not start on 16-byte boundaries, single elements.
+// kVec elements of a row at a time: 16 bytes of the widest type involved (a
+// thread with two of them would ask for each 32-byte sector twice), or single
+// elements where rows do not start on 16-byte boundaries.
 template <typename T, int kVec>
 __device__ __forceinline__ void load_vec(const T *src, float (&v)[kVec])
 {
     if constexpr (kVec == 1) {
         v[0] = (float)src[0];
+    } else if constexpr (sizeof(T) == 2 && kVec == 4) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(src);
+        v[0] = __uint_as_float(a.x << 16);
+        v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(a.y << 16);
+        v[3] = __uint_as_float(a.y & 0xFFFF0000u);
     } else if constexpr (sizeof(T) == 2) {
         static_assert(kVec == 8, "16 bytes");
         const uint4 a = ld_once_u4(src);
@@ -555,13 +562,16 @@ __device__ __forceinline__ void store_vec(T *dst, const float (&v)[kVec])
         else
             dst[0] = v[0];
     } else if constexpr (sizeof(T) == 2) {
-        uint32_t w[4];
+        uint32_t w[kVec / 2];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < kVec / 2; i++) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (kVec == 8)
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; i += 4)
@@ -569,7 +579,7 @@ __device__ __forceinline__ void store_vec(T *dst, const float (&v)[kVec])
     }
 }
 
-// The same, unconverted: 16 bytes (FP32: 32) a thread and row on their way.
+// The same, unconverted: what is on its way of a row in a thread.
 template <typename T, int kVec>
 struct Vec;
 template <>
@@ -587,15 +597,21 @@ struct Vec<__nv_bfloat16, 8> {
     }
 };
 template <>
-struct Vec<float, 8> {
-    float w[8];
-    __device__ __forceinline__ void zero()
+struct Vec<__nv_bfloat16, 4> {
+    uint2 w;
+    __device__ __forceinline__ void zero() { w = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ float get(int e) const
     {
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            w[e] = 0.0f;
+        const uint32_t u = e & 2 ? w.y : w.x;
+        return __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
     }
-    __device__ __forceinline__ void load(const float *p) { load_vec<float, 8>(p, w); }
+};
+template <>
+struct Vec<float, 4> {
+    float w[4];
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0.0f; }
+    __device__ __forceinline__ void load(const float *p) { load_vec<float, 4>(p, w); }
     __device__ __forceinline__ float get(int e) const { return w[e]; }
 };
 template <typename T>
@@ -740,20 +756,22 @@ int combine_threads(int64_t N, int vec)
 template <typename TY, typename TO>
 cudaError_t run_combine(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
 {
-    const int vec = a.N % 8 == 0 ? 8 : 1, threads = combine_threads(a.N, vec);
+    constexpr int kVec = sizeof(TY) == 4 || sizeof(TO) == 4 ? 4 : 8;
+    const int vec = a.N % kVec == 0 ? kVec : 1, threads = combine_threads(a.N, vec);
     // few tokens: a row's vectors over several CTAs (16 tokens of 4096: 2.6 us, 6.1 in one); many: one for all of them
     // (8192 tokens: 100 us, 119 in two)
     const dim3 grid((unsigned)a.T, a.T < 512 ? (unsigned)((a.N + vec * threads - 1) / (vec * threads)) : 1u);
-    return vec == 8 ? launch_dependent(combine_kernel<TY, TO, 8>, grid, threads, 0, s, p)
-                    : launch_dependent(combine_kernel<TY, TO, 1>, grid, threads, 0, s, p);
+    return vec > 1 ? launch_dependent(combine_kernel<TY, TO, kVec>, grid, threads, 0, s, p)
+                   : launch_dependent(combine_kernel<TY, TO, 1>, grid, threads, 0, s, p);
 }
 
 template <typename T>
 cudaError_t run_combine_grad(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
 {
+    constexpr int kVec = 16 / sizeof(T);
     const dim3 grid((unsigned)a.T);
-    return a.N % 8 == 0 ? launch_dependent(combine_grad_kernel<T, 8>, grid, combine_threads(a.N, 8), 0, s, p)
-                        : launch_dependent(combine_grad_kernel<T, 1>, grid, combine_threads(a.N, 1), 0, s, p);
+    return a.N % kVec == 0 ? launch_dependent(combine_grad_kernel<T, kVec>, grid, combine_threads(a.N, kVec), 0, s, p)
+                           : launch_dependent(combine_grad_kernel<T, 1>, grid, combine_threads(a.N, 1), 0, s, p);
 }
 
 CombineParams combine_params(const MoeCombineArgs &a)
