@@ -80,83 +80,154 @@ __device__ __forceinline__ uint32_t key_of(float v)
     return v > -INFINITY ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : 0u;
 }
 
-__device__ __forceinline__ void order_pair(uint64_t &a, uint64_t &b)
+__device__ __forceinline__ void order_pair(uint32_t &a, uint32_t &b)
 {
-    const uint64_t hi = a > b ? a : b, lo = a > b ? b : a;
+    const uint32_t hi = max(a, b), lo = min(a, b);
     a = hi;
     b = lo;
 }
 
-// The best expert left, by a warp: its index in every lane, or none.  Up to
-// eight experts a lane these are sorted first (key, and the complement of the
-// index below it, so that equal keys go by index), and a round only looks at
-// the lanes' heads: 20 instructions instead of 50 for eight (16384 tokens, 256
-// experts, 8 taken: the kernel executes 40 % fewer).
+// Descending, by exchanges of two instructions each.
 template <int kPer>
-struct Best {
-    static constexpr bool kSorted = kPer <= 8;
-    uint64_t v[kPer];
-    __device__ __forceinline__ void set(int i, int lane, uint32_t key)
-    {
-        v[i] = (uint64_t)key << 32 | (0xFFFFFFFFu - (uint32_t)(lane + 32 * i));
+__device__ __forceinline__ void sort_keys(uint32_t (&v)[kPer])
+{
+    if constexpr (kPer == 8) {
+        // odd-even merges: 19 exchanges
+        order_pair(v[0], v[1]), order_pair(v[2], v[3]), order_pair(v[4], v[5]), order_pair(v[6], v[7]);
+        order_pair(v[0], v[2]), order_pair(v[1], v[3]), order_pair(v[4], v[6]), order_pair(v[5], v[7]);
+        order_pair(v[1], v[2]), order_pair(v[5], v[6]);
+        order_pair(v[0], v[4]), order_pair(v[1], v[5]), order_pair(v[2], v[6]), order_pair(v[3], v[7]);
+        order_pair(v[2], v[4]), order_pair(v[3], v[5]);
+        order_pair(v[1], v[2]), order_pair(v[3], v[4]), order_pair(v[5], v[6]);
+    } else if constexpr (kPer == 4) {
+        order_pair(v[0], v[1]), order_pair(v[2], v[3]);
+        order_pair(v[0], v[2]), order_pair(v[1], v[3]);
+        order_pair(v[1], v[2]);
+    } else {
+        static_assert(kPer == 2, "2, 4 or 8 keys");
+        order_pair(v[0], v[1]);
     }
-    __device__ __forceinline__ void sort()
-    {
-        if constexpr (kPer == 8) {
-            // odd-even merges: 19 exchanges
-            order_pair(v[0], v[1]), order_pair(v[2], v[3]), order_pair(v[4], v[5]), order_pair(v[6], v[7]);
-            order_pair(v[0], v[2]), order_pair(v[1], v[3]), order_pair(v[4], v[6]), order_pair(v[5], v[7]);
-            order_pair(v[1], v[2]), order_pair(v[5], v[6]);
-            order_pair(v[0], v[4]), order_pair(v[1], v[5]), order_pair(v[2], v[6]), order_pair(v[3], v[7]);
-            order_pair(v[2], v[4]), order_pair(v[3], v[5]);
-            order_pair(v[1], v[2]), order_pair(v[3], v[4]), order_pair(v[5], v[6]);
-        } else if constexpr (kPer == 4) {
-            order_pair(v[0], v[1]), order_pair(v[2], v[3]);
-            order_pair(v[0], v[2]), order_pair(v[1], v[3]);
-            order_pair(v[1], v[2]);
-        } else if constexpr (kPer == 2) {
-            order_pair(v[0], v[1]);
-        }
-    }
-    __device__ __forceinline__ int take()
-    {
-        uint64_t head = v[0];
-        if constexpr (!kSorted) {
-#pragma unroll
-            for (int i = 1; i < kPer; i++)
-                head = v[i] > head ? v[i] : head;
-        }
-        const uint32_t top = __reduce_max_sync(kAll, (uint32_t)(head >> 32));
-        if (top == 0)
-            return -1;
-        const bool mine = (uint32_t)(head >> 32) == top;
-        const uint32_t low = __reduce_max_sync(kAll, mine ? (uint32_t)head : 0u);
-        const uint64_t gone = (uint64_t)top << 32 | low;
-        if constexpr (kSorted) {
-            const bool won = head == gone;
-#pragma unroll
-            for (int i = 0; i + 1 < kPer; i++)
-                v[i] = won ? v[i + 1] : v[i];
-            v[kPer - 1] = won ? 0u : v[kPer - 1];
-        } else {
+}
+
+// The k experts of the largest keys, in order; equal keys by index.  A lane has
+// kPer experts behind one another, so of equal keys the lowest lane's is first.
+// Returns lane j's choice j, -1 where there is none.
+//
+// Up to eight experts a lane and eight choices: the lane's keys are sorted, a
+// round finds the largest head by a reduction over the warp and its lane by a
+// vote, and which expert a key was is looked up at the end, in as many turns as
+// a lane has choices (two or three).  The integer pipe bounds it (63 % of its
+// cycles): 16384 tokens with 8 of 256 experts take 19 us, 24 with rounds that look
+// at all keys, as more experts or choices take.
+template <int kPer>
+__device__ __forceinline__ int choose(const uint32_t (&key)[kPer], int k, int lane, int *s_choice)
+{
+    int mine = -1;
+    if constexpr (kPer <= 8) {
+        if (k <= 8) {
+            uint32_t v[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; i++)
-                v[i] = v[i] == gone ? 0u : v[i];
+                v[i] = key[i];
+            sort_keys<kPer>(v);
+            uint32_t head = v[0], taken = 0;   // taken: the lane's choices, four bits each
+            int n = 0, found = 0;
+            for (int j = 0; j < k; j++) {
+                const uint32_t top = __reduce_max_sync(kAll, head);
+                if (top == 0)
+                    break;
+                found++;
+                if (lane == __ffs(__ballot_sync(kAll, head == top)) - 1) {
+                    taken |= (uint32_t)j << (4 * n);
+                    n++;
+                    head = 0;
+#pragma unroll
+                    for (int i = 1; i < kPer; i++)
+                        head = n == i ? v[i] : head;
+                }
+            }
+            uint32_t used = 0;
+#pragma unroll
+            for (int m = 0; m < kPer; m++) {
+                if (!__any_sync(kAll, n > m))
+                    break;
+                if (n > m) {
+                    int at = 0;
+#pragma unroll
+                    for (int i = kPer - 1; i >= 0; i--)
+                        at = key[i] == v[m] && !(used >> i & 1) ? i : at;
+                    used |= 1u << at;
+                    s_choice[taken >> (4 * m) & 15] = lane * kPer + at;
+                }
+            }
+            __syncwarp();
+            mine = lane < found ? s_choice[lane] : -1;
+            __syncwarp();
+            return mine;
         }
-        return (int)(0xFFFFFFFFu - low);
     }
-};
+    uint32_t left[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; i++)
+        left[i] = key[i];
+    for (int j = 0; j < k; j++) {
+        uint32_t head = left[0];
+#pragma unroll
+        for (int i = 1; i < kPer; i++)
+            head = max(head, left[i]);
+        const uint32_t top = __reduce_max_sync(kAll, head);
+        if (top == 0)
+            break;
+        const int from = __ffs(__ballot_sync(kAll, head == top)) - 1;
+        int at = 0;
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; i--)
+            at = left[i] == top ? i : at;
+        at = __shfl_sync(kAll, at, from);
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            left[i] = lane == from && i == at ? 0u : left[i];
+        mine = lane == j ? from * kPer + at : mine;
+    }
+    return mine;
+}
 
-// One token by one warp.  kPer values a lane: expert lane + 32 i.
+// kPer logits behind one another from element `at` (of row t), -inf behind the last expert.
 template <int kPer, bool kF32>
-__device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, int lane)
+__device__ __forceinline__ void load_logits(const RouteParams &p, int64_t t, int e0, float (&z)[kPer])
+{
+    constexpr int kBytes = kPer * (kF32 ? 4 : 2), kStep = kBytes < 16 ? kBytes : 16;
+    const char *src = reinterpret_cast<const char *>(p.z) + (t * p.ldz + e0) * (kF32 ? 4 : 2);
+    if (e0 + kPer <= p.E && p.ldz * (kF32 ? 4 : 2) % kStep == 0) {
+        uint32_t w[kBytes / 4];
+#pragma unroll
+        for (int i = 0; i < kBytes / kStep; i++) {
+            if constexpr (kStep == 16) {
+                const uint4 a = ld_once_u4(src + 16 * i);
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            } else if constexpr (kStep == 8) {
+                const uint2 a = *reinterpret_cast<const uint2 *>(src);
+                w[0] = a.x, w[1] = a.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t *>(src);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            z[i] = kF32 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            z[i] = e0 + i < p.E ? load_z(p.z, kF32, t * p.ldz + e0 + i) : -INFINITY;
+    }
+}
+
+// One token by one warp, kPer experts a lane.
+template <int kPer, bool kF32>
+__device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, int lane, int *s_choice)
 {
     float z[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
-        const int e = lane + 32 * i;
-        z[i] = e < p.E ? load_z(p.z, kF32, t * p.ldz + e) : -INFINITY;
-    }
+    load_logits<kPer, kF32>(p, t, lane * kPer, z);
     bool nan = false;   // the softmax of the row has no value
 #pragma unroll
     for (int i = 0; i < kPer; i++)
@@ -174,29 +245,22 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, int
             denom += z[i] > -INFINITY ? expf(z[i] - zmax) : 0.0f;
         denom = warp_sum(denom);
     }
-    Best<kPer> best;
+    uint32_t key[kPer];
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-            const int e = lane + 32 * i;
+            const int e = lane * kPer + i;
             float v = z[i];
             if (e < p.E && v > -INFINITY)
                 v = (p.sigmoid ? sigmoid(v) : expf(v - zmax) / denom) + p.bias[e];
-            best.set(i, lane, key_of(v));
+            key[i] = key_of(v);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kPer; i++)
-            best.set(i, lane, key_of(z[i]));
+            key[i] = key_of(z[i]);
     }
-    best.sort();
-    int mine = -1;   // lane j: expert of slot j
-    for (int j = 0; j < p.k; j++) {
-        const int e = best.take();
-        if (e < 0)
-            break;
-        mine = lane == j ? e : mine;
-    }
+    const int mine = choose<kPer>(key, p.k, lane, s_choice);
     const float zj = mine >= 0 ? load_z(p.z, kF32, t * p.ldz + mine) : -INFINITY;
     float w = 0.0f;
     if (p.renorm) {
@@ -214,25 +278,25 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, int
     }
 }
 
-// The tokens t0, t0 + kRtWarps, ... below t1.
+// The tokens t0, t0 + step, ... below t1.
 template <bool kF32>
-__device__ __forceinline__ void route_tokens(const RouteParams &p, int64_t t0, int64_t t1, int lane)
+__device__ __forceinline__ void route_tokens(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, int *s_choice)
 {
     if (p.E <= 64)
-        for (int64_t t = t0; t < t1; t += kRtWarps)
-            route_token<2, kF32>(p, t, lane);
+        for (int64_t t = t0; t < t1; t += step)
+            route_token<2, kF32>(p, t, lane, s_choice);
     else if (p.E <= 128)
-        for (int64_t t = t0; t < t1; t += kRtWarps)
-            route_token<4, kF32>(p, t, lane);
+        for (int64_t t = t0; t < t1; t += step)
+            route_token<4, kF32>(p, t, lane, s_choice);
     else if (p.E <= 256)
-        for (int64_t t = t0; t < t1; t += kRtWarps)
-            route_token<8, kF32>(p, t, lane);
+        for (int64_t t = t0; t < t1; t += step)
+            route_token<8, kF32>(p, t, lane, s_choice);
     else if (p.E <= 512)
-        for (int64_t t = t0; t < t1; t += kRtWarps)
-            route_token<16, kF32>(p, t, lane);
+        for (int64_t t = t0; t < t1; t += step)
+            route_token<16, kF32>(p, t, lane, s_choice);
     else
-        for (int64_t t = t0; t < t1; t += kRtWarps)
-            route_token<32, kF32>(p, t, lane);
+        for (int64_t t = t0; t < t1; t += step)
+            route_token<32, kF32>(p, t, lane, s_choice);
 }
 
 // Calls f(slot, expert, rank) for the slots of this warp's run in groups of
@@ -271,7 +335,8 @@ __device__ __forceinline__ void block_scan3(int (&v)[3], int (*s_warp)[3], int w
             s_warp[warp][c] = v[c];
     __syncthreads();
     if (warp == 0) {
-        int w[3] = {s_warp[lane][0], s_warp[lane][1], s_warp[lane][2]};
+        const bool is = lane < (int)(blockDim.x >> 5);
+        int w[3] = {is ? s_warp[lane][0] : 0, is ? s_warp[lane][1] : 0, is ? s_warp[lane][2] : 0};
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
 #pragma unroll
@@ -292,14 +357,18 @@ __device__ __forceinline__ void block_scan3(int (&v)[3], int (*s_warp)[3], int w
 // kFirst: experts (where there are logits), each slot's rank among the CTA's
 // slots of its expert, and the CTA's counts.  kSecond: offsets, lists and the
 // slots' places.  Both: one CTA does it all.
-template <bool kFirst, bool kSecond>
+// kTopk: there are logits.  As many warps as the experts and the slots of a CTA
+// need: fewer meet faster at the barriers (the plan of one token with 8 of 128
+// experts: 3.9 us, 5.1 with 32 warps).
+template <bool kTopk, bool kFirst, bool kSecond>
 __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
 {
     extern __shared__ uint16_t s_hist[];            // [warps][E]
     __shared__ int s_base[kMoeMaxExperts];          // row of the expert's first slot of this CTA
     __shared__ int s_off[kMoeMaxExperts + 1], s_fb[kMoeMaxExperts + 1], s_ft[kMoeMaxExperts + 1];
     __shared__ int s_warp[kRtWarps][3];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ int s_choice[kTopk ? kRtWarps : 1][8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x, warps = threads >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
     const int64_t c0 = t0 * p.k, c1 = max(c0, t1 * p.k);    // the CTA's slots
     int32_t *counts = p.plan + p.counts, *position = p.plan + p.position;
@@ -307,22 +376,22 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
     pdl_wait();
     int total = 0, before = 0;
     if (kFirst) {
-        if (p.z) {
+        if constexpr (kTopk) {
             if (p.z_fp32)
-                route_tokens<true>(p, t0 + warp, t1, lane);
+                route_tokens<true>(p, t0 + warp, t1, warps, lane, s_choice[warp]);
             else
-                route_tokens<false>(p, t0 + warp, t1, lane);
+                route_tokens<false>(p, t0 + warp, t1, warps, lane, s_choice[warp]);
         }
         uint16_t *hist = s_hist + warp * p.E;
         for (int i = lane; i < p.E; i += 32)
             hist[i] = 0;
         __syncthreads();
         // this warp's run of the CTA's slots
-        const int64_t per = (c1 - c0 + 32 * kRtWarps - 1) / (32 * kRtWarps) * 32;
+        const int64_t per = (c1 - c0 + threads - 1) / threads * 32;
         const int64_t s0 = min(c1, c0 + warp * per), s1 = min(c1, s0 + per);
         bool bad = false;
         each_slot(p, s0, s1, lane, [&](int64_t s, int e, int rank, bool last) {
-            if (!p.z && s < s1)
+            if (!kTopk && s < s1)
                 bad |= p.experts[s] >= p.E;
             const int h = e >= 0 ? hist[e] : 0;
             __syncwarp();
@@ -337,7 +406,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
         // per expert: counts of the warps before, and the CTA's
         if (tid < p.E) {
 #pragma unroll 8
-            for (int w = 0; w < kRtWarps; w++) {
+            for (int w = 0; w < warps; w++) {
                 const int c = s_hist[w * p.E + tid];
                 s_hist[w * p.E + tid] = (uint16_t)total;
                 total += c;
@@ -356,12 +425,12 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
     } else {
         // counts of all CTAs; the threads share out the CTAs where there are few experts
         __shared__ int s_before[kMoeMaxExperts], s_total[kMoeMaxExperts];
-        s_before[tid] = s_total[tid] = 0;
+        s_before[tid] = s_total[tid] = 0;   // 1024 threads
         __syncthreads();
-        const int width = (p.E + 31) / 32 * 32, groups = kRtThreads / width, g = tid / width, e = tid % width;
+        const int width = (p.E + 31) / 32 * 32, groups = threads / width, g = tid / width, e = tid % width;
         if (g < groups && e < p.E) {
             int b = 0, all = 0;
-#pragma unroll 4
+#pragma unroll 16
             for (int c = g; c < (int)gridDim.x; c += groups) {
                 const int v = counts[(int64_t)c * p.E + e];
                 all += v;
@@ -393,7 +462,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
     __syncthreads();
     const int rows = s_off[p.E];
     if (blockIdx.x == 0) {
-        for (int e = tid; e <= p.E; e += kRtThreads) {
+        for (int e = tid; e <= p.E; e += threads) {
             p.plan[p.offsets + e] = s_off[e];
             p.plan[p.first_block + e] = s_fb[e];
         }
@@ -402,20 +471,22 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
                           : tid == kMoeTileRows ? p.tile_rows : 0;
     }
     // lists of blocks and tiles: expert, first row of the padded and of the compact order, rows
-    int4 *blocks = reinterpret_cast<int4 *>(p.plan + p.blocks), *tiles = reinterpret_cast<int4 *>(p.plan + p.tiles);
-    for (int e = (int)blockIdx.x * kRtWarps + warp; e < p.E; e += (int)gridDim.x * kRtWarps) {
-        const int ne = s_off[e + 1] - s_off[e];
-        for (int b = lane; b < s_fb[e + 1] - s_fb[e]; b += 32)
-            blocks[s_fb[e] + b] = make_int4(e, (s_fb[e] + b) * kMoeBlock, s_off[e] + b * kMoeBlock,
-                                            min(kMoeBlock, ne - b * kMoeBlock));
-        for (int b = lane; b < s_ft[e + 1] - s_ft[e]; b += 32)
-            tiles[s_ft[e] + b] = make_int4(e, s_fb[e] * kMoeBlock + b * p.tile_rows, s_off[e] + b * p.tile_rows,
-                                           min(p.tile_rows, ne - b * p.tile_rows));
-    }
-    for (int64_t r = rows + (int64_t)blockIdx.x * kRtThreads + tid; r < p.slots; r += (int64_t)gridDim.x * kRtThreads)
+    auto list = [&](const int *first, int size, int4 *out) {
+        for (int i = (int)blockIdx.x * threads + tid; i < first[p.E]; i += (int)gridDim.x * threads) {
+            int e = 0;   // the last expert whose first is i or below
+            for (int step = kMoeMaxExperts / 2; step; step >>= 1)
+                if (e + step < p.E && first[e + step] <= i)
+                    e += step;
+            const int r = (i - first[e]) * size;
+            out[i] = make_int4(e, s_fb[e] * kMoeBlock + r, s_off[e] + r, min(size, s_off[e + 1] - s_off[e] - r));
+        }
+    };
+    list(s_fb, kMoeBlock, reinterpret_cast<int4 *>(p.plan + p.blocks));
+    list(s_ft, p.tile_rows, reinterpret_cast<int4 *>(p.plan + p.tiles));
+    for (int64_t r = rows + (int64_t)blockIdx.x * threads + tid; r < p.slots; r += (int64_t)gridDim.x * threads)
         p.plan[p.order + r] = -1;
     // places; in one CTA each thread meets the ranks that another warp wrote before the last barriers
-    for (int64_t s = c0 + tid; s < c1; s += kRtThreads) {
+    for (int64_t s = c0 + tid; s < c1; s += threads) {
         int e = p.experts[s], pos = -1, pad = -1;
         if (e >= 0 && e < p.E) {
             pos = s_base[e] + position[s];
@@ -791,6 +862,26 @@ CombineParams combine_params(const MoeCombineArgs &a)
     return p;
 }
 
+template <bool kTopk>
+cudaError_t run_route(const RouteParams &p, const MoeLayout &l, cudaStream_t s, const DeviceInfo &dev)
+{
+    if (l.ctas == 1) {
+        // a thread for each expert and each slot, a warp for each token
+        const int64_t want = std::max<int64_t>({p.E, l.slots, kTopk ? 32 * p.T : 0});
+        const int threads = (int)std::min<int64_t>(kRtThreads, (want + 31) / 32 * 32);
+        const cudaError_t e = allow_smem<route_kernel<kTopk, true, true>>(kRtMaxSmem, dev);
+        return e != cudaSuccess ? e : launch_dependent(route_kernel<kTopk, true, true>, 1, threads,
+                                                       (size_t)(threads / 32) * p.E * 2, s, p);
+    }
+    cudaError_t e = allow_smem<route_kernel<kTopk, true, false>>(kRtMaxSmem, dev);
+    if (e == cudaSuccess)
+        e = launch_dependent(route_kernel<kTopk, true, false>, (unsigned)l.ctas, kRtThreads, (size_t)kRtWarps * p.E * 2, s,
+                             p);
+    if (e == cudaSuccess)
+        e = launch_dependent(route_kernel<false, false, true>, (unsigned)l.ctas, kRtThreads, 0, s, p);
+    return e;
+}
+
 }  // namespace
 
 cudaError_t launch_moe_route(const MoeRouteArgs &a, cudaStream_t s, const DeviceInfo &dev)
@@ -822,17 +913,7 @@ cudaError_t launch_moe_route(const MoeRouteArgs &a, cudaStream_t s, const Device
     p.slots = l.slots;
     p.ctl = a.ctl;
     p.chunk = (int)((a.T + l.ctas - 1) / l.ctas);
-    const size_t smem = (size_t)kRtWarps * a.E * 2;   // of the first kernel
-    if (l.ctas == 1) {
-        const cudaError_t e = allow_smem<route_kernel<true, true>>(kRtMaxSmem, dev);
-        return e != cudaSuccess ? e : launch_dependent(route_kernel<true, true>, 1, kRtThreads, smem, s, p);
-    }
-    cudaError_t e = allow_smem<route_kernel<true, false>>(kRtMaxSmem, dev);
-    if (e == cudaSuccess)
-        e = launch_dependent(route_kernel<true, false>, (unsigned)l.ctas, kRtThreads, smem, s, p);
-    if (e == cudaSuccess)
-        e = launch_dependent(route_kernel<false, true>, (unsigned)l.ctas, kRtThreads, 0, s, p);
-    return e;
+    return a.z ? run_route<true>(p, l, s, dev) : run_route<false>(p, l, s, dev);
 }
 
 cudaError_t launch_moe_route_backward(const MoeRouteArgs &a, const float *dw, void *dz, int64_t lddz, cudaStream_t s)
