@@ -16,7 +16,10 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 bool ld_aligned(int64_t ld, nvfp4_dtype d) { return ld % (d == NVFP4_OUT_FP32 ? 4 : 8) == 0; }
 nvfp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
-bool matrix_ok(int64_t rows, int64_t K) { return rows >= 1 && rows <= kMaxDim && K >= 16 && K <= kMaxK && K % 16 == 0; }
+bool matrix_ok(int64_t rows, int64_t K)
+{
+    return rows >= 1 && rows <= kMaxDim && K >= 16 && K <= kMaxK && K % 16 == 0 && rows * K <= (1LL << 42);
+}
 
 Int8GemmArgs gemm_args(const void *x, const float *x_scale, const int8_t *w, const float *w_scale, int64_t M, int64_t N,
                        int64_t K, void *y, nvfp4_dtype dt, void *ws)

@@ -399,7 +399,8 @@ nvfp4_status nvfp4_moe_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, i
 size_t nvfp4_moe_linear_backward_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K)
 {
     // dX = Q(dY) Q_c(W): over N;  dW = Q_c(dY)^T Q_c(X): over the rows
-    if (!layer_ok(T, k, E, N, K) || !layer_ok(T, k, E, K, N))
+    if (!layer_ok(T, k, E, N, K) || !layer_ok(T, k, E, K, N) ||
+        E * ((N + 255) / 256) * ((K + 255) / 256) > (1LL << 30))
         return 0;
     const int64_t P = nvfp4_moe_padded_rows(T, k, E);
     return align256(kWsHeaderBytes) + align256(code_bytes(P, N)) + align256(scale_bytes(P, N)) +
