@@ -215,6 +215,17 @@ __device__ __forceinline__ uint4 ld_once_u4(const void *p)
     return v;
 }
 
+// The same through L1, for 16 bytes of a sector whose others are loaded next.
+__device__ __forceinline__ uint4 ld_u4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint4 ld_stream_u4(const void *p)
 {
     uint4 v;

@@ -13,6 +13,13 @@
 // them to TMEM.  Shared memory then carries each weight twice as one byte, and
 // not again as two bytes written and read.  Tokens are quantised to fp16
 // integers by a kernel before this one and come by TMA.
+//
+// What bounds it.  One token through 18944 x 3584: 15.8 us on the GPU, of which the
+// weights' bytes are 10; the rest is the launch, the first stage's way and the join
+// of two shares.  100 tokens through 3584 x 18944: 17 us and the quantiser's 5 (bytes
+// 10, MMAs 9; 37 us with one ring for codes, tokens and converted weights).  8192
+// tokens through 18944 x 3584: 664 us, 1.68 PFLOP/s, 97 % of what the library's bf16
+// product sustains and 87 % of its burst (power).
 #include <algorithm>
 #include <type_traits>
 

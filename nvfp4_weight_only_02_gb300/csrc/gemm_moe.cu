@@ -11,6 +11,14 @@
 // quantised operands every expert's rows begin on a multiple of 128, where the
 // tiled scales and the copies can start; in Y the rows are compact, so stores
 // are by row and never touch a row of another expert or one behind the last.
+//
+// What bounds it.  Few rows: the weights' bytes (64 tokens with 4 of 60 experts of
+// 2600 x 3584: 46 us, 6.5 TB/s).  Many: 8192 tokens with 8 of 128 experts of 1536 x
+// 4096 take 155 us for 764 MB moved (DRAM 4.9 TB/s, tensor pipe 59 %); the experts'
+// last tiles are a quarter more tiles than full ones would be, and a tile of few
+// rows costs 0.23 us a stage, one of 256 rows 0.28 (gemm_w4a4_tile.cu).  Measured
+// and left out: rows gathered by the product itself (mx_quant.cu), weights or Y
+// marked to be evicted first (217 and 203 us for the layer, 204 without).
 #include <algorithm>
 
 #include "common.cuh"
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(kMsThreads, 2)
     __shared__ __align__(8) uint64_t full[kWsMaxStages], empty[kWsMaxStages], acc_full[1];
     __shared__ uint32_t s_tmem;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
     const int item = blockIdx.x / p.split, wt = item % p.wtiles;
     const int ks0 = (int)((int64_t)p.ksteps * rank / p.split), ks1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);

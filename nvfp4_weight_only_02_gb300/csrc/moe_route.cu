@@ -13,6 +13,11 @@
 // depends on nothing but the experts: a warp counts its run of slots 32 at a
 // time (lanes with equal experts rank themselves by match), counts are summed
 // over warps and CTAs, and the second pass places each slot.
+//
+// What bounds it.  16384 tokens, 8 of 256 experts: choosing 19 us (the integer
+// pipe), placing about 10 (the second kernel waits for each CTA's counts, 152 x
+// 256 of them read by every CTA), gradient 5 (bytes).  8192 tokens, 8 rows each of
+// 4096 in bf16: sum 96 us (93 % of the copy rate), its gradients 197 (85 %).
 #include <algorithm>
 
 #include "common.cuh"

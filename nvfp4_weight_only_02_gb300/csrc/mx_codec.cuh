@@ -83,6 +83,7 @@ template <>
 struct Raw8<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = ld_once_u4(p); }
+    __device__ __forceinline__ void load_near(const __nv_bfloat16 *p) { a = ld_u4(p); }   // neighbours follow: by L1
     __device__ __forceinline__ void store_shared(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void floats(float (&v)[8]) const
@@ -127,6 +128,11 @@ struct Raw8<float> {
     {
         a = ld_once_u4(p);
         b = ld_once_u4(p + 4);
+    }
+    __device__ __forceinline__ void load_near(const float *p)
+    {
+        a = ld_u4(p);
+        b = ld_u4(p + 4);
     }
     __device__ __forceinline__ void store_shared(float *p) const
     {

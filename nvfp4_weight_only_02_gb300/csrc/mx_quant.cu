@@ -261,18 +261,19 @@ __global__ void __launch_bounds__(kMqThreads)
     }
 }
 
-// Rows of x to their places in the experts' order, each read once: a warp takes
-// 1024 elements of a row, quantises them and writes codes and scale words to
-// every place that the row has (a token has one for each of its experts).  Four
-// lanes hold a block of 32, eight elements each, in four passes over 256; the
-// codes change lanes so that each lane stores 16 bytes, and the scale words are
-// stored a place a lane.  The rows behind an expert's last one are left as they
-// are: a product's output rows depend on their own row only.
+// Rows of x to their places in the experts' order, each read once: a lane takes
+// a block of 32 elements and writes its codes, 16 bytes, to every place that the
+// row has (a token has one for each of its experts); four lanes put their scale
+// bytes into a word and store it to four places at a time.  The rows behind an
+// expert's last one are left as they are: a product's output rows depend on their
+// own row only.
 //
-// What bounds it: bytes; with 4-byte stores and a scale word at a time it was
-// bound by issue (8192 tokens of 4096, 8 places each: 66 us).  Measured against
-// it: one copy of the codes, whose rows the product gathers by TMA (four rows an
-// instruction): 18 cycles a row, and the product takes three times as long.
+// What bounds it: bytes.  8192 tokens of 4096 with 8 places each: 36 us (6.1 TB/s,
+// 89 % of the copy rate); with a block over four lanes, exchanged by shuffles for
+// 16-byte stores, 38, with 4-byte stores 66 (issue).  Measured against it: one copy of
+// the codes, whose rows the product gathers by TMA (four rows an instruction: 18
+// cycles a row, three times what its MMAs take) or by cp.async (the product takes 21
+// us longer, this kernel 12 us less).
 constexpr int kMrChunk = 1024;
 
 template <typename T>
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(256)
 {
     const int lane = threadIdx.x & 31;
     const int64_t chunks = (cols + kMrChunk - 1) / kMrChunk, ktiles = (cols + 127) / 128;
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), r = i / chunks, c0 = i % chunks * kMrChunk;
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), r = i / chunks;
+    const int64_t c = i % chunks * kMrChunk + lane * 32;   // this lane's block
     pdl_wait();
     pdl_launch_dependents();
     if (r >= (m.k ? rows : min(rows, (int64_t)m.header[0])))   // grouped rows that there are
@@ -290,51 +292,26 @@ __global__ void __launch_bounds__(256)
     Raw8<T> raw[4];
 #pragma unroll
     for (int u = 0; u < 4; u++) {
-        const int64_t c = c0 + u * 256 + lane * 8;
         raw[u].zero();
         if (c < cols)
-            raw[u].load(x + r * ld + c);
+            raw[u].load_near(x + r * ld + c + u * 8);
     }
     const int n = m.k ? m.k : 1;
     // lane j: place j of the row
     int mine = -1;
     if (lane < n)
         mine = m.padded[m.k ? r * n + lane : m.order[r]];
-    uint32_t q[4], word[4];   // word: this lane's half of the 256 elements, four blocks
+    uint32_t a = 0, byte, q[4];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-        uint32_t a = raw[u].amax_bits();
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        uint32_t byte;
+    for (int u = 0; u < 4; u++)
+        a = max(a, raw[u].amax_bits());
+#pragma unroll
+    for (int u = 0; u < 4; u++)
         q[u] = raw[u].encode(a, byte);
-        // bytes of lanes 4 b + .. of the half
-        uint32_t w = byte << (lane & 12) * 2;
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        w |= __shfl_xor_sync(0xffffffffu, w, 8);
-        word[u] = w;
-    }
-    // four lanes exchange: lane l gets pass l % 4 of its group of four, 16 bytes
-#pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-        const bool up = lane & d;
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            if (!(u & d)) {
-                const uint32_t give = up ? q[u] : q[u | d];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
-                q[u] = up ? got : q[u];
-                q[u | d] = up ? q[u | d] : got;
-            }
-        }
-    }
-    const int64_t c = c0 + (lane & 3) * 256 + (lane >> 2) * 32;
-    // scale words: place lane / 8 (four places at a time), pass and half lane % 8
-    const uint32_t s0 = __shfl_sync(0xffffffffu, word[0], (lane & 1) * 16), s1 = __shfl_sync(0xffffffffu, word[1], (lane & 1) * 16);
-    const uint32_t s2 = __shfl_sync(0xffffffffu, word[2], (lane & 1) * 16), s3 = __shfl_sync(0xffffffffu, word[3], (lane & 1) * 16);
-    const int pass = (lane & 7) >> 1;
-    const uint32_t sw = pass & 2 ? (pass & 1 ? s3 : s2) : (pass & 1 ? s1 : s0);
-    const int64_t kt = c0 / 128 + (lane & 7);
+    uint32_t word = byte << (lane & 3) * 8;
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    const int64_t kt = c / 128;
     for (int j0 = 0; j0 < n; j0 += 4) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -342,10 +319,10 @@ __global__ void __launch_bounds__(256)
             if (at >= 0 && c < cols)
                 *reinterpret_cast<uint4 *>(codes + ((int64_t)at * cols + c) / 2) = make_uint4(q[0], q[1], q[2], q[3]);
         }
-        const int at = __shfl_sync(0xffffffffu, mine, (j0 + (lane >> 3)) & 31);
-        if (j0 + (lane >> 3) < n && at >= 0 && kt < ktiles)
+        const int at = __shfl_sync(0xffffffffu, mine, (j0 + (lane & 3)) & 31);
+        if (j0 + (lane & 3) < n && at >= 0 && kt < ktiles)
             *reinterpret_cast<uint32_t *>(scales + ((int64_t)(at >> 7) * ktiles + kt) * 512 + (at & 31) * 16 +
-                                          (at & 127) / 32 * 4) = sw;
+                                          (at & 127) / 32 * 4) = word;
     }
 }
 
