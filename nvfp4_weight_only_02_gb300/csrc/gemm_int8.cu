@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kIsThreads, IsShape<NT, kTok>::kCtas)
     } else if (warp == kI8Conv + 2) {
         // ---------------- MMA
         if (elect_one()) {
-            constexpr uint32_t id = idesc_f16(kI8Rows, NT, 0);
+            const uint32_t id = idesc_f16(kI8Rows, (cols + 15) & ~15, 0);
             bool ok = !S::kOwn || mbar_wait(&x_full[0], 0);
             int i = 0;
             for (; i < nk && ok; i++) {
@@ -732,6 +732,11 @@ cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const Device
         return run_int8_stream<32>(a, s, dev);
     if (a.M <= 64)
         return run_int8_stream<64>(a, s, dev);
+    // More than 128 tokens go to the tile kernel, 256 x 256 at a time on 76 pairs of CTAs, unless there are few such tiles
+    // or long sums for them: only the stream splits K (N = 3584, with the quantiser, 200 tokens: K = 18944 42.7 us and 88.9 with
+    // tiles, K = 3584 17.9 and 25.2; 400 and 512: 67.4 and 98.7, 19.8 and 28.6).
+    // Its tokens bound it there: each CTA of 128 weight rows copies them all, 55 of the 64 bytes a cycle that an SM gets.
+    // 256 tokens at a time are no better (200 tokens 59 us, 512 81): more to copy for a stage, and room for two stages only.
     const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
     if (a.M <= 128 || (big * 5 <= dev.num_sms && a.M <= 512))
         return run_int8_stream<128>(a, s, dev);

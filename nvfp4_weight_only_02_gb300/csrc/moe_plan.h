@@ -48,7 +48,7 @@ struct MoeLayout {
         const int64_t some = std::min<int64_t>(slots, E);   // experts with rows, at most
         max_blocks = slots / kMoeBlock + some;
         max_tiles = slots / tile_rows + some;
-        ctas = (int)std::max<int64_t>(std::min<int64_t>(152, (slots + 511) / 512), (slots + kMoeChunk - 1) / kMoeChunk);
+        ctas = (int)std::max<int64_t>(std::min<int64_t>(152, (slots + 1023) / 1024), (slots + kMoeChunk - 1) / kMoeChunk);
         int64_t at = kMoeHeader;
         auto take = [&](int64_t words) {
             const int64_t p = at;
