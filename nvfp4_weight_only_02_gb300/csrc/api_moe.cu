@@ -391,6 +391,7 @@ nvfp4_status nvfp4_moe_linear(const void *x, nvfp4_dtype x_dtype, int64_t ldx, i
         a.x_scales = q.scales;
         a.w_codes = w_codes;
         a.w_scales = w_scales;
+        a.after_quantise = true;
         e = launch_moe_gemm(a, (cudaStream_t)stream, *dev);
     }
     return from_cuda(e);
@@ -451,6 +452,7 @@ nvfp4_status nvfp4_moe_linear_backward(const void *dy, nvfp4_dtype dy_dtype, int
         a.x_scales = scales;
         a.w_codes = w_codes_t;
         a.w_scales = w_scales_t;
+        a.after_quantise = true;
         e = launch_moe_gemm(a, s, *dev);
     }
     if (e == cudaSuccess && dw) {

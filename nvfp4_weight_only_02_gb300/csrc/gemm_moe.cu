@@ -45,6 +45,7 @@ struct MoeParams {
     int wrows;     // scale tiles over an expert's rows
     int split;     // streaming: CTAs of a cluster that share a tile's K
     int stages;
+    int early;     // the plan and the weights were complete before the kernel before this one started its work
     void *y;
     int y_fp32;
     uint32_t *ctl;
@@ -300,10 +301,17 @@ __global__ void __launch_bounds__(kMsThreads, 2)
     const int item = blockIdx.x / p.split, wt = item % p.wtiles;
     const int ks0 = (int)((int64_t)p.ksteps * rank / p.split), ks1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);
     const int nk = ks1 - ks0;
-    pdl_wait();
-    pdl_launch_dependents();
-    if (item / p.wtiles >= p.header[kMoeTiles])
-        return;     // the whole cluster
+    // Behind the quantiser, which waited for what is before it, the list and the weights can be read at once; only the
+    // rows are waited for.
+    if (!p.early) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    if (item / p.wtiles >= p.header[kMoeTiles]) {
+        if (p.early)
+            pdl_wait();     // a launch of nothing but these must not end before the quantiser
+        return;             // the whole cluster
+    }
     const int4 tile = p.tiles[item / p.wtiles];
 
     uint8_t *sW = smem, *sX = sW + kStages * kWsRows * 128;
@@ -332,20 +340,37 @@ __global__ void __launch_bounds__(kMsThreads, 2)
             const uint8_t *wsc = p.w_scales + ((size_t)tile.x * p.wrows + wt) * p.ktiles * 512;
             const uint8_t *xsc = p.x_scales + (size_t)(tile.y / kMoeBlock) * p.ktiles * 512;
             const bool few = tile.w <= kMsFew;
-            int st = 0;
-            uint32_t ph = 1;
-            for (int i = 0; i < nk; i++) {
-                if (i >= kStages && !mbar_wait(&empty[st], ph)) {
-                    record_status(p.ctl, NVFP4_ERR_TIMEOUT);
-                    break;
-                }
+            auto scale_bytes = [&](int ks) { return (uint32_t)min(S::kTiles, p.ktiles - ks * S::kTiles) * 512u; };
+            auto load_w = [&](int i, int st) {
                 const int ks = ks0 + i;
-                const uint32_t sb = (uint32_t)min(S::kTiles, p.ktiles - ks * S::kTiles) * 512u;
+                const uint32_t sb = scale_bytes(ks);
                 mbar_arrive_expect_tx(&full[st], (kWsRows + (few ? kMsFew : NT)) * 128 + 2 * sb);
                 tma_load_3d(sW + st * kWsRows * 128, &tm_w, &full[st], ks * 128, wt * kWsRows, tile.x);
                 bulk_g2s(sWs + st * S::kScaleBytes, wsc + (size_t)ks * S::kScaleBytes, sb, &full[st]);
+            };
+            auto load_x = [&](int i, int st) {
+                const int ks = ks0 + i;
                 tma_load_2d(sX + st * NT * 128, few ? &tm_few : &tm_x, &full[st], ks * 128, tile.y);
-                bulk_g2s(sXs + st * S::kScaleBytes, xsc + (size_t)ks * S::kScaleBytes, sb, &full[st]);
+                bulk_g2s(sXs + st * S::kScaleBytes, xsc + (size_t)ks * S::kScaleBytes, scale_bytes(ks), &full[st]);
+            };
+            const int head = min(nk, kStages);
+            for (int i = 0; i < head; i++)
+                load_w(i, i);
+            if (p.early) {
+                pdl_wait();
+                pdl_launch_dependents();
+            }
+            for (int i = 0; i < head; i++)
+                load_x(i, i);
+            int st = 0;
+            uint32_t ph = 0;
+            for (int i = head; i < nk; i++) {
+                if (!mbar_wait(&empty[st], ph)) {
+                    record_status(p.ctl, NVFP4_ERR_TIMEOUT);
+                    break;
+                }
+                load_w(i, st);
+                load_x(i, st);
                 if (++st == kStages) {
                     st = 0;
                     ph ^= 1;
@@ -413,6 +438,8 @@ __global__ void __launch_bounds__(kMsThreads, 2)
             }
         }
     } else {
+        if (p.early)
+            pdl_wait();     // before Y is written
         if (!mbar_wait_warp(acc_full, 0)) {
             if (threadIdx.x == 0)
                 record_status(p.ctl, NVFP4_ERR_TIMEOUT);
@@ -779,6 +806,7 @@ MoeParams params(const MoeGemmArgs &a)
     p.ktiles = (int)((a.K + 127) / 128);
     p.wrows = (int)((a.N + 127) / 128);
     p.split = 1;
+    p.early = a.after_quantise ? 1 : 0;
     p.y = a.y;
     p.y_fp32 = a.y_fp32 ? 1 : 0;
     p.ctl = a.ctl;

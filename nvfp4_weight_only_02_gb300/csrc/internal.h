@@ -250,6 +250,7 @@ struct MoeGemmArgs {
     void *y;                             // rows x N
     bool y_fp32;
     uint32_t *ctl;
+    bool after_quantise;                 // launched right behind the quantiser of x on the same stream
 };
 cudaError_t launch_moe_gemm(const MoeGemmArgs &a, cudaStream_t s, const DeviceInfo &dev);
 // dW[e] = A_e^T X_e over the expert's rows: operands N x padded rows and K x

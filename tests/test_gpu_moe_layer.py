@@ -153,3 +153,33 @@ def test_weights_quantised_as_each_alone(nv):
             assert torch.equal(q.row.codes[e], one.row.codes) and torch.equal(q.row.scales[e], one.row.scales)
             assert torch.equal(q.col.codes[e], one.col.codes) and torch.equal(q.col.scales[e], one.col.scales)
             assert torch.equal(q.row.expert(e).dequantize(), one.row.dequantize())
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 2, 4), (30, 2, 5), (400, 2, 4)])
+def test_layers_behind_one_another(nv, T, k, E):
+    """Launches overlap: each call's rows are what the call before has just written, its output goes where that read,
+    and every other call's plan has just been made."""
+    g = _gen(T)
+    K, R = 512, T * k
+    ex = _experts(T, k, E, "random", g)
+    ws_ = [nv.moe_quantize_weights(torch.randn(E, K, K, device="cuda", generator=g) / K ** 0.5).row for _ in range(3)]
+    x = torch.randn(R, K, device="cuda", generator=g)
+    plan = nv.moe_plan(ex, E)
+    space = nv.new_workspace(nv.nvfp4_moe_linear_workspace_bytes(T, k, E, K, K))
+    want, t = [], x
+    for i in range(12):
+        t = nv.moe_linear(t, ws_[i % 3], plan, sorted_rows=True)
+        torch.cuda.synchronize()
+        want.append(t)
+    for _ in range(3):
+        buf = [x.clone(), torch.empty_like(x)]
+        torch.cuda.synchronize()
+        for i in range(12):
+            a, b = buf[i % 2], buf[1 - i % 2]
+            if i % 2:
+                plan = nv.moe_plan(ex, E)
+            nv._call("nvfp4_moe_linear", a.data_ptr(), nv.OUT_FP32, K, 1, *ws_[i % 3].addresses(), plan.buffer.data_ptr(),
+                     plan.nbytes, T, k, E, K, K, b.data_ptr(), nv.OUT_FP32, space.data_ptr(), space.numel(),
+                     nv._raw_stream())
+        assert torch.equal(buf[0], want[11]) and torch.equal(buf[1], want[10])
+    assert nv.nvfp4_get_device_status(space) == nv.OK
