@@ -18,8 +18,8 @@
 // weights' bytes are 10; the rest is the launch, the first stage's way and the join
 // of two shares.  100 tokens through 3584 x 18944: 17 us and the quantiser's 5 (bytes
 // 10, MMAs 9; 37 us with one ring for codes, tokens and converted weights).  8192
-// tokens through 18944 x 3584: 664 us, 1.68 PFLOP/s, 97 % of what the library's bf16
-// product sustains and 87 % of its burst (power).
+// tokens through 18944 x 3584: about 600 us beside the quantiser, 1.85 PFLOP/s, 96 % of
+// the library's bf16 product in a burst and 107 % of what it sustains (power).
 #include <algorithm>
 #include <type_traits>
 
@@ -394,29 +394,37 @@ __global__ void __launch_bounds__(kIsThreads, IsShape<NT, kTok>::kCtas)
 }
 
 // ---------------------------------------------------------------- many tokens
-// CTA pairs, 256 weight rows x 256 tokens at a time, persistent.  Both CTAs
+// CTA pairs, 256 weight rows x BN tokens at a time, persistent.  Both CTAs
 // convert their 128 weight rows into their own TMEM; the leader's MMAs read
-// both, and half of the tokens from each CTA's shared memory.
-constexpr int kItTokens = 256;
+// both, and half of the tokens from each CTA's shared memory.  Up to 192 tokens
+// there are two accumulators beside the converted weights' columns, so that a
+// tile's results are scaled and stored while the next tile is multiplied.
 constexpr int kItEpi = 4;
 constexpr int kItThreads = 32 * (kI8Conv + kItEpi + 2);   // converting, epilogue, copies, MMA
-constexpr int kItStages = 4;
-static_assert(kItStages % kI8Groups == 0, "see the converting warps' waits");
-constexpr int kItXBytes = kItTokens / 2 * kI8K * 2, kItStageBytes = kI8WBytes + kItXBytes;
-constexpr size_t kItSmem = 512 + (size_t)kItStages * kItStageBytes + kStageOut;
 constexpr int kItGroup = 8;   // raster: token tiles per group
 
-template <bool kF32>
+template <int BN>
+struct ItShape {
+    static constexpr int kXBytes = BN / 2 * kI8K * 2, kStageBytes = kI8WBytes + kXBytes;
+    static constexpr int kFit = (232448 - 512 - kStageOut) / kStageBytes, kStages = kFit < 6 ? kFit : 6;
+    static constexpr size_t kSmem = 512 + (size_t)kStages * kStageBytes + kStageOut;
+    static constexpr int kAcc = BN <= 192 ? 2 : 1;               // accumulators
+    static constexpr int kFree = (512 - kAcc * BN) / kI8ACols, kA = kFree < 4 ? kFree : 4;   // stages of converted weights
+    static_assert(kA % kI8Groups == 0 && kStages >= kA, "see the converting warps' waits");
+};
+
+template <int BN, bool kF32>
 __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
     int8_tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Int8Params p)
 {
-    constexpr int kStages = kItStages;
+    using S = ItShape<BN>;
+    constexpr int kStages = S::kStages, kA = S::kA, kAcc = S::kAcc;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sW = smem, *sX = sW + kStages * kI8WBytes;
-    uint8_t *sOut = sX + kStages * kItXBytes;
+    uint8_t *sW = smem, *sX = sW + kStages * kI8WBytes, *sOut = sX + kStages * S::kXBytes;
     uint64_t *full_w = reinterpret_cast<uint64_t *>(sOut + kStageOut), *full_x = full_w + kStages;
-    uint64_t *a_full = full_x + kStages, *done = a_full + kStages, *acc_full = done + kStages, *acc_empty = acc_full + 1;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 1);
+    uint64_t *done = full_x + kStages, *a_full = done + kStages, *a_empty = a_full + kA;
+    uint64_t *acc_full = a_empty + kA, *acc_empty = acc_full + kAcc;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + kAcc);
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
     volatile uint32_t *s_loaded = s_tmem + 2, *s_issued = s_tmem + 3;   // stages copied and multiplied
 
@@ -426,11 +434,16 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
         for (int s = 0; s < kStages; s++) {
             mbar_init(&full_w[s], 1);
             mbar_init(&full_x[s], 1);
-            mbar_init(&a_full[s], 2 * 4);
             mbar_init(&done[s], 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 2 * kItEpi);
+        for (int s = 0; s < kA; s++) {
+            mbar_init(&a_full[s], 2 * 4);
+            mbar_init(&a_empty[s], 1);
+        }
+        for (int s = 0; s < kAcc; s++) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 2 * kItEpi);
+        }
         *s_abort = 0;
         *s_loaded = 0;
         *s_issued = 0;
@@ -442,7 +455,7 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers and TMEM before anything of the pair touches them
     tc_fence_after();
-    const uint32_t tmem = *s_tmem, a_ring = tmem + kItTokens;
+    const uint32_t tmem = *s_tmem, a_ring = tmem + kAcc * BN;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
         nt = i / gm;
     };
     // columns of a tile's MMAs
-    auto width = [&](int mt) { return (min(kItTokens, p.M - mt * kItTokens) + 31) & ~31; };
+    auto width = [&](int mt) { return (min(BN, p.M - mt * BN) + 31) & ~31; };
 
     if (warp == kI8Conv + kItEpi) {
         // ---------------- copies: this CTA's weight rows, and half of the tokens for the leader's barrier
@@ -469,7 +482,7 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
             for (int t = cid; t < ntot && !*s_abort; t += ncl) {
                 int mt, nt;
                 tile_at(t, mt, nt);
-                const int m0 = mt * kItTokens + crank * (width(mt) / 2), n0 = nt * 256 + crank * 128;
+                const int m0 = mt * BN + crank * (width(mt) / 2), n0 = nt * 256 + crank * 128;
                 for (int ks = 0; ks < p.ksteps; ks++, it++) {
                     const int st = it % kStages;
                     if (!mbar_wait(&done[st], ((it / kStages) & 1) ^ 1)) {
@@ -480,9 +493,9 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
                     tma_load_2d(sW + st * kI8WBytes, &tm_w, &full_w[st], ks * kI8K, n0);
                     const uint32_t bar = cluster_addr(&full_x[st], 0);
                     if (crank == 0)
-                        mbar_arrive_expect_tx(&full_x[st], 2 * kItXBytes);
-                    tma_load_2d_pair(sX + st * kItXBytes, &tm_x, bar, ks * kI8K, m0);
-                    tma_load_2d_pair(sX + st * kItXBytes + kItXBytes / 2, &tm_x, bar, ks * kI8K + 64, m0);
+                        mbar_arrive_expect_tx(&full_x[st], 2 * S::kXBytes);
+                    tma_load_2d_pair(sX + st * S::kXBytes, &tm_x, bar, ks * kI8K, m0);
+                    tma_load_2d_pair(sX + st * S::kXBytes + S::kXBytes / 2, &tm_x, bar, ks * kI8K + 64, m0);
                 }
             }
             // every stage released before leaving: the leader's commits must not arrive at a CTA that is gone
@@ -501,27 +514,29 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
                 int mt, nt;
                 tile_at(t, mt, nt);
                 const uint32_t id = idesc_f16(256, width(mt), 0);
-                if (lt >= 1 && !mbar_wait(acc_empty, (lt - 1) & 1)) {
+                if (lt >= kAcc && !mbar_wait(&acc_empty[lt % kAcc], (lt / kAcc - 1) & 1)) {
                     fail();
                     break;
                 }
                 tc_fence_after();
+                const uint32_t acc = tmem + lt % kAcc * BN;
                 bool ok = true;
                 for (int ks = 0; ks < p.ksteps; ks++, it++) {
-                    const int st = it % kStages;
-                    if (!mbar_wait(&full_x[st], (it / kStages) & 1) || !mbar_wait(&a_full[st], (it / kStages) & 1)) {
+                    const int st = it % kStages, sa = it % kA;
+                    if (!mbar_wait(&full_x[st], (it / kStages) & 1) || !mbar_wait(&a_full[sa], (it / kA) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * kItXBytes));
+                    const uint64_t xd = smem_desc_sw128(smem_addr(sX + st * S::kXBytes));
 #pragma unroll
                     for (int j = 0; j < kI8K / 16; j++)
-                        mma_f16_ts_pair(tmem, a_ring + st * kI8ACols + j * 8, xd + (j / 4) * (kItXBytes / 2 / 16) + (j % 4) * 2,
+                        mma_f16_ts_pair(acc, a_ring + sa * kI8ACols + j * 8, xd + (j / 4) * (S::kXBytes / 2 / 16) + (j % 4) * 2,
                                         id, (ks | j) != 0);
+                    mma_commit_pair(&a_empty[sa]);
                     mma_commit_pair(&done[st]);
                     if (ks + 1 == p.ksteps)
-                        mma_commit_pair(acc_full);
+                        mma_commit_pair(&acc_full[lt % kAcc]);
                 }
                 if (!ok) {
                     fail();
@@ -535,32 +550,32 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t it = (uint32_t)warp / 4;
         const uint32_t total = (uint32_t)((ntot - cid + ncl - 1) / ncl) * (uint32_t)p.ksteps;
         for (; it < total; it += kI8Groups) {
-            const int st = it % kStages;
-            // a stage that has landed was copied when the MMAs on its TMEM columns were done (a group has every use of
-            // a barrier that it has one of: kStages is a multiple of the groups)
-            if (!mbar_wait_warp(&full_w[st], (it / kStages) & 1)) {
+            const int st = it % kStages, sa = it % kA;
+            // In this order, as in the streaming kernel: the MMAs kA stages ago are behind the use of full_w before this one.
+            // (A group has every use of the columns that it has one of.)
+            if ((it >= kA && !mbar_wait_warp(&a_empty[sa], (it / kA - 1) & 1)) ||
+                !mbar_wait_warp(&full_w[st], (it / kStages) & 1)) {
                 fail();
                 break;
             }
             if (aborted())
                 break;
             tc_fence_after();
-            convert_rows(sW + st * kI8WBytes, a_ring + st * kI8ACols, warp, lane);
+            convert_rows(sW + st * kI8WBytes, a_ring + sa * kI8ACols, warp, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(cluster_addr(&a_full[st], 0));   // hands over TMEM that is written (wait::st)
+                mbar_arrive_cluster(cluster_addr(&a_full[sa], 0));   // hands over TMEM that is written (wait::st)
         }
     } else {
         // ---------------- epilogue: a warp has 32 weight rows
         const int quad = warp & 3;
-        const uint32_t bar = cluster_addr(acc_empty, 0);
         uint32_t lt = 0;
         bool dead = false;   // after a wait that gave up: the four warps that store together stay together
         for (int t = cid; t < ntot; t += ncl, lt++) {
             int mt, nt;
             tile_at(t, mt, nt);
-            const int n0 = nt * 256 + crank * 128, rows = min(kItTokens, p.M - mt * kItTokens);
+            const int n0 = nt * 256 + crank * 128, rows = min(BN, p.M - mt * BN);
             // scales of the outputs that the thread's registers hold: its lane's, or in the fragments' layout four
             float sw[4];
 #pragma unroll
@@ -568,28 +583,28 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
                 const int n = n0 + quad * 32 + (kF32 ? lane : 8 * i + lane / 4);
                 sw[i] = n < p.N ? p.w_scale[n] : 0.0f;
             }
-            if (!dead && (aborted() || !mbar_wait_warp(acc_full, lt & 1))) {
+            if (!dead && (aborted() || !mbar_wait_warp(&acc_full[lt % kAcc], (lt / kAcc) & 1))) {
                 fail();
                 dead = true;
             }
             tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + lt % kAcc * BN;
             uint32_t buf[2][32];
             tile_ld_start<kF32>(acc, buf[0]);
 #pragma unroll
-            for (int c = 0; c < kItTokens / 32; c++) {
+            for (int c = 0; c < BN / 32; c++) {
                 uint32_t(&v)[32] = buf[c & 1];
                 __syncwarp();   // the stores before may have parted the warp
                 tmem_ld32_finish(v);
-                if (c + 1 < kItTokens / 32) {
+                if (c + 1 < BN / 32) {
                     tile_ld_start<kF32>(acc + (c + 1) * 32, buf[(c + 1) & 1]);
                 } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive_cluster(bar);
+                        mbar_arrive_cluster(cluster_addr(&acc_empty[lt % kAcc], 0));
                 }
-                const int left = min(32, rows - c * 32), m = mt * kItTokens + c * 32;
+                const int left = min(32, rows - c * 32), m = mt * BN + c * 32;
                 if (left <= 0 || n0 >= p.N)
                     continue;
                 const float sx = lane < left ? p.x_scale[m + lane] : 0.0f;
@@ -694,21 +709,48 @@ cudaError_t run_int8_stream(const Int8GemmArgs &a, cudaStream_t s, const DeviceI
     return cudaLaunchKernelEx(&cfg, int8_stream_kernel<NT, kTok>, tw, tx, p);
 }
 
-template <bool kF32>
+template <int BN, bool kF32>
 cudaError_t run_int8_tile(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
 {
+    using S = ItShape<BN>;
     CUtensorMap tw, tx;
-    cudaError_t e = maps(&tw, &tx, a, kItTokens / 2);
+    cudaError_t e = maps(&tw, &tx, a, BN / 2);
     if (e == cudaSuccess)
-        e = allow_smem<int8_tile_kernel<kF32>>(kItSmem, dev);
+        e = allow_smem<int8_tile_kernel<BN, kF32>>(S::kSmem, dev);
     if (e != cudaSuccess)
         return e;
     Int8Params p = params(a);
-    p.mtiles = (int)((a.M + kItTokens - 1) / kItTokens);
+    p.mtiles = (int)((a.M + BN - 1) / BN);
     p.ntiles = (int)((a.N + 255) / 256);
     const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
-    return launch_dependent(int8_tile_kernel<kF32>, dim3(2 * (unsigned)std::min<int64_t>(tiles, dev.num_sms / 2)), kItThreads,
-                            kItSmem, s, tw, tx, p);
+    return launch_dependent(int8_tile_kernel<BN, kF32>, dim3(2 * (unsigned)std::min<int64_t>(tiles, dev.num_sms / 2)),
+                            kItThreads, S::kSmem, s, tw, tx, p);
+}
+
+// Tokens a tile: the width whose waves of pairs take least.  A stage of 128
+// elements of K takes 0.66 us at 256 tokens, 0.53 at 192 and 0.355 at 128 (near the
+// power limit), and 2.5 us pass between tiles of 256.  With the quantiser, us at 256
+// / 192 / 128: 8192 x 18944 x 3584 685 / 628 / 621; 1024 94 / 99 / 86; 200 x 27648 x
+// 5120 62 / 71 / 52; 700 x 3584 x 18944 103 / 94 / 110; 4096 340 / 441 / 365; 2048 x 3584
+// x 3584 54 / 58 / 42.
+template <bool kF32>
+cudaError_t run_widths(const Int8GemmArgs &a, cudaStream_t s, const DeviceInfo &dev)
+{
+    const int widths[3] = {256, 192, 128};
+    const double stage[3] = {0.66, 0.53, 0.355}, apart[3] = {2.5, 0.3, 0.3};
+    const int64_t ksteps = (a.K + kI8K - 1) / kI8K, pairs = dev.num_sms / 2;
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < 3; i++) {
+        const int64_t tiles = ((a.M + widths[i] - 1) / widths[i]) * ((a.N + 255) / 256);
+        const double t = (double)((tiles + pairs - 1) / pairs) * (ksteps * stage[i] + apart[i]);
+        if (i == 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    return best == 0 ? run_int8_tile<256, kF32>(a, s, dev) : best == 1 ? run_int8_tile<192, kF32>(a, s, dev)
+                                                                       : run_int8_tile<128, kF32>(a, s, dev);
 }
 
 }  // namespace
@@ -740,7 +782,7 @@ cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const Device
     const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
     if (a.M <= 128 || (big * 5 <= dev.num_sms && a.M <= 512))
         return run_int8_stream<128>(a, s, dev);
-    return a.y_fp32 ? run_int8_tile<true>(a, s, dev) : run_int8_tile<false>(a, s, dev);
+    return a.y_fp32 ? run_widths<true>(a, s, dev) : run_widths<false>(a, s, dev);
 }
 
 }  // namespace nvfp4
