@@ -774,13 +774,12 @@ cudaError_t launch_int8_gemm(const Int8GemmArgs &a, cudaStream_t s, const Device
         return run_int8_stream<32>(a, s, dev);
     if (a.M <= 64)
         return run_int8_stream<64>(a, s, dev);
-    // More than 128 tokens go to the tile kernel, 256 x 256 at a time on 76 pairs of CTAs, unless there are few such tiles
-    // or long sums for them: only the stream splits K (N = 3584, with the quantiser, 200 tokens: K = 18944 42.7 us and 88.9 with
-    // tiles, K = 3584 17.9 and 25.2; 400 and 512: 67.4 and 98.7, 19.8 and 28.6).
-    // Its tokens bound it there: each CTA of 128 weight rows copies them all, 55 of the 64 bytes a cycle that an SM gets.
-    // 256 tokens at a time are no better (200 tokens 59 us, 512 81): more to copy for a stage, and room for two stages only.
-    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (a.M <= 128 || (big * 5 <= dev.num_sms && a.M <= 512))
+    // More than 128 tokens go to the tile kernel, unless there are few tiles: only the stream splits K (with the quantiser,
+    // stream / tiles: 200 x 3584 x 18944 42.6 / 58.4 us, 512 x 1000 x 4096 15.0 / 19.6; without a split 300 x 3584 x 18944
+    // 65.2 / 58.4, 512 x 3584 x 3584 19.9 / 21.1; up to 128 tokens 100 x 18944 x 3584 21.7 / 24.1).  Its tokens bound it:
+    // each CTA of 128 weight rows copies them all, 55 of the 64 bytes a cycle that an SM gets.
+    const int64_t tiles = ((a.M + 127) / 128) * ((a.N + kI8Rows - 1) / kI8Rows);
+    if (a.M <= 128 || (a.M <= 512 && 2 * tiles <= dev.num_sms))
         return run_int8_stream<128>(a, s, dev);
     return a.y_fp32 ? run_widths<true>(a, s, dev) : run_widths<false>(a, s, dev);
 }
