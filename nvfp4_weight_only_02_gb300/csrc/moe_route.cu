@@ -14,7 +14,7 @@
 // time (lanes with equal experts rank themselves by match), counts are summed
 // over warps and CTAs, and the second pass places each slot.
 //
-// What bounds it.  16384 tokens, 8 of 256 experts: choosing 19 us (the integer
+// What bounds it.  16384 tokens, 8 of 256 experts: choosing 18 us (the integer
 // pipe), placing about 10 (the second kernel waits for each CTA's counts, 152 x
 // 256 of them read by every CTA), gradient 5 (bytes).  8192 tokens, 8 rows each of
 // 4096 in bf16: sum 96 us (93 % of the copy rate), its gradients 197 (85 %).
@@ -122,7 +122,7 @@ __device__ __forceinline__ void sort_keys(uint32_t (&v)[kPer])
 // round finds the largest head by a reduction over the warp and its lane by a
 // vote, and which expert a key was is looked up at the end, in as many turns as
 // a lane has choices (two or three).  The integer pipe bounds it (63 % of its
-// cycles): 16384 tokens with 8 of 256 experts take 19 us, 24 with rounds that look
+// cycles): 16384 tokens with 8 of 256 experts take 18 us, 24 with rounds that look
 // at all keys, as more experts or choices take.
 template <int kPer>
 __device__ __forceinline__ int choose(const uint32_t (&key)[kPer], int k, int lane, int *s_choice)
@@ -135,20 +135,23 @@ __device__ __forceinline__ int choose(const uint32_t (&key)[kPer], int k, int la
             for (int i = 0; i < kPer; i++)
                 v[i] = key[i];
             sort_keys<kPer>(v);
-            uint32_t head = v[0], taken = 0;   // taken: the lane's choices, four bits each
+            uint32_t u[kPer], taken = 0;   // what is left; the lane's choices, four bits each
+#pragma unroll
+            for (int i = 0; i < kPer; i++)
+                u[i] = v[i];
             int n = 0, found = 0;
             for (int j = 0; j < k; j++) {
-                const uint32_t top = __reduce_max_sync(kAll, head);
+                const uint32_t top = __reduce_max_sync(kAll, u[0]);
                 if (top == 0)
                     break;
                 found++;
-                if (lane == __ffs(__ballot_sync(kAll, head == top)) - 1) {
+                if (lane == __ffs(__ballot_sync(kAll, u[0] == top)) - 1) {
                     taken |= (uint32_t)j << (4 * n);
                     n++;
-                    head = 0;
 #pragma unroll
-                    for (int i = 1; i < kPer; i++)
-                        head = n == i ? v[i] : head;
+                    for (int i = 0; i + 1 < kPer; i++)
+                        u[i] = u[i + 1];
+                    u[kPer - 1] = 0;
                 }
             }
             uint32_t used = 0;
@@ -229,10 +232,8 @@ __device__ __forceinline__ void load_logits(const RouteParams &p, int64_t t, int
 
 // One token by one warp, kPer experts a lane.
 template <int kPer, bool kF32>
-__device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, int lane, int *s_choice)
+__device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, const float (&z)[kPer], int lane, int *s_choice)
 {
-    float z[kPer];
-    load_logits<kPer, kF32>(p, t, lane * kPer, z);
     bool nan = false;   // the softmax of the row has no value
 #pragma unroll
     for (int i = 0; i < kPer; i++)
@@ -283,25 +284,43 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, int
     }
 }
 
-// The tokens t0, t0 + step, ... below t1.
+// The tokens t0, t0 + step, ... below t1; up to eight experts a lane the next one's logits are on their way meanwhile.
+template <int kPer, bool kF32>
+__device__ __forceinline__ void route_run(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, int *s_choice)
+{
+    constexpr bool kAhead = kPer <= 8;
+    float z[kPer], next[kAhead ? kPer : 1];
+    if constexpr (kAhead) {
+        if (t0 < t1)
+            load_logits<kPer, kF32>(p, t0, lane * kPer, next);
+    }
+    for (int64_t t = t0; t < t1; t += step) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < kPer; i++)
+                z[i] = next[i];
+            if (t + step < t1)
+                load_logits<kPer, kF32>(p, t + step, lane * kPer, next);
+        } else {
+            load_logits<kPer, kF32>(p, t, lane * kPer, z);
+        }
+        route_token<kPer, kF32>(p, t, z, lane, s_choice);
+    }
+}
+
 template <bool kF32>
 __device__ __forceinline__ void route_tokens(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, int *s_choice)
 {
     if (p.E <= 64)
-        for (int64_t t = t0; t < t1; t += step)
-            route_token<2, kF32>(p, t, lane, s_choice);
+        route_run<2, kF32>(p, t0, t1, step, lane, s_choice);
     else if (p.E <= 128)
-        for (int64_t t = t0; t < t1; t += step)
-            route_token<4, kF32>(p, t, lane, s_choice);
+        route_run<4, kF32>(p, t0, t1, step, lane, s_choice);
     else if (p.E <= 256)
-        for (int64_t t = t0; t < t1; t += step)
-            route_token<8, kF32>(p, t, lane, s_choice);
+        route_run<8, kF32>(p, t0, t1, step, lane, s_choice);
     else if (p.E <= 512)
-        for (int64_t t = t0; t < t1; t += step)
-            route_token<16, kF32>(p, t, lane, s_choice);
+        route_run<16, kF32>(p, t0, t1, step, lane, s_choice);
     else
-        for (int64_t t = t0; t < t1; t += step)
-            route_token<32, kF32>(p, t, lane, s_choice);
+        route_run<32, kF32>(p, t0, t1, step, lane, s_choice);
 }
 
 // Calls f(slot, expert, rank) for the slots of this warp's run in groups of
