@@ -934,24 +934,25 @@ class MoePlan:
     offsets (E + 1): rows offsets[e] .. offsets[e + 1] - 1 are expert e's; order (T k): slot of each row, -1 behind the
     last one; position (T, k): row of each slot, -1 without an expert."""
 
-    __slots__ = ("T", "k", "E", "rows", "padded_rows", "nbytes", "buffer", "index", "_at")
+    __slots__ = ("T", "k", "E", "rows", "padded_rows", "nbytes", "buffer", "index", "_sizes")
 
     def __init__(self, T, k, E, device, index):
-        self.nbytes, *self._at, self.padded_rows = _moe_sizes(T, k, E)
+        self._sizes = sizes = _moe_sizes(T, k, E)
+        self.nbytes, self.padded_rows = sizes[0], sizes[4]
         self.T, self.k, self.E, self.rows, self.index = T, k, E, T * k, index
-        self.buffer = torch.empty(self.nbytes // 4, dtype=torch.int32, device=device)
+        self.buffer = torch.empty(sizes[0] // 4, dtype=torch.int32, device=device)
 
     @property
     def offsets(self):
-        return self.buffer.as_strided((self.E + 1,), (1,), self._at[0])
+        return self.buffer.as_strided((self.E + 1,), (1,), self._sizes[1])
 
     @property
     def order(self):
-        return self.buffer.as_strided((self.rows,), (1,), self._at[1])
+        return self.buffer.as_strided((self.rows,), (1,), self._sizes[2])
 
     @property
     def position(self):
-        return self.buffer.as_strided((self.T, self.k), (self.k, 1), self._at[2])
+        return self.buffer.as_strided((self.T, self.k), (self.k, 1), self._sizes[3])
 
 
 class MoeRouting:

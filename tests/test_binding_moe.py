@@ -21,7 +21,8 @@ def plan_sizes(monkeypatch):
 
 def plan(index=0):
     p = nv.MoePlan.__new__(nv.MoePlan)
-    p.nbytes, *p._at, p.padded_rows = nv._moe_sizes(T, k, E)
+    p._sizes = nv._moe_sizes(T, k, E)
+    p.nbytes, p.padded_rows = p._sizes[0], p._sizes[4]
     p.T, p.k, p.E, p.rows, p.index, p.buffer = T, k, E, T * k, index, Fake((1024,), i32, index)
     return p
 
