@@ -14,10 +14,11 @@
 // time (lanes with equal experts rank themselves by match), counts are summed
 // over warps and CTAs, and the second pass places each slot.
 //
-// What bounds it.  16384 tokens, 8 of 256 experts: choosing 18 us (the integer
-// pipe), placing about 10 (the second kernel waits for each CTA's counts, 152 x
-// 256 of them read by every CTA), gradient 5 (bytes).  8192 tokens, 8 rows each of
-// 4096 in bf16: sum 96 us (93 % of the copy rate), its gradients 197 (85 %).
+// What bounds it.  16384 tokens, 8 of 256 experts: 22 us, of which choosing 16
+// (instructions) and placing 6 (the second kernel waits for each CTA's counts,
+// 152 x 256 of them read by every CTA; 9 when a thread asked for few of them at a
+// time and for its slots afterwards); gradient 5 (bytes).  8192 tokens, 8 rows each
+// of 4096 in bf16: sum 96 us (93 % of the copy rate), its gradients 197 (85 %).
 #include <algorithm>
 
 #include "common.cuh"
@@ -85,91 +86,74 @@ __device__ __forceinline__ uint32_t key_of(float v)
     return v > -INFINITY ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : 0u;
 }
 
-__device__ __forceinline__ void order_pair(uint32_t &a, uint32_t &b)
-{
-    const uint32_t hi = max(a, b), lo = min(a, b);
-    a = hi;
-    b = lo;
-}
-
-// Descending, by exchanges of two instructions each.
-template <int kPer>
-__device__ __forceinline__ void sort_keys(uint32_t (&v)[kPer])
-{
-    if constexpr (kPer == 8) {
-        // odd-even merges: 19 exchanges
-        order_pair(v[0], v[1]), order_pair(v[2], v[3]), order_pair(v[4], v[5]), order_pair(v[6], v[7]);
-        order_pair(v[0], v[2]), order_pair(v[1], v[3]), order_pair(v[4], v[6]), order_pair(v[5], v[7]);
-        order_pair(v[1], v[2]), order_pair(v[5], v[6]);
-        order_pair(v[0], v[4]), order_pair(v[1], v[5]), order_pair(v[2], v[6]), order_pair(v[3], v[7]);
-        order_pair(v[2], v[4]), order_pair(v[3], v[5]);
-        order_pair(v[1], v[2]), order_pair(v[3], v[4]), order_pair(v[5], v[6]);
-    } else if constexpr (kPer == 4) {
-        order_pair(v[0], v[1]), order_pair(v[2], v[3]);
-        order_pair(v[0], v[2]), order_pair(v[1], v[3]);
-        order_pair(v[1], v[2]);
-    } else {
-        static_assert(kPer == 2, "2, 4 or 8 keys");
-        order_pair(v[0], v[1]);
-    }
-}
-
 // The k experts of the largest keys, in order; equal keys by index.  A lane has
 // kPer experts behind one another, so of equal keys the lowest lane's is first.
 // Returns lane j's choice j, -1 where there is none.
 //
-// Up to eight experts a lane and eight choices: the lane's keys are sorted, a
-// round finds the largest head by a reduction over the warp and its lane by a
-// vote, and which expert a key was is looked up at the end, in as many turns as
-// a lane has choices (two or three).  The integer pipe bounds it (63 % of its
-// cycles): 16384 tokens with 8 of 256 experts take 18 us, 24 with rounds that look
-// at all keys, as more experts or choices take.
+// Up to 16 choices: the k-th of the lanes' largest keys (each distinct one
+// counted once) is a bound that the k best reach and few others, about 9 keys for
+// k = 8 and 21 for k = 16 whatever E is, when experts are in no order.  Those that
+// reach it are collected, a lane each, and a key's place is the number of larger
+// ones.  Where more than 32 reach it, and for more choices, each round looks at
+// all keys.  Calls for 16384 tokens, 8 of 256, 8 of 512, 16 of 1024 experts: 25, 32
+// and 63 us; 44 for the 512 and 108 for the 1024 with rounds over all keys, 27 for
+// the 256 with each lane's keys sorted first.
+constexpr int kRtFew = 16;
+struct Candidates {
+    uint32_t key[32];
+    int expert[32];
+};
 template <int kPer>
-__device__ __forceinline__ int choose(const uint32_t (&key)[kPer], int k, int lane, int *s_choice)
+__device__ __forceinline__ int choose(const uint32_t (&key)[kPer], int k, int lane, Candidates &c)
 {
     int mine = -1;
-    if constexpr (kPer <= 8) {
-        if (k <= 8) {
-            uint32_t v[kPer];
+    if (k <= kRtFew) {
+        uint32_t head = key[0];
 #pragma unroll
-            for (int i = 0; i < kPer; i++)
-                v[i] = key[i];
-            sort_keys<kPer>(v);
-            uint32_t u[kPer], taken = 0;   // what is left; the lane's choices, four bits each
+        for (int i = 1; i < kPer; i++)
+            head = max(head, key[i]);
+        uint32_t bound = 0;
+        for (int j = 0; j < k; j++) {
+            bound = __reduce_max_sync(kAll, head);
+            if (bound == 0)
+                break;
+            head = head == bound ? 0u : head;
+        }
+        bound = max(bound, 1u);
+        int n = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; i++)
-                u[i] = v[i];
-            int n = 0, found = 0;
-            for (int j = 0; j < k; j++) {
-                const uint32_t top = __reduce_max_sync(kAll, u[0]);
-                if (top == 0)
-                    break;
-                found++;
-                if (lane == __ffs(__ballot_sync(kAll, u[0] == top)) - 1) {
-                    taken |= (uint32_t)j << (4 * n);
-                    n++;
+        for (int i = 0; i < kPer; i++)
+            n += key[i] >= bound;
+        // keys of the lanes before, and of all
+        int at = 0, all = 0;
 #pragma unroll
-                    for (int i = 0; i + 1 < kPer; i++)
-                        u[i] = u[i + 1];
-                    u[kPer - 1] = 0;
-                }
-            }
-            uint32_t used = 0;
+        for (int bit = 1; bit <= kPer; bit *= 2) {
+            const uint32_t has = __ballot_sync(kAll, n & bit);
+            at += bit * __popc(has & ((1u << lane) - 1u));
+            all += bit * __popc(has);
+        }
+        if (all <= 32) {
 #pragma unroll
-            for (int m = 0; m < kPer; m++) {
-                if (!__any_sync(kAll, n > m))
-                    break;
-                if (n > m) {
-                    int at = 0;
-#pragma unroll
-                    for (int i = kPer - 1; i >= 0; i--)
-                        at = key[i] == v[m] && !(used >> i & 1) ? i : at;
-                    used |= 1u << at;
-                    s_choice[taken >> (4 * m) & 15] = lane * kPer + at;
+            for (int i = 0; i < kPer; i++) {
+                if (key[i] >= bound) {
+                    c.key[at] = key[i];
+                    c.expert[at++] = lane * kPer + i;
                 }
             }
             __syncwarp();
-            mine = lane < found ? s_choice[lane] : -1;
+            const uint32_t own = lane < all ? c.key[lane] : 0u;
+            const int expert = lane < all ? c.expert[lane] : -1;
+            int place = 0;
+            for (int j = 0; j < all; j += 4) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)     // behind the last one: 0, above nothing
+                    place += __shfl_sync(kAll, own, j + i) + (j + i < lane) > own;
+            }
+            __syncwarp();
+            if (lane < all && place < k)
+                c.expert[place] = expert;
+            __syncwarp();
+            mine = lane < min(k, all) ? c.expert[lane] : -1;
             __syncwarp();
             return mine;
         }
@@ -232,7 +216,7 @@ __device__ __forceinline__ void load_logits(const RouteParams &p, int64_t t, int
 
 // One token by one warp, kPer experts a lane.
 template <int kPer, bool kF32>
-__device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, const float (&z)[kPer], int lane, int *s_choice)
+__device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, const float (&z)[kPer], int lane, Candidates &s_cand)
 {
     bool nan = false;   // the softmax of the row has no value
 #pragma unroll
@@ -266,7 +250,7 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, con
         for (int i = 0; i < kPer; i++)
             key[i] = key_of(z[i]);
     }
-    const int mine = choose<kPer>(key, p.k, lane, s_choice);
+    const int mine = choose<kPer>(key, p.k, lane, s_cand);
     const float zj = mine >= 0 ? load_z(p.z, kF32, t * p.ldz + mine) : -INFINITY;
     float w = 0.0f;
     if (p.renorm) {
@@ -286,7 +270,7 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int64_t t, con
 
 // The tokens t0, t0 + step, ... below t1; up to eight experts a lane the next one's logits are on their way meanwhile.
 template <int kPer, bool kF32>
-__device__ __forceinline__ void route_run(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, int *s_choice)
+__device__ __forceinline__ void route_run(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, Candidates &s_cand)
 {
     constexpr bool kAhead = kPer <= 8;
     float z[kPer], next[kAhead ? kPer : 1];
@@ -304,23 +288,23 @@ __device__ __forceinline__ void route_run(const RouteParams &p, int64_t t0, int6
         } else {
             load_logits<kPer, kF32>(p, t, lane * kPer, z);
         }
-        route_token<kPer, kF32>(p, t, z, lane, s_choice);
+        route_token<kPer, kF32>(p, t, z, lane, s_cand);
     }
 }
 
 template <bool kF32>
-__device__ __forceinline__ void route_tokens(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, int *s_choice)
+__device__ __forceinline__ void route_tokens(const RouteParams &p, int64_t t0, int64_t t1, int step, int lane, Candidates &s_cand)
 {
     if (p.E <= 64)
-        route_run<2, kF32>(p, t0, t1, step, lane, s_choice);
+        route_run<2, kF32>(p, t0, t1, step, lane, s_cand);
     else if (p.E <= 128)
-        route_run<4, kF32>(p, t0, t1, step, lane, s_choice);
+        route_run<4, kF32>(p, t0, t1, step, lane, s_cand);
     else if (p.E <= 256)
-        route_run<8, kF32>(p, t0, t1, step, lane, s_choice);
+        route_run<8, kF32>(p, t0, t1, step, lane, s_cand);
     else if (p.E <= 512)
-        route_run<16, kF32>(p, t0, t1, step, lane, s_choice);
+        route_run<16, kF32>(p, t0, t1, step, lane, s_cand);
     else
-        route_run<32, kF32>(p, t0, t1, step, lane, s_choice);
+        route_run<32, kF32>(p, t0, t1, step, lane, s_cand);
 }
 
 // Calls f(slot, expert, rank) for the slots of this warp's run in groups of
@@ -391,7 +375,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
     __shared__ int s_base[kMoeMaxExperts];          // row of the expert's first slot of this CTA
     __shared__ int s_off[kMoeMaxExperts + 1], s_fb[kMoeMaxExperts + 1], s_ft[kMoeMaxExperts + 1];
     __shared__ int s_warp[kRtWarps][3];
-    __shared__ int s_choice[kTopk ? kRtWarps : 1][8];
+    __shared__ Candidates s_cand[kTopk ? kRtWarps : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x, warps = threads >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
     const int64_t c0 = t0 * p.k, c1 = max(c0, t1 * p.k);    // the CTA's slots
@@ -399,12 +383,17 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
     pdl_launch_dependents();
     pdl_wait();
     int total = 0, before = 0;
+    int expert = -1, rank = 0;      // of the thread's next slot
+    if (!kFirst && c0 + tid < c1) {
+        expert = p.experts[c0 + tid];
+        rank = position[c0 + tid];
+    }
     if (kFirst) {
         if constexpr (kTopk) {
             if (p.z_fp32)
-                route_tokens<true>(p, t0 + warp, t1, warps, lane, s_choice[warp]);
+                route_tokens<true>(p, t0 + warp, t1, warps, lane, s_cand[warp]);
             else
-                route_tokens<false>(p, t0 + warp, t1, warps, lane, s_choice[warp]);
+                route_tokens<false>(p, t0 + warp, t1, warps, lane, s_cand[warp]);
         }
         uint16_t *hist = s_hist + warp * p.E;
         for (int i = lane; i < p.E; i += 32)
@@ -447,18 +436,25 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
         if (!kSecond)
             return;
     } else {
-        // counts of all CTAs; the threads share out the CTAs where there are few experts
+        // counts of all CTAs, 16 a thread on their way at once; the threads share out the CTAs where there are few experts
         __shared__ int s_before[kMoeMaxExperts], s_total[kMoeMaxExperts];
         s_before[tid] = s_total[tid] = 0;   // 1024 threads
         __syncthreads();
         const int width = (p.E + 31) / 32 * 32, groups = threads / width, g = tid / width, e = tid % width;
         if (g < groups && e < p.E) {
             int b = 0, all = 0;
-#pragma unroll 16
-            for (int c = g; c < (int)gridDim.x; c += groups) {
-                const int v = counts[(int64_t)c * p.E + e];
-                all += v;
-                b += c < (int)blockIdx.x ? v : 0;
+            for (int first = g; first < (int)gridDim.x; first += 16 * groups) {
+                int v[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int c = first + i * groups;
+                    v[i] = c < (int)gridDim.x ? counts[(int64_t)c * p.E + e] : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    all += v[i];
+                    b += first + i * groups < (int)blockIdx.x ? v[i] : 0;
+                }
             }
             atomicAdd(&s_before[e], b);
             atomicAdd(&s_total[e], all);
@@ -510,10 +506,19 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
     for (int64_t r = rows + (int64_t)blockIdx.x * threads + tid; r < p.slots; r += (int64_t)gridDim.x * threads)
         p.plan[p.order + r] = -1;
     // places; in one CTA each thread meets the ranks that another warp wrote before the last barriers
+    if (kFirst && c0 + tid < c1) {
+        expert = p.experts[c0 + tid];
+        rank = position[c0 + tid];
+    }
     for (int64_t s = c0 + tid; s < c1; s += threads) {
-        int e = p.experts[s], pos = -1, pad = -1;
+        const int e = expert, r = rank;
+        int pos = -1, pad = -1;
+        if (s + threads < c1) {
+            expert = p.experts[s + threads];
+            rank = position[s + threads];
+        }
         if (e >= 0 && e < p.E) {
-            pos = s_base[e] + position[s];
+            pos = s_base[e] + r;
             pad = s_fb[e] * kMoeBlock + pos - s_off[e];
             p.plan[p.order + pos] = (int32_t)s;
         }

@@ -109,6 +109,27 @@ def test_rows_that_leave_little(nv):
     assert nv.moe_route(torch.tensor([[9.0, 1.0, 0.0]], device="cuda"), 3, bias=b).experts.tolist() == [[1, 2, -1]]
 
 
+@pytest.mark.parametrize("E", [40, 64, 100, 128, 256, 300, 512, 1024])
+@pytest.mark.parametrize("k", [1, 6, 8, 16, 17, 32])
+def test_orders_of_experts(nv, E, k):
+    """Logits in ascending and descending order (the best in few lanes), equal ones, few distinct ones, and a largest
+    value that 31 to 34 experts share: the choice is that of a stable sort."""
+    g = _gen(E + k)
+    up = torch.arange(E, device="cuda", dtype=F32)
+    rows = [up, -up, torch.zeros_like(up), up // 3, -(up // 5), up % 7]
+    for n in (31, 32, 33, 34):
+        row = torch.randn(E, device="cuda", generator=g).clamp_(max=2.0)
+        row[torch.randperm(E, device="cuda", generator=g)[:n]] = 3.0
+        rows.append(row)
+    z = torch.cat([torch.stack(rows), torch.randn(40, E, device="cuda", generator=g).mul_(3).round_()])
+    want = torch.argsort(z, dim=1, descending=True, stable=True)[:, :k].int()
+    r = nv.moe_route(z, k)
+    assert torch.equal(r.experts, want)
+    _same_plan(r.plan, want)
+    assert torch.equal(nv.moe_route(z, k, scoring="sigmoid", bias=-z.new_full((E,), float("inf"))).experts,
+                       torch.full_like(want, -1))
+
+
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (7, 3, 2), (1000, 1, 5), (700, 4, 1000), (5000, 8, 60),
                                    (40000, 2, 17)])
 @pytest.mark.parametrize("how", ["random", "one", "twice", "dropped"])
