@@ -18,7 +18,7 @@
 // (instructions) and placing 6 (the second kernel waits for each CTA's counts,
 // 152 x 256 of them read by every CTA; 9 when a thread asked for few of them at a
 // time and for its slots afterwards); gradient 5 (bytes).  8192 tokens, 8 rows each
-// of 4096 in bf16: sum 96 us (93 % of the copy rate), its gradients 197 (85 %).
+// of 4096 in bf16: sum 92 us (96 % of the copy rate), its gradients 175 (97 %).
 #include <algorithm>
 
 #include "common.cuh"
@@ -653,6 +653,7 @@ __device__ __forceinline__ void load_vec(const T *src, float (&v)[kVec])
     }
 }
 
+// Rows that are written once: evicted first.
 template <typename T, int kVec>
 __device__ __forceinline__ void store_vec(T *dst, const float (&v)[kVec])
 {
@@ -669,13 +670,13 @@ __device__ __forceinline__ void store_vec(T *dst, const float (&v)[kVec])
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
         if constexpr (kVec == 8)
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
         else
             *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; i += 4)
-            *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            __stcs(reinterpret_cast<float4 *>(dst + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
     }
 }
 
@@ -774,22 +775,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p)
 }
 
 // dy[position[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[position[t][j]]>: a CTA a token, dout read once for
-// eight slots.
-template <typename T, int kVec>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const CombineParams p)
+// kRows slots, whose rows of y are on their way while the rows of dy are written.  Registers for that many loads and
+// CTAs for the rest: bounds of 3 (bf16, eight rows), 5 (four), 4 and 6 (FP32).  8192 tokens of 4096 in bf16, eight
+// rows each: 170 us (187 with loads as they are used, in 40 registers), four rows 92 (105); bounds of 2 and 4: 177, 183.
+template <typename T, int kVec, int kRows>
+__global__ void __launch_bounds__(256, kVec == 8 ? (kRows == 8 ? 3 : 5)
+                                             : kVec == 4 ? (kRows == 8 ? 4 : 6) : 1) combine_grad_kernel(const CombineParams p)
 {
-    __shared__ float s_part[8][kCbRows];
+    __shared__ float s_part[8][kRows];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
     const T *dout = reinterpret_cast<const T *>(p.dout) + t * p.N, *y = reinterpret_cast<const T *>(p.y);
     T *dy = reinterpret_cast<T *>(p.dy);
-    for (int j0 = 0; j0 < p.k; j0 += kCbRows) {
-        float dot[kCbRows], w[kCbRows];
-        int pos[kCbRows];
+    for (int j0 = 0; j0 < p.k; j0 += kRows) {
+        float dot[kRows], w[kRows];
+        int pos[kRows];
 #pragma unroll
-        for (int j = 0; j < kCbRows; j++) {
+        for (int j = 0; j < kRows; j++) {
             dot[j] = 0.0f;
             pos[j] = j0 + j < p.k ? p.position[t * p.k + j0 + j] : -1;
             w[j] = pos[j] >= 0 ? p.weights[t * p.k + j0 + j] : 0.0f;
@@ -797,23 +801,18 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const CombineParams p
         for (int c = tid * kVec; c < p.N; c += blockDim.x * kVec) {
             float d[kVec];
             load_vec<T, kVec>(dout + c, d);
+            Vec<T, kVec> v[kRows];
             if (p.dw) {
-                Vec<T, kVec> v[kCbRows];
 #pragma unroll
-                for (int j = 0; j < kCbRows; j++) {
+                for (int j = 0; j < kRows; j++) {
                     v[j].zero();
                     if (pos[j] >= 0)
                         v[j].load(y + (int64_t)pos[j] * p.N + c);
                 }
-#pragma unroll
-                for (int j = 0; j < kCbRows; j++)
-#pragma unroll
-                    for (int e = 0; e < kVec; e++)
-                        dot[j] = fmaf(d[e], v[j].get(e), dot[j]);
             }
-            if (dy) {
+            if (dy) {   // while y's rows are on their way
 #pragma unroll
-                for (int j = 0; j < kCbRows; j++) {
+                for (int j = 0; j < kRows; j++) {
                     if (pos[j] >= 0) {
                         float o[kVec];
 #pragma unroll
@@ -823,17 +822,24 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const CombineParams p
                     }
                 }
             }
+            if (p.dw) {
+#pragma unroll
+                for (int j = 0; j < kRows; j++)
+#pragma unroll
+                    for (int e = 0; e < kVec; e++)
+                        dot[j] = fmaf(d[e], v[j].get(e), dot[j]);
+            }
         }
         if (p.dw) {
 #pragma unroll
-            for (int j = 0; j < kCbRows; j++) {
+            for (int j = 0; j < kRows; j++) {
                 // a slot without an expert adds nothing, whatever dout holds
                 const float s = warp_sum(pos[j] >= 0 ? dot[j] : 0.0f);
                 if (lane == 0)
                     s_part[warp][j] = s;
             }
             __syncthreads();
-            if (tid < kCbRows && j0 + tid < p.k) {
+            if (tid < kRows && j0 + tid < p.k) {
                 float s = 0.0f;
                 for (int i = 0; i < warps; i++)
                     s += s_part[i][tid];
@@ -865,13 +871,14 @@ cudaError_t run_combine(const MoeCombineArgs &a, const CombineParams &p, cudaStr
                    : launch_dependent(combine_kernel<TY, TO, 1>, grid, threads, 0, s, p);
 }
 
-template <typename T>
+template <typename T, int kRows>
 cudaError_t run_combine_grad(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
 {
     constexpr int kVec = 16 / sizeof(T);
     const dim3 grid((unsigned)a.T);
-    return a.N % kVec == 0 ? launch_dependent(combine_grad_kernel<T, kVec>, grid, combine_threads(a.N, kVec), 0, s, p)
-                           : launch_dependent(combine_grad_kernel<T, 1>, grid, combine_threads(a.N, 1), 0, s, p);
+    return a.N % kVec == 0
+               ? launch_dependent(combine_grad_kernel<T, kVec, kRows>, grid, combine_threads(a.N, kVec), 0, s, p)
+               : launch_dependent(combine_grad_kernel<T, 1, kRows>, grid, combine_threads(a.N, 1), 0, s, p);
 }
 
 CombineParams combine_params(const MoeCombineArgs &a)
@@ -976,7 +983,9 @@ cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t s)
 cudaError_t launch_moe_combine_backward(const MoeCombineArgs &a, cudaStream_t s)
 {
     const CombineParams p = combine_params(a);
-    return a.y_fp32 ? run_combine_grad<float>(a, p, s) : run_combine_grad<__nv_bfloat16>(a, p, s);
+    if (a.k <= 4)
+        return a.y_fp32 ? run_combine_grad<float, 4>(a, p, s) : run_combine_grad<__nv_bfloat16, 4>(a, p, s);
+    return a.y_fp32 ? run_combine_grad<float, 8>(a, p, s) : run_combine_grad<__nv_bfloat16, 8>(a, p, s);
 }
 
 }  // namespace nvfp4
