@@ -17,11 +17,12 @@
 //     stored as a hi + lo pair of bf16 (2^-16 relative), pre-multiplied by
 //     rho = s / s_t when the LoRA term shares the accumulator with the
 //     weights' term (see below);
-//   * the GEMM: TMA brings 128 x 64 tiles of X'' and 256 x 64 tiles of W into
-//     a 4-deep ring (128-byte swizzle); one thread issues tcgen05.mma
-//     kind::f16 with bf16 operands over K, then one or two extra K-steps of
-//     MMAs of [T'' hi | T'' lo] against [B | B].  Two 128 x 256 fp32
-//     accumulators in TMEM (512 columns).
+//   * the GEMM, on CTA pairs: TMA brings 128 x 64 tiles of X'' and half of the
+//     pair's 256 x 64 tile of W into each CTA's 6-deep ring (128-byte swizzle);
+//     one thread of the pair issues tcgen05.mma kind::f16 (256 x 256) with bf16
+//     operands over K, then one or two extra K-steps of MMAs of [T'' hi | T'' lo]
+//     against [B | B].  Two 128 x 256 fp32 accumulators in each CTA's TMEM (512
+//     columns).
 // Fused mode (2^-40 <= |s / s_t| <= 2^40, every practical case): the extra
 // K-steps go into the same accumulator, acc = X' 2^-p W^T/s_t + rho T'' B^T,
 // Y = s_t 2^p_m acc, and the epilogue of one tile overlaps the next tile's
@@ -30,9 +31,9 @@
 // the second TMEM accumulator and the epilogue forms
 // s_t 2^p_m acc_W + s 2^p_m acc_T, each factor applied as mantissa times an
 // exact power of two, so any finite s_t works; one tile at a time.
-// Roles in a block of 6 warps (persistent over 128 x 256 output tiles):
+// Roles in a block of 6 warps (a pair is persistent over 256 x 256 output tiles):
 //   warps 0-3  epilogue (one TMEM lane = one output row per thread);
-//   warp 4     TMA producer;  warp 5  TMEM allocation and MMA issue.
+//   warp 4     TMA producer;  warp 5  TMEM allocation and (pair leader) MMA issue.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -41,6 +42,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
+#include "w4a4_pair.cuh"
 
 namespace nvfp4 {
 
@@ -49,12 +51,12 @@ using namespace sm100;
 constexpr int kPfBM = 128;         // tokens per tile
 constexpr int kPfBN = 256;         // weight rows per tile
 constexpr int kPfBK = 64;          // K per stage (128 bytes of bf16)
-constexpr int kPfStages = 4;
+constexpr int kPfStages = 6;
 constexpr int kPfThreads = 192;
 constexpr int kPfGroupN = 16;      // tile raster: n-tiles per group (W rows kept in L2 while X'' streams)
 constexpr int kPfMaxR = 64;
 constexpr uint32_t kPfABytes = kPfBM * kPfBK * 2;  // 16 KB
-constexpr uint32_t kPfBBytes = kPfBN * kPfBK * 2;  // 32 KB
+constexpr uint32_t kPfBBytes = kPfBN / 2 * kPfBK * 2;  // 16 KB: a CTA of the pair holds half of a weight tile
 constexpr size_t kPfSmem = 1024 + kPfStages * (kPfABytes + kPfBBytes) + 256;
 
 struct PrefillParams {
@@ -785,39 +787,41 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem;
     uint8_t *sB = smem + kPfStages * kPfABytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sB + kPfStages * kPfBBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sB + kPfStages * kPfBBytes);   // the leader's: both CTAs' copies
     uint64_t *empty = full + kPfStages;
     uint64_t *acc_full = empty + kPfStages;
-    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *acc_empty = acc_full + 2;                                          // the leader's: both epilogues
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    volatile uint32_t *s_loaded = s_tmem + 2, *s_issued = s_tmem + 3;            // stages copied and multiplied
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPfStages; s++) {
             mbar_init(&full[s], 1);   // TMA producer (with tx bytes)
-            mbar_init(&empty[s], 2);  // tcgen05.commit of both CTAs of the pair
+            mbar_init(&empty[s], 1);  // tcgen05.commit of the pair
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], 2 * 4);
         }
         *s_abort = 0;
+        *s_loaded = 0;
+        *s_issued = 0;
         mbar_fence_init();
     }
-    if (warp == 5) {
-        tmem_alloc(s_tmem, 512);
-        tmem_relinquish();
-    }
+    if (warp == 5)
+        tmem_alloc_pair(s_tmem, 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers and TMEM before anything of the pair touches them
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    cluster_sync();  // the peer's barriers are initialised before any copy targets them
     pdl_wait();      // X'', p_m, T'', W and B from the preparation kernels
 
     // CTA pairs (clusters of 2) take pairs of row tiles that share a weight
-    // tile: each CTA copies half of the B tile and multicasts it to both
+    // tile: each CTA copies its row tile and half of the weight tile, and the
+    // pair's MMA reads both halves where they are
     const int crank = (int)cluster_ctarank(), cid = (int)cluster_id_x(), ncl = (int)cluster_count_x();
     const int mpairs = (p.mtiles + 1) / 2, npairs = mpairs * p.ntiles;
     const int KB = p.K / kPfBK, KS = KB + p.ES;
@@ -829,7 +833,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
     if (warp == 4) {
         // ---------------- TMA producer: X' and W tiles, then the LoRA extension
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t it = 0;
             for (int pt = cid; pt < npairs && !*s_abort; pt += ncl) {
                 int mp, nt;
@@ -844,48 +848,56 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     }
                     mx = copy ? &tmap_x : &tmap_xd;
                 }
+                const int by = nt * kPfBN + crank * (kPfBN / 2);
                 for (int ks = 0; ks < KS; ks++, it++) {
                     const int st = it % kPfStages;
-                    const uint32_t ph = (it / kPfStages) & 1;
-                    if (!mbar_wait(&empty[st], ph ^ 1)) { fail(); break; }
-                    mbar_arrive_expect_tx(&full[st], kPfABytes + kPfBBytes);
-                    // the stage is free in both CTAs (empty counts both commits)
-                    uint8_t *bh = sB + st * kPfBBytes + crank * (kPfBBytes / 2);
-                    const int by = nt * kPfBN + crank * (kPfBN / 2);
+                    if (!mbar_wait(&empty[st], ((it / kPfStages) & 1) ^ 1)) {
+                        fail();
+                        break;
+                    }
+                    const uint32_t bar = cluster_addr(&full[st], 0);
+                    if (crank == 0)
+                        mbar_arrive_expect_tx(&full[st], 2 * (kPfABytes + kPfBBytes));
                     if (ks < KB) {
-                        tma_load_2d(sA + st * kPfABytes, mx, &full[st], ks * kPfBK, mt * kPfBM);
-                        tma_load_2d_mc(bh, &tmap_wh, &full[st], ks * kPfBK, by, 3);
+                        tma_load_2d_pair(sA + st * kPfABytes, mx, bar, ks * kPfBK, mt * kPfBM);
+                        tma_load_2d_pair(sB + st * kPfBBytes, &tmap_wh, bar, ks * kPfBK, by);
                     } else {
-                        tma_load_2d(sA + st * kPfABytes, &tmap_ta, &full[st], (ks - KB) * kPfBK, mt * kPfBM);
-                        tma_load_2d_mc(bh, &tmap_tbh, &full[st], (ks - KB) * kPfBK, by, 3);
+                        tma_load_2d_pair(sA + st * kPfABytes, &tmap_ta, bar, (ks - KB) * kPfBK, mt * kPfBM);
+                        tma_load_2d_pair(sB + st * kPfBBytes, &tmap_tbh, bar, (ks - KB) * kPfBK, by);
                     }
                 }
             }
-            // every stage released by both CTAs before leaving: the peer's
-            // last commits must not arrive after this CTA has exited
+            // every stage released before leaving: the leader's commits must
+            // not arrive at a CTA that is gone
             for (int k = 0; k < kPfStages && !*s_abort; k++) {
                 const uint32_t i2 = it + k;
                 if (i2 >= (uint32_t)kPfStages && !mbar_wait(&empty[i2 % kPfStages], ((i2 / kPfStages) & 1) ^ 1))
                     fail();
             }
+            *s_loaded = it;
         }
     } else if (warp == 5) {
-        // ---------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f16(kPfBM, kPfBN, 1);  // bf16 x bf16, fp32 accumulate
+        // ---------------- MMA issue, by one thread of the pair's leader
+        if (crank == 0 && elect_one()) {
+            constexpr uint32_t idesc = idesc_f16(2 * kPfBM, kPfBN, 1);  // bf16 x bf16, fp32 accumulate
             const bool split = p.ES > 0 && !lora_fused(p.lora_scale, *p.tensor_scale);
             uint32_t it = 0, lt = 0;
             for (int pt = cid; pt < npairs && !*s_abort; pt += ncl, lt++) {
                 // split: accumulator 0 takes the weights' term, 1 the LoRA term
                 const int buf = split ? 0 : lt & 1;
                 const uint32_t aph = split ? lt & 1 : (lt >> 1) & 1;
-                if (!mbar_wait(&acc_empty[buf], aph ^ 1)) { fail(); break; }
+                if (!mbar_wait(&acc_empty[buf], aph ^ 1)) {
+                    fail();
+                    break;
+                }
                 tc_fence_after();
                 bool ok = true;
                 for (int ks = 0; ks < KS; ks++, it++) {
                     const int st = it % kPfStages;
-                    const uint32_t ph = (it / kPfStages) & 1;
-                    if (!mbar_wait(&full[st], ph)) { ok = false; break; }
+                    if (!mbar_wait(&full[st], (it / kPfStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
                     const uint64_t ad = smem_desc_sw128(smem_addr(sA + st * kPfABytes));
                     const uint64_t bd = smem_desc_sw128(smem_addr(sB + st * kPfBBytes));
@@ -894,26 +906,35 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     const int kk = split && ext ? ks - KB : ks;   // 0: start a fresh accumulation
 #pragma unroll
                     for (int j = 0; j < kPfBK / 16; j++)
-                        mma_f16_ss(d, ad + 2 * j, bd + 2 * j, idesc, (kk | j) != 0);
-                    mma_commit_mc(&empty[st], 3);
+                        mma_f16_pair(d, ad + 2 * j, bd + 2 * j, idesc, (kk | j) != 0);
+                    mma_commit_pair(&empty[st]);
+                    if (ks + 1 == KS)
+                        mma_commit_pair(&acc_full[buf]);
                 }
-                if (!ok) { fail(); break; }
-                mma_commit(&acc_full[buf]);
+                if (!ok) {
+                    fail();
+                    break;
+                }
             }
+            *s_issued = it;
         }
     } else {
         // ---------------- epilogue: warps 0-3, one accumulator row per thread
         const int row = warp * 32 + lane;
         const float s_t = *p.tensor_scale;
         const bool split = p.ES > 0 && !lora_fused(p.lora_scale, s_t);
+        const uint32_t bar0 = cluster_addr(&acc_empty[0], 0), bar1 = cluster_addr(&acc_empty[1], 0);
         uint32_t lt = 0;
-        for (int pt = cid; pt < npairs && !*s_abort; pt += ncl, lt++) {
+        for (int pt = cid; pt < npairs && !__any_sync(0xffffffffu, *s_abort); pt += ncl, lt++) {
             int mp, nt;
             tile_coords(pt, mpairs, p.ntiles, mp, nt);
             const int mt = 2 * mp + crank;
             const int buf = split ? 0 : lt & 1;
             const uint32_t aph = split ? lt & 1 : (lt >> 1) & 1;
-            if (!mbar_wait(&acc_full[buf], aph)) { fail(); break; }
+            if (!mbar_wait_warp(&acc_full[buf], aph)) {
+                fail();
+                break;
+            }
             tc_fence_after();
             const int m = mt * kPfBM + row;
             const bool mrow = m < p.M;
@@ -925,6 +946,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             for (int cc = 0; cc < kPfBN / 32; cc++) {
                 const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
                 uint32_t v[32];
+                __syncwarp();   // the stores before may have parted the warp
                 tmem_ld32(lane_base + buf * kPfBN + cc * 32, v);
                 float yv[32];
                 if (split) {
@@ -983,16 +1005,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&acc_empty[buf]);
+                mbar_arrive_cluster(buf ? bar1 : bar0);
         }
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // neither CTA leaves while the other may still copy into it
+    if (crank == 0 && warp == 5 && *s_abort) {
+        // after a wait that gave up: copies on their way land, and MMAs issued are done, before either CTA leaves
+        const uint32_t loaded = *s_loaded, issued = *s_issued;
+        ring_drain(full, kPfStages, loaded > (uint32_t)kPfStages ? loaded - kPfStages : 0u, loaded);
+        if (issued > 0)
+            ring_drain(empty, kPfStages, issued - 1, issued);
+        __syncwarp();
+    }
+    cluster_sync();  // neither CTA leaves while the other may still signal or read it
     if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 

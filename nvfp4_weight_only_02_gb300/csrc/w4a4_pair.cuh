@@ -1,6 +1,6 @@
 // w4a4_pair.cuh -- what the 4-bit products on CTA pairs share (gemm_w4a4_tile.cu,
-// gemm_moe.cu): shared memory and TMEM of a tile, and the wrappers of the
-// instructions that work on both CTAs of a pair.
+// gemm_moe.cu): shared memory and TMEM of a tile; and for all products on pairs
+// the wrappers of the instructions that work on both CTAs.
 #pragma once
 
 #include "common.cuh"
@@ -121,6 +121,17 @@ __device__ __forceinline__ void mma_fp4_pair(uint32_t d_tmem, uint64_t a_desc, u
                 d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
             : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T over 16 elements of K, f16 or bf16 operands.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // One arrival on the barrier at bar's offset in both CTAs when the MMAs (and
