@@ -528,6 +528,15 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
 }
 
 // dz of the router, a warp a token.
+//
+// With u = w / scale, a softmax over the taken ones (j among them), dl_i = w_i (dw_i -
+// sum_j u_j dw_j): with a weight near 1, or dw that share an offset, the difference
+// cancels (logits 14, 0, -1, -2: the largest one's gradient off by 3 %).  So the dw
+// of the largest weight, r, is taken off all of them first, d = dw - dw_r; then
+//     dl_i = w_i (d_i - sum_j u_j d_j),
+// whose sum is all that r has and which cancels k-fold at most for the others.  With
+// scores over all experts, of which A are taken and B = 1 - A are not (each summed by
+// itself), dl_i = w_i (A d_i + B dw_i - sum_j u_j d_j).
 struct RouteGradParams {
     const void *z;
     int z_fp32;
@@ -541,6 +550,55 @@ struct RouteGradParams {
     int64_t lddz;
 };
 
+__device__ __forceinline__ void put_dz(const RouteGradParams &p, int64_t at, float v)
+{
+    if (p.z_fp32)
+        reinterpret_cast<float *>(p.dz)[at] = v;
+    else
+        reinterpret_cast<__nv_bfloat16 *>(p.dz)[at] = __float2bfloat16_rn(v);
+}
+
+// A row whose scores are a softmax over all experts, lane, lane + 32, ... of them a
+// lane's.  e, w, dw: this lane's slot (e < 0: none); d, sum as above; own = w dw.
+template <int kPer>
+__device__ __forceinline__ void softmax_grad(const RouteGradParams &p, int64_t t, int lane, int e, float w, float dw, float d,
+                                             float sum, float own)
+{
+    uint32_t taken = 0;
+    for (int j = 0; j < p.k; j++) {
+        const int apart = __shfl_sync(kAll, e, j) - lane;   // no expert: not a multiple of 32 apart, or below 0
+        taken |= apart >= 0 && (apart & 31) == 0 ? 1u << (apart >> 5) : 0u;
+    }
+    float s[kPer], zmax = -INFINITY, in = 0.0f, out = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kPer; u++) {
+        const int i = lane + 32 * u;
+        s[u] = i < p.E ? load_z(p.z, p.z_fp32, t * p.ldz + i) : -INFINITY;
+        zmax = fmaxf(zmax, s[u]);
+    }
+    zmax = warp_max(zmax);
+#pragma unroll
+    for (int u = 0; u < kPer; u++) {
+        s[u] = s[u] == -INFINITY ? 0.0f : expf(s[u] - zmax);
+        in += taken >> u & 1u ? s[u] : 0.0f;
+        out += taken >> u & 1u ? 0.0f : s[u];
+    }
+    in = warp_sum(in);
+    out = warp_sum(out);
+    const float denom = in + out, dot = warp_sum(own), share = dot / denom;
+#pragma unroll
+    for (int u = 0; u < kPer; u++) {
+        const int i = lane + 32 * u;
+        if (i < p.E)
+            put_dz(p, t * p.lddz + i, dot != dot ? dot : s[u] == 0.0f ? 0.0f : -s[u] * share);
+    }
+    __syncwarp();   // the chosen ones over what their lanes' neighbours wrote
+    if (e >= 0)
+        put_dz(p, t * p.lddz + e, dot != dot ? dot : w * ((in * d + out * dw) / denom - sum));
+}
+
+// kPer: experts a lane where the scores are a softmax over all of them, else 0.
+template <int kPer>
 __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p)
 {
     const int lane = threadIdx.x & 31;
@@ -550,71 +608,48 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
     if (t >= p.T)
         return;
     int e = -1;
-    float w = 0.0f, dw = 0.0f, g = 0.0f;
+    float w = 0.0f, dw = 0.0f;
     if (lane < p.k) {
         e = p.experts[t * p.k + lane];
-        if (e >= p.E)
+        if (e >= p.E || e < 0)
             e = -1;
         w = p.weights[t * p.k + lane];
         dw = p.dw[t * p.k + lane];
     }
     const bool none = e < 0;
-    const bool softmax_all = !p.sigmoid && !p.renorm;
     // a NaN weight reaches the gradient of its row, an unused slot's dw does not
-    const float dot = p.renorm || softmax_all ? warp_sum(none ? w * 0.0f : w * dw) : 0.0f;
-    if (!none) {
-        if (p.renorm) {
-            // w = scale u: scale u (dw - sum u dw) = w dw - w (sum w dw) / scale
-            g = w * (dw - (p.scale != 0.0f ? dot / p.scale : 0.0f));
-            if (p.sigmoid)
-                g *= sigmoid(-load_z(p.z, p.z_fp32, t * p.ldz + e));
-        } else if (p.sigmoid) {
-            g = w * dw * sigmoid(-load_z(p.z, p.z_fp32, t * p.ldz + e));
-        } else {
-            g = w * dw;
-        }
+    const float own = none ? w * 0.0f : w * dw;
+    float d = dw, sum = 0.0f;
+    bool nan = false;
+    if (p.renorm || kPer > 0) {
+        const uint32_t size = none ? 0u : __float_as_uint(fabsf(w));
+        const int r = __ffs(__ballot_sync(kAll, size == __reduce_max_sync(kAll, size))) - 1;
+        const float dr = __shfl_sync(kAll, dw, r);
+        d = lane == r ? 0.0f : dw - dr;
+        sum = warp_sum(none || lane == r ? 0.0f : w * d);
+        sum = p.scale != 0.0f ? sum / p.scale : 0.0f;
+        nan = __any_sync(kAll, own != own);
     }
-    float zmax = -INFINITY, denom = 0.0f;
-    if (softmax_all) {
-        for (int i = lane; i < p.E; i += 32)
-            zmax = fmaxf(zmax, load_z(p.z, p.z_fp32, t * p.ldz + i));
-        zmax = warp_max(zmax);
-        for (int i = lane; i < p.E; i += 32) {
-            const float z = load_z(p.z, p.z_fp32, t * p.ldz + i);
-            denom += z == -INFINITY ? 0.0f : expf(z - zmax);
-        }
-        denom = warp_sum(denom);
+    if constexpr (kPer > 0) {
+        softmax_grad<kPer>(p, t, lane, e, w, dw, d, sum, own);
+        return;
     }
-    auto put = [&](int i, float v) {
-        if (p.z_fp32)
-            reinterpret_cast<float *>(p.dz)[t * p.lddz + i] = v;
-        else
-            reinterpret_cast<__nv_bfloat16 *>(p.dz)[t * p.lddz + i] = __float2bfloat16_rn(v);
-    };
-    if (softmax_all) {
-        for (int i = lane; i < p.E; i += 32) {
-            const float z = load_z(p.z, p.z_fp32, t * p.ldz + i);
-            put(i, dot != dot ? dot : z == -INFINITY ? 0.0f : -expf(z - zmax) / denom * dot);
-        }
-        if (!none) {
-            const float z = load_z(p.z, p.z_fp32, t * p.ldz + e);
-            g = g - expf(z - zmax) / denom * dot;
-        }
+    const float v = nan ? __uint_as_float(0x7FC00000u) : 0.0f;   // a row without a value
+    float g = w * (d - sum);
+    if (p.sigmoid && !none)
+        g *= sigmoid(-load_z(p.z, p.z_fp32, t * p.ldz + e));
+    const int size = p.z_fp32 ? 4 : 2;
+    char *row = reinterpret_cast<char *>(p.dz) + t * p.lddz * size;
+    if (p.E * size % 16 == 0 && p.lddz * size % 16 == 0 && !nan) {
+        for (int i = lane; i < p.E * size / 16; i += 32)
+            reinterpret_cast<uint4 *>(row)[i] = make_uint4(0u, 0u, 0u, 0u);
     } else {
-        const float v = dot != dot ? dot : 0.0f;   // a row without a value
-        const int size = p.z_fp32 ? 4 : 2;
-        char *row = reinterpret_cast<char *>(p.dz) + t * p.lddz * size;
-        if (p.E * size % 16 == 0 && p.lddz * size % 16 == 0 && v == 0.0f) {
-            for (int i = lane; i < p.E * size / 16; i += 32)
-                reinterpret_cast<uint4 *>(row)[i] = make_uint4(0u, 0u, 0u, 0u);
-        } else {
-            for (int i = lane; i < p.E; i += 32)
-                put(i, v);
-        }
+        for (int i = lane; i < p.E; i += 32)
+            put_dz(p, t * p.lddz + i, v);
     }
     __syncwarp();   // the chosen ones over what their lanes' neighbours wrote
     if (!none)
-        put(e, g);
+        put_dz(p, t * p.lddz + e, nan ? v : g);
 }
 
 // ---------------------------------------------------------------- combine
@@ -969,7 +1004,11 @@ cudaError_t launch_moe_route_backward(const MoeRouteArgs &a, const float *dw, vo
     p.experts = a.experts;
     p.dz = dz;
     p.lddz = lddz;
-    return launch_dependent(route_grad_kernel, dim3((unsigned)((a.T + 7) / 8)), 256, 0, s, p);
+    const dim3 grid((unsigned)((a.T + 7) / 8));
+    if (a.sigmoid || a.renorm)
+        return launch_dependent(route_grad_kernel<0>, grid, 256, 0, s, p);
+    return a.E <= 256 ? launch_dependent(route_grad_kernel<8>, grid, 256, 0, s, p)
+                      : launch_dependent(route_grad_kernel<32>, grid, 256, 0, s, p);
 }
 
 cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t s)
