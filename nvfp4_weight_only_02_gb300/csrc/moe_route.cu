@@ -901,7 +901,8 @@ cudaError_t run_combine(const MoeCombineArgs &a, const CombineParams &p, cudaStr
     const int vec = a.N % kVec == 0 ? kVec : 1, threads = combine_threads(a.N, vec);
     // few tokens: a row's vectors over several CTAs (16 tokens of 4096: 2.6 us, 6.1 in one); many: one for all of them
     // (8192 tokens: 100 us, 119 in two)
-    const dim3 grid((unsigned)a.T, a.T < 512 ? (unsigned)((a.N + vec * threads - 1) / (vec * threads)) : 1u);
+    const int64_t pieces = std::min<int64_t>((a.N + vec * threads - 1) / (vec * threads), 65535);   // a grid's most in y
+    const dim3 grid((unsigned)a.T, a.T < 512 ? (unsigned)pieces : 1u);
     return vec > 1 ? launch_dependent(combine_kernel<TY, TO, kVec>, grid, threads, 0, s, p)
                    : launch_dependent(combine_kernel<TY, TO, 1>, grid, threads, 0, s, p);
 }
