@@ -798,6 +798,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p)
                 v[j].zero();
                 if (pos >= 0)
                     v[j].load(y + (int64_t)pos * p.N + c);
+                else if (w[j] == w[j])
+                    w[j] = 0.0f;    // an infinite weight of a slot without an expert adds nothing either
             }
 #pragma unroll
             for (int j = 0; j < kCbRows; j++)
