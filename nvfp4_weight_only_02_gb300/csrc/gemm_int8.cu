@@ -118,6 +118,15 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank)
     return v;
 }
 
+// v s w, where v s must not overflow by itself: sums are below 2^31 in magnitude, so
+// from 2^96 on the token's scale comes last.
+constexpr float kI8Wide = 0x1p96f;
+__device__ __forceinline__ float scaled(float v, float s, float w)
+{
+    const bool wide = fabsf(s) > kI8Wide;
+    return __fmul_rn(__fmul_rn(v, wide ? w : s), wide ? s : w);
+}
+
 // ---------------------------------------------------------------- few tokens
 // A CTA takes 128 weight rows and NT tokens; K is split over the CTAs of a
 // cluster when there are fewer tiles than CTA places, the shares added in rank
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kIsThreads, IsShape<NT, kTok>::kCtas)
     }
     __syncwarp();
     auto store = [&](int m, int n, float v) {
-        v = __fmul_rn(__fmul_rn(v, S::kOwn ? s_scale[m] : p.x_scale[m]), p.w_scale[n]);
+        v = scaled(v, S::kOwn ? s_scale[m] : p.x_scale[m], p.w_scale[n]);
         if (p.y_fp32)
             reinterpret_cast<float *>(p.y)[(size_t)m * p.N + n] = v;
         else
@@ -608,12 +617,19 @@ __global__ void __launch_bounds__(kItThreads, 1) __cluster_dims__(2, 1, 1)
                 if (left <= 0 || n0 >= p.N)
                     continue;
                 const float sx = lane < left ? p.x_scale[m + lane] : 0.0f;
+                // register i: row i, or row 8 (i / 4 % 4) + 2 (lane % 4) + i % 2 of output 16 (i / 16) + 8 (i / 2 % 2)
+                auto row_scale = [&](int i) {
+                    return __shfl_sync(0xffffffffu, sx, kF32 ? i : 8 * (i / 4 % 4) + 2 * (lane & 3) + i % 2);
+                };
+                auto out_scale = [&](int i) { return sw[kF32 ? 0 : 2 * (i / 16) + i / 2 % 2]; };
+                if (__any_sync(0xffffffffu, fabsf(sx) > kI8Wide)) {
 #pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    // register i: row i, or row 8 (i / 4 % 4) + 2 (lane % 4) + i % 2 of output 16 (i / 16) + 8 (i / 2 % 2)
-                    const float s = __shfl_sync(0xffffffffu, sx, kF32 ? i : 8 * (i / 4 % 4) + 2 * (lane & 3) + i % 2);
-                    v[i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[i]), s),
-                                                     sw[kF32 ? 0 : 2 * (i / 16) + i / 2 % 2]));
+                    for (int i = 0; i < 32; i++)
+                        v[i] = __float_as_uint(scaled(__uint_as_float(v[i]), row_scale(i), out_scale(i)));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        v[i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[i]), row_scale(i)), out_scale(i)));
                 }
                 store_rows<kF32>(v, sOut, 1, p.y, m, left, p.N, n0, quad, lane, !dead);
             }
