@@ -34,3 +34,29 @@ def test_scales_far_apart(nv, M, N, K, dtype, out):
     over = want.abs() > LARGEST * (1 + 2.0 ** -6)
     assert (y[over].double() == torch.sign(want[over]) * torch.inf).all()
     assert torch.equal(nv.int8_gemm(nv.int8_quantize(x), w, out_dtype=out), y)
+
+
+@pytest.mark.parametrize("M,K", [(1, 1024), (100, 1024), (1, 18944), (16, 18944), (40, 18944), (100, 18944), (200, 18944),
+                                 (600, 18944), (1, 131072), (100, 131072)])
+@pytest.mark.parametrize("how", ["random", "negative", "127 x 126", "123 x 125"])
+def test_sums_of_one_sign(nv, M, K, how):
+    """Against 64-bit integers.  An instruction adds 16 products to a running sum in 2^e .. 2^(e + 1).  Each product loses
+    what lies below 2^(e - 25), and the sum is rounded to the nearest step, 2^(e - 23): 16 / 4 + 1 / 2 steps at most.
+    (600 rows of 123 x 125, K = 18944: by this 93 instructions lose 112, 546 lose 48 and 273 lose 16, together 40992; 40896
+    were measured.)  Running sums grow evenly, random ones within 5 %, so n instructions are off by 4.5 (n + 1) / 2 steps of
+    the whole, and a sum whose K is shared out by 8 roundings more.  A stage of 128 left out would be 128 / K of it, which
+    is above that."""
+    g = torch.Generator("cuda").manual_seed(K + M)
+    N = 260
+    if how in ("random", "negative"):
+        a, w = (torch.randint(0, 128, (n, K), device="cuda", generator=g, dtype=torch.int8) for n in (M, N))
+        a = -a if how == "negative" else a
+    else:
+        a, w = (torch.full((n, K), v, device="cuda", dtype=torch.int8) for n, v in zip((M, N), map(int, how.split(" x "))))
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    y = nv.int8_gemm(nv.Int8Matrix(a, one(M)), nv.Int8Matrix(w, one(N))).double()
+    want = a.double() @ w.double().t()      # below 2^53: exact
+    n = K / 16 / (8 if K > 2 ** 16 else 1)      # three tiles of outputs: eight CTAs share K
+    steps = 0 if 127 ** 2 * K < 2 ** 24 else 1.05 * (4.5 * (n + 1) / 2 + 8)
+    assert steps * 2.0 ** -23 < 128 / K
+    assert ((y - want).abs() <= steps * 2.0 ** -23 * want.abs()).all()
