@@ -23,10 +23,11 @@ __device__ __forceinline__ float int8_round(float v, float inv, float amax)
     const float a = fabsf(v), f = a * inv;
     float r = rintf(f);
     if (fabsf(f - r) >= 0.4999f) {
-        // the nearest tie h, and the sign of 127 a - h amax from the products' exact halves
+        // the nearest tie h, and the sign of 127 a - h amax from the products' exact halves (rounded here for
+        // certain: a product that the compiler fused with th - ph would count its remainder twice)
         const float h = f >= r ? r + 0.5f : r - 0.5f;
-        const float th = 127.0f * a, tl = fmaf(127.0f, a, -th), ph = h * amax, pl = fmaf(h, amax, -ph);
-        const float d = (th - ph) + (tl - pl);
+        const float th = __fmul_rn(127.0f, a), tl = fmaf(127.0f, a, -th), ph = __fmul_rn(h, amax), pl = fmaf(h, amax, -ph);
+        const float d = __fadd_rn(__fsub_rn(th, ph), __fsub_rn(tl, pl));
         r = d > 0.0f ? h + 0.5f : d < 0.0f ? h - 0.5f : rintf(h);
     }
     return copysignf(r, v);

@@ -60,3 +60,30 @@ def test_sums_of_one_sign(nv, M, K, how):
     steps = 0 if 127 ** 2 * K < 2 ** 24 else 1.05 * (4.5 * (n + 1) / 2 + 8)
     assert steps * 2.0 ** -23 < 128 / K
     assert ((y - want).abs() <= steps * 2.0 ** -23 * want.abs()).all()
+
+
+@pytest.mark.parametrize("power", [-140, -100, -61, -59, 0, 60, 103])
+@pytest.mark.parametrize("cols", [512, 8192, 24576])
+def test_ties_of_full_mantissas(nv, cols, power):
+    """A largest magnitude of 254 c, c of 16 bits, makes ties of all odd multiples of c, whose products with 127 have more
+    bits than FP32; among them their neighbours, a step of FP32 to either side."""
+    g = torch.Generator("cuda").manual_seed(cols + power)
+    rows = 40
+    c = torch.randint(2 ** 14, 2 ** 15, (rows, 1), device="cuda", generator=g).float() * 2 + 1
+    x = (torch.randint(0, 127, (rows, cols), device="cuda", generator=g).float() * 2 + 1) * c
+    x[:, ::3] = torch.nextafter(x[:, ::3], torch.full_like(x[:, ::3], torch.inf))
+    x[:, 1::3] = torch.nextafter(x[:, 1::3], torch.zeros_like(x[:, 1::3]))
+    x *= torch.randint(0, 2, x.shape, device="cuda", generator=g).float() * 2 - 1
+    x[:, 7] = 254 * c[:, 0]
+    x[:, 16] = 0
+    x = (x.double() * 2.0 ** power).to(F32)     # exact, except below the normal numbers
+    amax = x.double().abs().amax(1, keepdim=True)
+    # 31 bits over 24: in 64 bits ties stay ties and their neighbours do not become any
+    want = torch.round(127 * x.double() / amax)
+    q = nv.int8_quantize(x)
+    assert torch.equal(q.codes.double(), want)
+    assert ((q.scales.double() - amax[:, 0] / 127).abs() <= 2.0 ** -24 * amax[:, 0] / 127 + 2.0 ** -150).all()
+    if cols <= 512:     # tokens quantised by the product itself
+        w = nv.int8_quantize(torch.randn(300, cols, device="cuda", generator=g))
+        for m in (1, 9):
+            assert torch.equal(nv.int8_linear(x[:m], w), nv.int8_gemm(nv.int8_quantize(x[:m]), w))
