@@ -61,7 +61,6 @@ MoeRows rows_of(const MoeLayout &l, const void *plan, int64_t k, bool sorted)
     m.padded = w + l.padded;
     m.blocks = (const int4 *)(w + l.blocks);
     m.max_blocks = l.max_blocks;
-    m.slots = l.slots;
     m.k = sorted ? 0 : (int)k;
     return m;
 }

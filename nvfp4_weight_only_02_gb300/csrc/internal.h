@@ -226,7 +226,6 @@ struct MoeRows {
     const int32_t *padded;    // padded row of each slot
     const int4 *blocks;       // expert, first padded row, first row, rows
     int64_t max_blocks;
-    int64_t slots;
     int k;                    // rows of x are tokens, k slots each; 0: they are the grouped rows
 };
 // Rows of x to their places (csrc/mx_quant.cu): codes padded rows x cols/2.

@@ -95,9 +95,9 @@ __device__ __forceinline__ uint32_t key_of(float v)
 // k = 8 and 21 for k = 16 whatever E is, when experts are in no order.  Those that
 // reach it are collected, a lane each, and a key's place is the number of larger
 // ones.  Where more than 32 reach it, and for more choices, each round looks at
-// all keys.  Calls for 16384 tokens, 8 of 256, 8 of 512, 16 of 1024 experts: 25, 32
-// and 63 us; 44 for the 512 and 108 for the 1024 with rounds over all keys, 27 for
-// the 256 with each lane's keys sorted first.
+// all keys.  Routing 16384 tokens, 8 of 256, 8 of 512, 16 of 1024 experts takes 22, 34
+// and 54 us; with rounds over all keys the 512 took 12 more and the 1024 45, with each
+// lane's keys sorted first the 256 2 more.
 constexpr int kRtFew = 16;
 struct Candidates {
     uint32_t key[32];
@@ -487,8 +487,7 @@ __global__ void __launch_bounds__(kRtThreads) route_kernel(const RouteParams p)
             p.plan[p.first_block + e] = s_fb[e];
         }
         if (tid < kMoeHeader)
-            p.plan[tid] = tid == kMoeRows ? rows : tid == kMoeBlocks ? s_fb[p.E] : tid == kMoeTiles ? s_ft[p.E]
-                          : tid == kMoeTileRows ? p.tile_rows : 0;
+            p.plan[tid] = tid == kMoeRows ? rows : tid == kMoeBlocks ? s_fb[p.E] : tid == kMoeTiles ? s_ft[p.E] : 0;
     }
     // lists of blocks and tiles: expert, first row of the padded and of the compact order, rows
     auto list = [&](const int *first, int size, int4 *out) {
@@ -901,8 +900,10 @@ cudaError_t run_combine(const MoeCombineArgs &a, const CombineParams &p, cudaStr
 {
     constexpr int kVec = sizeof(TY) == 4 || sizeof(TO) == 4 ? 4 : 8;
     const int vec = a.N % kVec == 0 ? kVec : 1, threads = combine_threads(a.N, vec);
-    // few tokens: a row's vectors over several CTAs (16 tokens of 4096: 2.6 us, 6.1 in one); many: one for all of them
-    // (8192 tokens: 100 us, 119 in two)
+    // few tokens: a row's vectors over several CTAs, many: one for all of them.  Rows of 4096 in bf16, us over several /
+    // in one, for 64, 256, 512, 1536, 4096 tokens: eight rows each 2.7 / 3.4, 3.9 / 4.1, 8.2 / 6.9, 19.4 / 19.2, 45.8 /
+    // 45.2; two 2.7 / 3.4, 3.4 / 4.1, 4.8 / 5.5, 12.3 / 11.7, 30.0 / 27.5; rows of 7168, eight each: 3.1 / 5.5, 6.9 / 8.2,
+    // 12.4 / 12.0, 31.9 / 32.0, 78.5 / 77.3
     const int64_t pieces = std::min<int64_t>((a.N + vec * threads - 1) / (vec * threads), 65535);   // a grid's most in y
     const dim3 grid((unsigned)a.T, a.T < 512 ? (unsigned)pieces : 1u);
     return vec > 1 ? launch_dependent(combine_kernel<TY, TO, kVec>, grid, threads, 0, s, p)
