@@ -768,18 +768,39 @@ struct CombineParams {
 };
 
 // out[t] = base[t] + sum_j w[t][j] y[position[t][j]], in FP32, j ascending.  A
-// CTA takes a token, or a part of its row, eight rows' loads on their way at once.
+// CTA takes a token, or a part of its row, eight rows' loads on their way at once:
+// bounds that leave registers for them, 5 CTAs an SM for rows in FP32 or element by
+// element, 6 for bf16 rows summed to FP32, else 4.  8192 x 8 rows of 4096 in bf16 take
+// 87.5 us (93.5 with 5, 112 without a bound, in 40 registers), 8192 x 4 in FP32 96.7 (99.4
+// with 4), 4096 x 4 in bf16 to FP32 35.3 (38.3 with 7), 1000 x 8 of 2601 25.7 (35.7 without).
 constexpr int kCbRows = 8;
 
-template <typename TY, typename TO, int kVec>
-__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p)
+template <typename TY, typename TO, int kVec, bool kWeights>
+__global__ void __launch_bounds__(256, kVec == 1 || sizeof(TY) == 4 ? 5 : sizeof(TO) == 4 ? 6 : 4)
+    combine_kernel(const CombineParams p)
 {
     const int64_t t = blockIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    const int32_t *position = p.position + t * p.k;
-    const float *weights = p.weights ? p.weights + t * p.k : nullptr;
     const TY *y = reinterpret_cast<const TY *>(p.y);
+    int pos[kCbRows];
+    float w[kCbRows];
+    // all asked for before any row is; for up to eight slots once, not again for each piece of the row
+    auto slots = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < kCbRows; j++) {
+            pos[j] = j0 + j < p.k ? p.position[t * p.k + j0 + j] : -1;
+            w[j] = !kWeights ? 1.0f : j0 + j < p.k ? p.weights[t * p.k + j0 + j] : 0.0f;
+        }
+        if (kWeights) {
+#pragma unroll
+            for (int j = 0; j < kCbRows; j++)   // without an expert nothing is added, be the weight infinite; a NaN shows
+                w[j] = pos[j] >= 0 || w[j] != w[j] ? w[j] : 0.0f;
+        }
+    };
+    const bool once = p.k <= kCbRows;
+    if (once)
+        slots(0);
     for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * kVec; c < p.N; c += gridDim.y * blockDim.x * kVec) {
         float acc[kVec];
 #pragma unroll
@@ -788,17 +809,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p)
         if (p.base)
             load_vec<TO, kVec>(reinterpret_cast<const TO *>(p.base) + t * p.N + c, acc);
         for (int j0 = 0; j0 < p.k; j0 += kCbRows) {
+            if (!once)
+                slots(j0);
             Vec<TY, kVec> v[kCbRows];
-            float w[kCbRows];
 #pragma unroll
             for (int j = 0; j < kCbRows; j++) {
-                const int pos = j0 + j < p.k ? position[j0 + j] : -1;
-                w[j] = j0 + j >= p.k ? 0.0f : weights ? weights[j0 + j] : 1.0f;
                 v[j].zero();
-                if (pos >= 0)
-                    v[j].load(y + (int64_t)pos * p.N + c);
-                else if (w[j] == w[j])
-                    w[j] = 0.0f;    // an infinite weight of a slot without an expert adds nothing either
+                if (pos[j] >= 0)
+                    v[j].load(y + (int64_t)pos[j] * p.N + c);
             }
 #pragma unroll
             for (int j = 0; j < kCbRows; j++)
@@ -895,19 +913,28 @@ int combine_threads(int64_t N, int vec)
     return (int)std::min<int64_t>(256, (items + 31) / 32 * 32);
 }
 
-template <typename TY, typename TO>
+template <typename TY, typename TO, bool kWeights>
 cudaError_t run_combine(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
 {
     constexpr int kVec = sizeof(TY) == 4 || sizeof(TO) == 4 ? 4 : 8;
     const int vec = a.N % kVec == 0 ? kVec : 1, threads = combine_threads(a.N, vec);
     // few tokens: a row's vectors over several CTAs, many: one for all of them.  Rows of 4096 in bf16, us over several /
-    // in one, for 64, 256, 512, 1536, 4096 tokens: eight rows each 2.7 / 3.4, 3.9 / 4.1, 8.2 / 6.9, 19.4 / 19.2, 45.8 /
-    // 45.2; two 2.7 / 3.4, 3.4 / 4.1, 4.8 / 5.5, 12.3 / 11.7, 30.0 / 27.5; rows of 7168, eight each: 3.1 / 5.5, 6.9 / 8.2,
-    // 12.4 / 12.0, 31.9 / 32.0, 78.5 / 77.3
+    // in one, for 64, 256, 512, 1536, 4096 tokens: eight rows each 2.7 / 3.4, 3.9 / 4.1, 8.2 / 7.5, 19.9 / 19.6, 46.8 /
+    // 45.8; two 2.7 / 2.8, 3.4 / 3.4, 4.8 / 4.8, 11.1 / 10.3, 26.7 / 23.9; rows of 7168, eight each: 2.8 / 4.1, 6.9 / 8.2,
+    // 13.0 / 12.3, 33.3 / 32.5, 81.4 / 78.4
     const int64_t pieces = std::min<int64_t>((a.N + vec * threads - 1) / (vec * threads), 65535);   // a grid's most in y
     const dim3 grid((unsigned)a.T, a.T < 512 ? (unsigned)pieces : 1u);
-    return vec > 1 ? launch_dependent(combine_kernel<TY, TO, kVec>, grid, threads, 0, s, p)
-                   : launch_dependent(combine_kernel<TY, TO, 1>, grid, threads, 0, s, p);
+    return vec > 1 ? launch_dependent(combine_kernel<TY, TO, kVec, kWeights>, grid, threads, 0, s, p)
+                   : launch_dependent(combine_kernel<TY, TO, 1, kWeights>, grid, threads, 0, s, p);
+}
+
+template <bool kWeights>
+cudaError_t run_combine_types(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
+{
+    using B = __nv_bfloat16;
+    if (a.y_fp32)
+        return a.out_fp32 ? run_combine<float, float, kWeights>(a, p, s) : run_combine<float, B, kWeights>(a, p, s);
+    return a.out_fp32 ? run_combine<B, float, kWeights>(a, p, s) : run_combine<B, B, kWeights>(a, p, s);
 }
 
 template <typename T, int kRows>
@@ -1018,9 +1045,7 @@ cudaError_t launch_moe_route_backward(const MoeRouteArgs &a, const float *dw, vo
 cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t s)
 {
     const CombineParams p = combine_params(a);
-    if (a.y_fp32)
-        return a.out_fp32 ? run_combine<float, float>(a, p, s) : run_combine<float, __nv_bfloat16>(a, p, s);
-    return a.out_fp32 ? run_combine<__nv_bfloat16, float>(a, p, s) : run_combine<__nv_bfloat16, __nv_bfloat16>(a, p, s);
+    return a.weights ? run_combine_types<true>(a, p, s) : run_combine_types<false>(a, p, s);
 }
 
 cudaError_t launch_moe_combine_backward(const MoeCombineArgs &a, cudaStream_t s)
