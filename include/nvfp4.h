@@ -523,8 +523,8 @@ size_t nvfp4_moe_plan_part(int64_t T, int64_t k, int64_t E, nvfp4_moe_part part)
 /* The k experts of every token from its logits z (T x E, bf16 or FP32, ldz
  * elements between rows), their weights, and the plan.
  *   score s = softmax(z) or sigmoid(z) (elementwise);
- *   experts: the k largest of s + bias (E floats; NULL: of z), in descending
- *     order, equal ones by index; k <= E;
+ *   experts: the k largest of s + bias in FP32 (E floats; NULL: of z), in
+ *     descending order, equal ones by index; k <= E;
  *   weights: scale * s_j, or with renormalise != 0 scale * s_j / (sum of the
  *     k scores taken).  The bias chooses and is not part of the weight.
  * An expert whose logit is -inf (or whose s + bias is -inf or NaN) is not taken: a slot that finds none

@@ -24,8 +24,9 @@
 // weights' bytes are 10; the rest is the launch, the first stage's way and the join
 // of two shares.  100 tokens through 3584 x 18944: 17 us and the quantiser's 5 (bytes
 // 10, MMAs 9; 37 us with one ring for codes, tokens and converted weights).  8192
-// tokens through 18944 x 3584: about 600 us beside the quantiser, 1.85 PFLOP/s, 96 % of
-// the library's bf16 product in a burst and 107 % of what it sustains (power).
+// tokens through 18944 x 3584: 622 to 660 us with the quantiser from GPU to GPU, 1.69 to
+// 1.79 PFLOP/s, 87 to 93 % of the library's bf16 product in a burst and 98 to 104 % of what
+// it sustains (power).
 #include <algorithm>
 #include <type_traits>
 

@@ -17,8 +17,9 @@
 // What bounds it.  16384 tokens, 8 of 256 experts: 22 us, of which choosing 16
 // (instructions) and placing 6 (the second kernel waits for each CTA's counts,
 // 152 x 256 of them read by every CTA; 9 when a thread asked for few of them at a
-// time and for its slots afterwards); gradient 5 (bytes).  8192 tokens, 8 rows each
-// of 4096 in bf16: sum 94 us (95 % of the copy rate), its gradients 176 (96 %).
+// time and for its slots afterwards); gradient 4.5 (issue 55 %, latency; its 17 MB
+// stay in L2), 10.3 with scores over all experts (issue 76 %).  8192 tokens, 8 rows
+// each of 4096 in bf16: sum 87.5 us, its gradients 169 (99 % of the copy rate or more).
 #include <algorithm>
 
 #include "common.cuh"
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(256, kVec == 1 || sizeof(TY) == 4 ? 5 : sizeof
 // dy[position[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[position[t][j]]>: a CTA a token, dout read once for
 // kRows slots, whose rows of y are on their way while the rows of dy are written.  Registers for that many loads and
 // CTAs for the rest: bounds of 3 (bf16, eight rows), 5 (four), 4 and 6 (FP32).  8192 tokens of 4096 in bf16, eight
-// rows each: 170 us (187 with loads as they are used, in 40 registers), four rows 92 (105); bounds of 2 and 4: 177, 183.
+// rows each: 169 us (187 with loads as they are used, in 40 registers), four rows 92 (105); bounds of 2 and 4: 177, 183.
 template <typename T, int kVec, int kRows>
 __global__ void __launch_bounds__(256, kVec == 8 ? (kRows == 8 ? 3 : 5)
                                              : kVec == 4 ? (kRows == 8 ? 4 : 6) : 1) combine_grad_kernel(const CombineParams p)
