@@ -917,6 +917,7 @@ int combine_threads(int64_t N, int vec)
 template <typename TY, typename TO, bool kWeights>
 cudaError_t run_combine(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
 {
+    // rows that are no multiple of the vector go element by element: 8192 x 8 rows of 2601 in bf16 149 us, of 2600 55
     constexpr int kVec = sizeof(TY) == 4 || sizeof(TO) == 4 ? 4 : 8;
     const int vec = a.N % kVec == 0 ? kVec : 1, threads = combine_threads(a.N, vec);
     // few tokens: a row's vectors over several CTAs, many: one for all of them.  Rows of 4096 in bf16, us over several /
@@ -941,6 +942,8 @@ cudaError_t run_combine_types(const MoeCombineArgs &a, const CombineParams &p, c
 template <typename T, int kRows>
 cudaError_t run_combine_grad(const MoeCombineArgs &a, const CombineParams &p, cudaStream_t s)
 {
+    // element by element as above: 313 us instead of 126.  A CTA a token however few there are: 16 tokens, eight rows of
+    // 4096 each, 4.1 us.
     constexpr int kVec = 16 / sizeof(T);
     const dim3 grid((unsigned)a.T);
     return a.N % kVec == 0
